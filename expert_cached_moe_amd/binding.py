@@ -22,6 +22,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 MOE_OK, MOE_EINVAL, MOE_ESHAPE, MOE_ECAPACITY, MOE_EHIP, MOE_EUNSUPPORTED, MOE_ESTATE = 0, -1, -2, -3, -4, -5, -6
 MOE_W_F32, MOE_W_BF16, MOE_W_MXFP4 = 0, 1, 2
+MOE_A_F32, MOE_A_BF16, MOE_A_I8 = 0, 1, 2
 MOE_Q_NEAREST, MOE_Q_ARGMIN = 0, 1
 
 c_i32p = ctypes.POINTER(ctypes.c_int32)
@@ -37,6 +38,9 @@ EXPORTS = [
     "moe_expert_ffn_merge",
     "moe_prefill_stream", "moe_router_logits", "moe_lru_resize", "moe_move_slots",
     "moe_expert_ffn_merge_noalloc", "moe_noalloc_scratch_bytes",
+    "moe_i8_workspace_bytes", "moe_i8_quantize", "moe_i8_matmul", "moe_dense_workspace_bytes",
+    "moe_dense_save_bytes", "moe_dense_ffn", "moe_dense_ffn_backward", "moe_i8_blob_bytes", "moe_i8_pack",
+    "moe_i8_ffn",
 ]
 
 
@@ -101,6 +105,18 @@ _sig = {
     "moe_expert_ffn_merge_noalloc": (ctypes.c_int, [vp, vp, ctypes.c_int32, vp, vp, vp, vp, vp, vp, ctypes.c_int32,
                                                     vp, ctypes.c_int32, vp, vp, vp]),
     "moe_noalloc_scratch_bytes": (ctypes.c_int64, []),
+    "moe_i8_workspace_bytes": (ctypes.c_int64, [ctypes.c_int32, ctypes.c_int32]),
+    "moe_i8_quantize": (ctypes.c_int, [vp, vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, vp, vp,
+                                       vp]),
+    "moe_i8_matmul": (ctypes.c_int, [vp, vp, ctypes.c_int32, ctypes.c_int64, vp, ctypes.c_int32, vp, vp, ctypes.c_int32,
+                                     ctypes.c_int32, vp, ctypes.c_int32, ctypes.c_int64, vp, vp]),
+    "moe_dense_workspace_bytes": (ctypes.c_int64, [_P(moe_config), ctypes.c_int32]),
+    "moe_dense_save_bytes": (ctypes.c_int64, [_P(moe_config), ctypes.c_int32]),
+    "moe_dense_ffn": (ctypes.c_int, [vp, vp, ctypes.c_int32, vp, vp, vp, vp, vp]),
+    "moe_dense_ffn_backward": (ctypes.c_int, [vp, vp, vp, ctypes.c_int32, vp, vp, vp, vp, vp, vp]),
+    "moe_i8_blob_bytes": (ctypes.c_int64, [_P(moe_config)]),
+    "moe_i8_pack": (ctypes.c_int, [vp, vp, vp, vp]),
+    "moe_i8_ffn": (ctypes.c_int, [vp, vp, ctypes.c_int32, vp, vp, vp, vp]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -354,6 +370,54 @@ def moe_expert_ffn_merge_noalloc(ctx, d_x, T, h_topk_ids, d_topk_ids, d_topk_w, 
 
 def moe_noalloc_scratch_bytes() -> int:
     return int(_lib.moe_noalloc_scratch_bytes())
+
+
+def _size(v, name) -> int:
+    if v < 0:
+        raise MoeError(int(v), name)
+    return int(v)
+
+
+def moe_i8_workspace_bytes(max_T: int, K: int) -> int:
+    return _size(_lib.moe_i8_workspace_bytes(max_T, K), "moe_i8_workspace_bytes")
+
+
+def moe_i8_quantize(ctx, d_x, x_type, ld_x, rows, cols, d_q, d_scale, s=None) -> None:
+    _check(ctx, _lib.moe_i8_quantize(ctx, _ptr(d_x), x_type, ld_x, rows, cols, _ptr(d_q), _ptr(d_scale), _stream(s)))
+
+
+def moe_i8_matmul(ctx, d_x, x_type, ld_x, d_x_scale, T, d_w, d_w_scale, N, K, d_y, y_type, ld_y, d_ws, s=None) -> None:
+    _check(ctx, _lib.moe_i8_matmul(ctx, _ptr(d_x), x_type, ld_x, _ptr(d_x_scale), T, _ptr(d_w), _ptr(d_w_scale), N, K,
+                                   _ptr(d_y), y_type, ld_y, _ptr(d_ws), _stream(s)))
+
+
+def moe_dense_workspace_bytes(cfg: moe_config, max_T: int) -> int:
+    return _size(_lib.moe_dense_workspace_bytes(ctypes.byref(cfg), max_T), "moe_dense_workspace_bytes")
+
+
+def moe_dense_save_bytes(cfg: moe_config, T: int) -> int:
+    return _size(_lib.moe_dense_save_bytes(ctypes.byref(cfg), T), "moe_dense_save_bytes")
+
+
+def moe_dense_ffn(ctx, d_x, T, d_blob, d_save, d_y, d_ws, s=None) -> None:
+    _check(ctx, _lib.moe_dense_ffn(ctx, _ptr(d_x), T, _ptr(d_blob), _ptr(d_save), _ptr(d_y), _ptr(d_ws), _stream(s)))
+
+
+def moe_dense_ffn_backward(ctx, d_dy, d_x, T, d_blob, d_save, d_dx, d_dblob, d_ws, s=None) -> None:
+    _check(ctx, _lib.moe_dense_ffn_backward(ctx, _ptr(d_dy), _ptr(d_x), T, _ptr(d_blob), _ptr(d_save), _ptr(d_dx),
+                                            _ptr(d_dblob), _ptr(d_ws), _stream(s)))
+
+
+def moe_i8_blob_bytes(cfg: moe_config) -> int:
+    return _size(_lib.moe_i8_blob_bytes(ctypes.byref(cfg)), "moe_i8_blob_bytes")
+
+
+def moe_i8_pack(ctx, d_blob, d_blob8, s=None) -> None:
+    _check(ctx, _lib.moe_i8_pack(ctx, _ptr(d_blob), _ptr(d_blob8), _stream(s)))
+
+
+def moe_i8_ffn(ctx, d_x, T, d_blob8, d_y, d_ws, s=None) -> None:
+    _check(ctx, _lib.moe_i8_ffn(ctx, _ptr(d_x), T, _ptr(d_blob8), _ptr(d_y), _ptr(d_ws), _stream(s)))
 
 
 def moe_prefill_stream(ctx, d_layer_bufs, n_buffers, d_logits, d_x, T, d_shared, d_topk_ids, d_topk_w, d_counts,

@@ -1,0 +1,53 @@
+// Launchers of the dense operators (moe_i8_*, moe_dense_*), and the argument block of their
+// product kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "internal.h"
+
+namespace moe {
+namespace dense {
+
+constexpr int kMaxKI8 = 131056;       // 128 * 128 * K stays below 2^31
+
+// Element type of the operands of a product.
+enum { kF32 = 0, kBF16 = 1, kI8 = 2 };
+
+// Which operands of C[m][n] = sum_k A(m, k) B(n, k) have k as their contiguous dimension: NT
+// both (A [M][K], B [N][K]); NN only A (B [K][N]); TN neither (A [K][M], B [K][N]).
+enum { kNT = 0, kNN = 1, kTN = 2 };
+
+// What becomes of the sums.
+enum {
+    kStore = 0,   // out[m][n] = acc, rounded to the operands' type
+    kScale = 1,   // out[m][n] = acc * row_scale[m] * col_scale[n] (integer products)
+    kGate = 2,    // columns are interleaved gate / up: out[m][i] = silu(g) * u; gu[m][n] = acc if kept
+    kGate8 = 3,   // the same from integer sums and scales, out in fp32
+    kDGate = 4,   // acc = dh[m][i]: out[m][..] = dg, du interleaved, from gu (pre-activations)
+};
+
+struct Product {
+    const void* a;
+    const void* b;
+    int64_t lda, ldb;           // elements between rows of A and B
+    int64_t M;
+    int32_t N, K;
+    void* out;
+    int64_t ldo;                // elements between rows of out
+    int32_t out_f32;            // kScale: out is fp32 (else bf16)
+    const float* row_scale;     // kScale, kGate8
+    const float* col_scale;
+    void* gu;                   // kGate: written when not null; kDGate: read; rows of 2 I elements
+};
+
+// One product on stream s: type kF32 / kBF16 / kI8, layout kNT / kNN / kTN, epilogue as above.
+hipError_t launch_product(int type, int layout, int epi, const Product& p, hipStream_t s);
+// rows of cols numbers to codes and scales; x_type MOE_A_F32 / MOE_A_BF16
+hipError_t launch_quantize(const void* x, int x_type, int64_t ld_x, int64_t rows, int32_t cols, int8_t* q,
+                           float* scale, hipStream_t s);
+// n16 16-byte units of zeros
+hipError_t launch_zero(void* p, int64_t n16, hipStream_t s);
+
+}  // namespace dense
+}  // namespace moe

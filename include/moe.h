@@ -57,6 +57,11 @@ extern "C" {
 #define MOE_W_BF16 1
 #define MOE_W_MXFP4 2
 
+/* activation element formats of the dense operators (moe_i8_*) */
+#define MOE_A_F32 0
+#define MOE_A_BF16 1
+#define MOE_A_I8 2   /* 8-bit integer codes with one fp32 scale per row */
+
 /* integer readings of q* ~= m*B_P/B_H ([B] "The q* Policy") */
 #define MOE_Q_NEAREST 0  /* floor((m*B_P)/B_H + 1/2) in IEEE double, clamped to [0, m] */
 #define MOE_Q_ARGMIN 1   /* smallest q minimising max(q/B_P, (m-q)/(B_H-B_P)) */
@@ -320,6 +325,84 @@ int moe_expert_ffn_merge_noalloc(moe_ctx* ctx, const void* d_x, int32_t T, const
                                  int32_t with_shared, const float* d_y_host, void* d_out, hipStream_t s);
 /* Bytes of the scratch array moe_expert_ffn_merge_noalloc uses on each GPU. */
 int64_t moe_noalloc_scratch_bytes(void);
+
+/* ---------------------------------------------------------------- 8-bit integer products */
+/* The dense parts of a model around its MoE layers (projections, the output head, dense
+ * feed-forward blocks) with weights held in 8-bit integers: one fp32 scale per output
+ * channel (row of W) and one per token (row of x).  A row v of n numbers is held as
+ *   scale = fp32(max|v| / 127),   code[i] = v[i] / scale rounded to the nearest integer,
+ *           ties to the even one (the exact quotient, so codes lie in -127..127).
+ * A row whose scale would be below 2^-126 (all zeros, or max|v| under about 2^-119) has scale
+ * 0 and codes 0; a row that holds an infinity or a NaN has scale NaN and codes 0, so every
+ * product with it is NaN.
+ *
+ * Scratch bytes of moe_i8_matmul for up to max_T tokens of K numbers, or a negative status. */
+int64_t moe_i8_workspace_bytes(int32_t max_T, int32_t K);
+/* Quantise `rows` rows of `cols` numbers (async on s).  d_x: MOE_A_F32 or MOE_A_BF16, rows
+ * ld_x >= cols elements apart, any alignment of the element; d_q [rows][cols] codes (rows back
+ * to back, 16-byte aligned, cols a multiple of 16); d_scale [rows].  rows == 0 is a no-op.
+ * Errors: MOE_EINVAL (null, type, ld_x < cols, alignment), MOE_ESHAPE (cols). */
+int moe_i8_quantize(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, int32_t rows, int32_t cols,
+                    int8_t* d_q, float* d_scale, hipStream_t s);
+/* y[t][n] = x_scale[t] * w_scale[n] * sum_k x_code[t][k] * w_code[n][k] (async on s), the sum
+ * exact in 32-bit integers, the result rounded once to y_type.
+ *   d_x: MOE_A_I8: codes [T][K] back to back (ld_x = K) with d_x_scale [T]; MOE_A_F32 or
+ *     MOE_A_BF16: numbers, rows ld_x >= K elements apart, quantised on the way exactly as
+ *     moe_i8_quantize does (d_x_scale must be NULL; callers with several products of one x
+ *     quantise once and pass the codes);
+ *   d_w [N][K] codes and d_w_scale [N] (moe_i8_quantize of W's rows); any 8-bit codes, -128
+ *     included, are taken;
+ *   d_y [T][N], rows ld_y >= N elements apart, MOE_A_F32 or MOE_A_BF16; bytes between the rows
+ *     are not written;
+ *   d_ws: moe_i8_workspace_bytes(max_T >= T, K), 256-byte aligned.
+ * K is a multiple of 16 up to 131056 (so no sum leaves 32 bits), N >= 1, code arrays 16-byte
+ * aligned.  T == 0 is a no-op.  Errors: MOE_EINVAL, MOE_ESHAPE. */
+int moe_i8_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, const float* d_x_scale, int32_t T,
+                  const int8_t* d_w, const float* d_w_scale, int32_t N, int32_t K, void* d_y, int32_t y_type,
+                  int64_t ld_y, void* d_ws, hipStream_t s);
+
+/* ---------------------------------------------------------------- dense gated block */
+/* One gated feed-forward block over all tokens, y = Wd (silu(Wg x) * (Wu x)), on a blob of
+ * moe_pack_expert's layout (the shared expert, a dense feed-forward layer: a context whose
+ * config has that width).  Contexts with fp32 or bf16 weights; H = cfg.hidden, I = cfg.inter,
+ * activations in the weights' type.  Blob, x, y, dy, dx, save and workspace 16-byte aligned.
+ *
+ * Scratch bytes for up to max_T tokens of any moe_dense_* or moe_i8_ffn call. */
+int64_t moe_dense_workspace_bytes(const moe_config* cfg, int32_t max_T);
+/* Bytes a training step keeps from the forward to the backward pass for T tokens: the
+ * pre-activations Wg x and Wu x ([T][2I], interleaved like the blob's rows) and
+ * h = silu(Wg x) * (Wu x) ([T][I]), each rounded once to the activation type. */
+int64_t moe_dense_save_bytes(const moe_config* cfg, int32_t T);
+/* Forward pass of T tokens (async on s): d_x [T][H], d_blob, d_y [T][H].  d_save
+ * (moe_dense_save_bytes of the same T) is written when not NULL; y does not depend on it.
+ * Products accumulate in fp32 and h is rounded once to the activation type before the down
+ * projection, as in moe_expert_ffn.  T == 0 is a no-op.  Errors: MOE_EINVAL (null, alignment),
+ * MOE_EUNSUPPORTED (MXFP4 weights). */
+int moe_dense_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob, void* d_save, void* d_y, void* d_ws,
+                  hipStream_t s);
+/* Backward pass (async on s): from d_dy = dL/dy [T][H], the same x and blob as the forward
+ * call and the d_save it wrote, d_dx = dL/dx [T][H] and d_dblob = the gradient of the weights
+ * in the blob's layout and type (both overwritten; the blob's padding bytes are not written):
+ *   dh = dy Wd;  dg = dh * u * silu'(g),  du = dh * silu(g);
+ *   dx = dg Wg + du Wu;  dWg = dg^T x,  dWu = du^T x,  dWd = dy^T h.
+ * Products accumulate in fp32; dg and du are rounded once to the activation type before they
+ * are multiplied.  d_dx may be NULL (a first layer), d_dblob may be NULL (frozen weights).
+ * T == 0 writes zeros to d_dblob.  Results do not depend on the run.  Errors as above. */
+int moe_dense_ffn_backward(moe_ctx* ctx, const void* d_dy, const void* d_x, int32_t T, const void* d_blob,
+                           const void* d_save, void* d_dx, void* d_dblob, void* d_ws, hipStream_t s);
+
+/* The same block served from 8-bit weights.  Contexts with bf16 weights.
+ * Bytes of the 8-bit blob: codes Wgu [2I][H] (the blob's interleaved rows), codes Wd [H][I],
+ * scales of the Wgu rows [2I], scales of the Wd rows [H], each part 256-byte aligned. */
+int64_t moe_i8_blob_bytes(const moe_config* cfg);
+/* Quantise a device blob's rows (async on s): d_blob (moe_expert_bytes) to d_blob8
+ * (moe_i8_blob_bytes), both 256-byte aligned. */
+int moe_i8_pack(moe_ctx* ctx, const void* d_blob, void* d_blob8, hipStream_t s);
+/* y = block(x) with both products in integers (async on s): x [T][H] bf16 is quantised per
+ * token, gate and up are fp32 numbers scale * scale * (integer sum), h = silu(gate) * up in
+ * fp32 is quantised per token, and the down product's result is rounded once to bf16 y [T][H].
+ * Alignments and d_ws as moe_dense_ffn.  T == 0 is a no-op. */
+int moe_i8_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob8, void* d_y, void* d_ws, hipStream_t s);
 
 /* ---------------------------------------------------------------- layer streaming (prefill) */
 /* One T-token prefill chunk through cfg.n_layers MoE layers whose expert pools
