@@ -57,8 +57,12 @@ Blob8 blob8_layout(const moe_config& c) {
     return b;
 }
 
+constexpr int kMaxWidth = 1 << 20;    // H and I: row offsets inside a tile stay below 2 GiB
+
 int check_block(moe_ctx* ctx, int32_t T, bool i8) {
     if (T < 0) return fail(ctx, MOE_EINVAL, "T < 0");
+    if (ctx->cfg.hidden > kMaxWidth || ctx->cfg.inter > kMaxWidth)
+        return fail(ctx, MOE_ESHAPE, "the dense block takes H and I up to 2^20");
     if (i8 && ctx->cfg.w_dtype != MOE_W_BF16)
         return fail(ctx, MOE_EUNSUPPORTED, "the 8-bit block is made from and for bf16 contexts");
     if (!i8 && ctx->cfg.w_dtype == MOE_W_MXFP4)
@@ -135,6 +139,7 @@ int moe_i8_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, c
     p.out = d_y;
     p.ldo = ld_y;
     p.out_f32 = y_type == MOE_A_F32;
+    p.vec_out = aligned(d_y, p.out_f32 ? 16 : 8) && ld_y % 4 == 0;
     p.col_scale = d_w_scale;
     hipError_t e = launch_product(kI8, kNT, kScale, p, s);
     return e == hipSuccess ? MOE_OK : hip_fail(ctx, e, "moe_i8_matmul launch");
@@ -332,6 +337,7 @@ int moe_i8_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob8, vo
     p.out = d_y;
     p.ldo = c.hidden;
     p.out_f32 = 0;
+    p.vec_out = 1;
     p.row_scale = hs;
     p.col_scale = reinterpret_cast<const float*>(blob + b.d_scale);
     if (e == hipSuccess) e = launch_product(kI8, kNT, kScale, p, s);

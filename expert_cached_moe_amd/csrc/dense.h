@@ -36,6 +36,7 @@ struct Product {
     void* out;
     int64_t ldo;                // elements between rows of out
     int32_t out_f32;            // kScale: out is fp32 (else bf16)
+    int32_t vec_out;            // kScale: rows of out are aligned for stores of four values
     const float* row_scale;     // kScale, kGate8
     const float* col_scale;
     void* gu;                   // kGate: written when not null; kDGate: read; rows of 2 I elements
@@ -43,6 +44,8 @@ struct Product {
 
 // One product on stream s: type kF32 / kBF16 / kI8, layout kNT / kNN / kTN, epilogue as above.
 hipError_t launch_product(int type, int layout, int epi, const Product& p, hipStream_t s);
+// the same on the matrix cores: bf16 and 8-bit integers, row strides below 8 MiB
+hipError_t launch_mma(int type, int layout, int epi, const Product& p, hipStream_t s);
 // rows of cols numbers to codes and scales; x_type MOE_A_F32 / MOE_A_BF16
 hipError_t launch_quantize(const void* x, int x_type, int64_t ld_x, int64_t rows, int32_t cols, int8_t* q,
                            float* scale, hipStream_t s);

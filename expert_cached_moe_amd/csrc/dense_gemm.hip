@@ -125,21 +125,12 @@ hipError_t launch_simple(const Product& p, hipStream_t s) {
 
 hipError_t launch_product(int type, int layout, int epi, const Product& p, hipStream_t s) {
     if (p.M <= 0 || p.N <= 0) return hipSuccess;
-    if (type == kI8) {
-        if (layout == kNT && epi == kScale) return launch_simple<kI8, kNT, kScale>(p, s);
-        if (layout == kNT && epi == kGate8) return launch_simple<kI8, kNT, kGate8>(p, s);
-        return hipErrorInvalidValue;
-    }
-    if (layout == kNT && epi == kStore)
-        return type == kF32 ? launch_simple<kF32, kNT, kStore>(p, s) : launch_simple<kBF16, kNT, kStore>(p, s);
-    if (layout == kNT && epi == kGate)
-        return type == kF32 ? launch_simple<kF32, kNT, kGate>(p, s) : launch_simple<kBF16, kNT, kGate>(p, s);
-    if (layout == kNN && epi == kStore)
-        return type == kF32 ? launch_simple<kF32, kNN, kStore>(p, s) : launch_simple<kBF16, kNN, kStore>(p, s);
-    if (layout == kNN && epi == kDGate)
-        return type == kF32 ? launch_simple<kF32, kNN, kDGate>(p, s) : launch_simple<kBF16, kNN, kDGate>(p, s);
-    if (layout == kTN && epi == kStore)
-        return type == kF32 ? launch_simple<kF32, kTN, kStore>(p, s) : launch_simple<kBF16, kTN, kStore>(p, s);
+    if (type != kF32) return launch_mma(type, layout, epi, p, s);
+    if (layout == kNT && epi == kStore) return launch_simple<kF32, kNT, kStore>(p, s);
+    if (layout == kNT && epi == kGate) return launch_simple<kF32, kNT, kGate>(p, s);
+    if (layout == kNN && epi == kStore) return launch_simple<kF32, kNN, kStore>(p, s);
+    if (layout == kNN && epi == kDGate) return launch_simple<kF32, kNN, kDGate>(p, s);
+    if (layout == kTN && epi == kStore) return launch_simple<kF32, kTN, kStore>(p, s);
     return hipErrorInvalidValue;
 }
 

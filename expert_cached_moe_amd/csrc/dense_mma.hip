@@ -1,0 +1,349 @@
+// Products of the dense operators on the matrix cores: bf16 and 8-bit integers.
+//
+// C[m][n] = sum_k A(m, k) B(n, k) in tiles of BM x BN.  One K slice is 128 bytes of K (64 bf16
+// or 128 codes), so a row segment of an operand that is contiguous along K is one cache line and
+// both types move the same bytes per slice; the 16x16 matrix instructions take 16 bytes a lane
+// from each operand (32 bf16 or 64 codes of K) in the same time.  Slices are loaded straight
+// into two LDS stages by buffer loads; the one barrier of a slice stands before its last quarter,
+// so the loads of a slice have a whole slice's time to land and the matrix instructions of the
+// last quarter cover the first reads of the next slice.
+//
+// Operands contiguous along K lie in LDS as rows of 128 bytes, 16-byte chunk c of row r at slot
+// c ^ ((r >> 1) & 7): two rows share a 256-byte window of the banks, so the 16 rows of a
+// fragment read fall on different banks.  Operands contiguous along the other dimension (the
+// gradients' products) lie as rows of one k; their fragments are read with the transposing LDS
+// read, 4 k of 16 columns a group of 16 lanes, and the 32-byte units of row k are permuted by
+// bits 0, 1 and 3 of k, so the 8 rows that 32 lanes read fall on different banks.
+//
+// The weights' operand goes first into the instruction, so a lane ends with four consecutive
+// columns of one row: gate and up sums of an inner index are in one lane, and results leave as
+// 8 or 16 bytes a lane.
+//
+// Rows past M or N are read from the last row (their sums are dropped), and the part of the last
+// slice past K is zeros: a buffer load whose offset is out of range writes zeros to LDS.
+//
+// Workgroup b serves XCD b % 8; each XCD takes a contiguous run of the tile order, which walks
+// groups of 8 row tiles, so the tiles in flight on an XCD share operands in its L2.
+#include <hip/hip_runtime.h>
+
+#include "dense_common.h"
+#include "dense_epilogue.h"
+
+namespace moe {
+namespace dense {
+namespace {
+
+using dev::kWave;
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int kXcds = 8, kGroupM = 8;
+constexpr int kSlice = 128;                       // bytes of K in a slice
+constexpr uint32_t kOutside = 0xFFFFFFF0u;        // a buffer offset past every range
+constexpr uint32_t kRange = 0x80000000u;          // range of the buffer descriptors: 2 GiB
+
+template <int TYPE> struct Frag;
+template <> struct Frag<kBF16> {
+    typedef bf16x8 V;
+    typedef dev::f32x4 Acc;
+    static constexpr int ES = 2;
+};
+template <> struct Frag<kI8> {
+    typedef i32x4 V;
+    typedef i32x4 Acc;
+    static constexpr int ES = 1;
+};
+__device__ __forceinline__ dev::f32x4 mma(const bf16x8& a, const bf16x8& b, const dev::f32x4& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ i32x4 mma(const i32x4& a, const i32x4& b, const i32x4& c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+
+// permutation of the 32-byte units of row k of an operand that is not contiguous along K
+__device__ __forceinline__ int unit_swz(int k) { return (k & 3) | ((k >> 1) & 4); }
+
+// One operand's tile: X rows (tokens or weights) by one slice of K, X * 128 bytes in LDS.
+// KC: contiguous along K.
+template <int X, bool KC, int ES, int NW>
+struct Side {
+    static constexpr int Q = X * kSlice / 1024 / NW;      // 1 KiB loads of a wave per slice
+    static constexpr int KS = kSlice / ES;                // k in a slice
+    static_assert(Q * NW * 1024 == X * kSlice, "loads split over the waves");
+    static_assert(KC || (ES == 2 && X >= 128), "transposing reads: 16-bit elements, 8 units a row");
+
+    const uint8_t* base;     // (uniform) first row / column of the tile at the next slice to load
+    int64_t step;            // bytes from slice to slice
+    uint32_t off[Q];         // this lane's offsets from base
+
+    // x0: the tile's first row, n_rows rows in all; ld elements between rows (KC) or between k
+    __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t x0, int64_t n_rows) {
+        const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+        const uint32_t ldb = uint32_t(ld) * ES;
+        base = static_cast<const uint8_t*>(p) + (KC ? x0 * ld * ES : x0 * ES);
+        step = KC ? kSlice : int64_t(KS) * ld * ES;
+        const int left = int(n_rows - x0 < X ? n_rows - x0 : X);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int i = wave + NW * q;                  // 1 KiB block of the tile
+            if constexpr (KC) {
+                const int r = i * 8 + lane / 8, c = lane % 8 ^ ((r >> 1) & 7);
+                off[q] = uint32_t(r < left ? r : left - 1) * ldb + c * 16;
+            } else {
+                constexpr int CPR = X * ES / 16;          // 16-byte chunks of a k row
+                const int k = (i * 64 + lane) / CPR, c = (i * 64 + lane) % CPR;
+                const int col = (c ^ (unit_swz(k) << 1)) * (16 / ES);
+                off[q] = uint32_t(k) * ldb + (col < left ? col : 0) * ES;
+            }
+        }
+    }
+    // offset of load q when only k_left k of the slice exist
+    __device__ __forceinline__ uint32_t tail(int q, int k_left) const {
+        const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, i = wave + NW * q;
+        bool in;
+        if constexpr (KC) {
+            const int r = i * 8 + lane / 8, c = lane % 8 ^ ((r >> 1) & 7);
+            in = c * (16 / ES) < k_left;
+        } else {
+            in = (i * 64 + lane) / (X * ES / 16) < k_left;
+        }
+        return in ? off[q] : kOutside;
+    }
+    __device__ __forceinline__ void issue(uint8_t* lds, int k_left) {
+        const int wave = threadIdx.x / kWave;
+        const __amdgpu_buffer_rsrc_t r =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, kRange, 0x00027000);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const uint32_t o = k_left >= KS ? off[q] : tail(q, k_left);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + (wave + NW * q) * 1024), 16, o, 0, 0, 0);
+        }
+        base += step;
+    }
+};
+
+// This lane's fragment reads of one operand: rows x0 + 16 i + lane % 16 of the tile.
+template <int X, bool KC>
+struct Reader {
+    uint32_t at[2];          // KC: byte offset for half-slice 0 and 1
+    int unit, f;             // not KC: first 32-byte unit, its permutation
+    __device__ __forceinline__ void init(int x0) {
+        const int lane = threadIdx.x % kWave, j = lane % 16, g = lane / 16;
+        if constexpr (KC) {
+            const int sw = (j >> 1) & 7;
+            at[0] = (x0 + j) * kSlice + ((g ^ sw) << 4);
+            at[1] = at[0] ^ 64;
+        } else {
+            const int k = 8 * g + j / 4;
+            at[0] = k * (X * 2) + (j % 4) * 8;
+            at[1] = at[0] + 32 * (X * 2);
+            unit = x0 / 16;
+            f = unit_swz(k);
+        }
+    }
+    template <class V>
+    __device__ __forceinline__ V read(const uint8_t* lds, int half, int i) const {
+        if constexpr (KC) {
+            return *reinterpret_cast<const V*>(lds + at[half] + i * 16 * kSlice);
+        } else {
+            const uint8_t* p = lds + at[half] + (((unit + i) ^ f) << 5);
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * X * 2));
+            typedef __attribute__((ext_vector_type(8))) short s16x8;
+            return __builtin_bit_cast(V, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+    }
+};
+
+// Barrier that hands loaded slices over: every wave waits for its own loads first.
+__device__ __forceinline__ void barrier_loads() {
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+}
+
+template <int BM_, int BN_, int WM_, int WN_>
+struct Tile {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NW = WM * WN, kThreads = NW * kWave;
+    static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16, FH = FM / 2;
+    static constexpr int STAGE = (BM + BN) * kSlice, kLdsBytes = 2 * STAGE;
+    static constexpr int kWavesPerSimd = NW * (160 * 1024 / kLdsBytes) / 4 < 2 ? 1 : 2;
+    static_assert(FH * 32 == TM && FN * 16 == TN && FN % 2 == 0, "fragments");
+};
+
+template <int TYPE, int LAYOUT, int EPI, class C>
+__global__ void __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::kWavesPerSimd)))
+k_mma(const Product p, int m_tiles, int n_tiles) {
+    typedef typename Frag<TYPE>::V V;
+    typedef typename Frag<TYPE>::Acc Acc;
+    constexpr int ES = Frag<TYPE>::ES, KS = kSlice / ES;
+    constexpr bool AKC = LAYOUT != kTN, BKC = LAYOUT == kNT;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    // tile of this workgroup
+    const int total = m_tiles * n_tiles, per = (total + kXcds - 1) / kXcds;
+    const int lid = int(blockIdx.x % kXcds) * per + int(blockIdx.x / kXcds);
+    if (int(blockIdx.x / kXcds) >= per || lid >= total) return;
+    const int grp = lid / (kGroupM * n_tiles), in = lid % (kGroupM * n_tiles);
+    const int gm = min(kGroupM, m_tiles - grp * kGroupM);
+    const int64_t m0 = int64_t(grp * kGroupM + in % gm) * C::BM;
+    const int n0 = in / gm * C::BN;
+
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    Side<C::BM, AKC, ES, C::NW> sa;
+    Side<C::BN, BKC, ES, C::NW> sb;
+    sa.init(p.a, p.lda, m0, p.M);
+    sb.init(p.b, p.ldb, n0, p.N);
+    Reader<C::BM, AKC> ra;
+    Reader<C::BN, BKC> rb;
+    ra.init(wm * C::TM);
+    rb.init(wn * C::TN);
+
+    Acc acc[C::FM][C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) acc[i][j] = Acc{0, 0, 0, 0};
+    V fa[2][C::FH], fb[2][C::FN];
+
+    // quarter s of a slice: half-slice s / 2 of K, half s % 2 of the wave's rows
+    auto read = [&](const uint8_t* st, auto s_) {
+        constexpr int s = decltype(s_)::value;
+#pragma unroll
+        for (int i = 0; i < C::FH; ++i) fa[s % 2][i] = ra.template read<V>(st, s / 2, (s % 2) * C::FH + i);
+        if constexpr (s % 2 == 0) {
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) fb[s / 2][j] = rb.template read<V>(st + C::BM * kSlice, s / 2, j);
+        }
+    };
+    auto mul = [&](auto s_) {
+        constexpr int s = decltype(s_)::value;
+#pragma unroll
+        for (int i = 0; i < C::FH; ++i)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+                acc[(s % 2) * C::FH + i][j] = mma(fb[s / 2][j], fa[s % 2][i], acc[(s % 2) * C::FH + i][j]);
+    };
+    // matrix instructions of one quarter with the NR LDS reads of the next spread among them
+    auto sched = [&](auto nr_) {
+        constexpr int NR = decltype(nr_)::value, NM = C::FH * C::FN;
+        constexpr int PAIRS = NR < NM ? NR : NM;
+#pragma unroll
+        for (int n = 0; n < PAIRS; ++n) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        }
+        if constexpr (NM > PAIRS) __builtin_amdgcn_sched_group_barrier(0x008, NM - PAIRS, 0);
+    };
+    typedef std::integral_constant<int, 0> Q0;
+    typedef std::integral_constant<int, 1> Q1;
+    typedef std::integral_constant<int, 2> Q2;
+    typedef std::integral_constant<int, 3> Q3;
+    constexpr int RA = C::FH * (AKC ? 1 : 2), RB = C::FN * (BKC ? 1 : 2);
+    typedef std::integral_constant<int, RA> NA;
+    typedef std::integral_constant<int, RA + RB> NAB;
+
+    const int nk = (p.K + KS - 1) / KS;
+    auto issue = [&](int ks) {
+        uint8_t* st = lds + (ks & 1) * C::STAGE;
+        const int left = p.K - ks * KS;
+        sa.issue(st, left);
+        sb.issue(st + C::BM * kSlice, left);
+    };
+    issue(0);
+    barrier_loads();
+    if (nk > 1) issue(1);
+    read(lds, Q0{});
+    for (int ks = 0; ks + 1 < nk; ++ks) {
+        const uint8_t* st = lds + (ks & 1) * C::STAGE;
+        read(st, Q1{});
+        mul(Q0{});
+        read(st, Q2{});
+        mul(Q1{});
+        read(st, Q3{});
+        mul(Q2{});
+        sched(NA{});
+        sched(NAB{});
+        sched(NA{});
+        barrier_loads();       // slice ks is read by every wave, slice ks + 1 has landed
+        if (ks + 2 < nk) issue(ks + 2);
+        read(lds + ((ks + 1) & 1) * C::STAGE, Q0{});
+        mul(Q3{});
+        sched(NAB{});
+    }
+    {
+        const uint8_t* st = lds + ((nk - 1) & 1) * C::STAGE;
+        read(st, Q1{});
+        mul(Q0{});
+        read(st, Q2{});
+        mul(Q1{});
+        read(st, Q3{});
+        mul(Q2{});
+        mul(Q3{});
+    }
+
+    // lane: row m0 + wm TM + 16 i + lane % 16, columns n0 + wn TN + 16 j + 4 (lane / 16) .. + 3
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+        const int64_t m = m0 + wm * C::TM + i * 16 + lane % 16;
+        if (m >= p.M) continue;
+        const int nb = n0 + wn * C::TN + 4 * (lane / 16);
+        if constexpr (EPI == kGate || EPI == kGate8) {
+#pragma unroll
+            for (int j = 0; j < C::FN; j += 2) {
+                if (nb + j * 16 >= p.N) continue;
+                if constexpr (EPI == kGate) finish_gate(p, m, nb + j * 16, acc[i][j], acc[i][j + 1]);
+                else finish_gate8(p, m, nb + j * 16, acc[i][j], acc[i][j + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) {
+                if (nb + j * 16 >= p.N) continue;
+                if constexpr (EPI == kStore) finish_store(p, m, nb + j * 16, acc[i][j]);
+                else if constexpr (EPI == kScale) finish_scale(p, m, nb + j * 16, acc[i][j]);
+                else finish_dgate(p, m, nb + j * 16, acc[i][j]);
+            }
+        }
+    }
+}
+
+typedef Tile<256, 256, 2, 4> Big;
+
+template <int TYPE, int LAYOUT, int EPI, class C>
+hipError_t launch(const Product& p, hipStream_t s) {
+    const int64_t mt = (p.M + C::BM - 1) / C::BM, nt = (p.N + C::BN - 1) / C::BN;
+    if (mt * nt > 0x7FFFFFF0 / kXcds) return hipErrorInvalidValue;
+    static const hipError_t lds_ok = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_mma<TYPE, LAYOUT, EPI, C>),
+                                                         hipFuncAttributeMaxDynamicSharedMemorySize, C::kLdsBytes);
+    if (lds_ok != hipSuccess) return lds_ok;
+    const int64_t grid = (mt * nt + kXcds - 1) / kXcds * kXcds;
+    hipLaunchKernelGGL((k_mma<TYPE, LAYOUT, EPI, C>), dim3(unsigned(grid)), dim3(C::kThreads), C::kLdsBytes, s, p,
+                       int(mt), int(nt));
+    return hipGetLastError();
+}
+
+template <int TYPE, int LAYOUT, int EPI>
+hipError_t choose(const Product& p, hipStream_t s) {
+    return launch<TYPE, LAYOUT, EPI, Big>(p, s);
+}
+
+}  // namespace
+
+hipError_t launch_mma(int type, int layout, int epi, const Product& p, hipStream_t s) {
+    if (type == kI8) {
+        if (layout == kNT && epi == kScale) return choose<kI8, kNT, kScale>(p, s);
+        if (layout == kNT && epi == kGate8) return choose<kI8, kNT, kGate8>(p, s);
+    } else if (type == kBF16) {
+        if (layout == kNT && epi == kStore) return choose<kBF16, kNT, kStore>(p, s);
+        if (layout == kNT && epi == kGate) return choose<kBF16, kNT, kGate>(p, s);
+        if (layout == kNN && epi == kStore) return choose<kBF16, kNN, kStore>(p, s);
+        if (layout == kNN && epi == kDGate) return choose<kBF16, kNN, kDGate>(p, s);
+        if (layout == kTN && epi == kStore) return choose<kBF16, kTN, kStore>(p, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace dense
+}  // namespace moe

@@ -364,7 +364,8 @@ int moe_i8_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, c
 /* ---------------------------------------------------------------- dense gated block */
 /* One gated feed-forward block over all tokens, y = Wd (silu(Wg x) * (Wu x)), on a blob of
  * moe_pack_expert's layout (the shared expert, a dense feed-forward layer: a context whose
- * config has that width).  Contexts with fp32 or bf16 weights; H = cfg.hidden, I = cfg.inter,
+ * config has that width).  Contexts with fp32 or bf16 weights; H = cfg.hidden, I = cfg.inter
+ * (each up to 2^20; up to 131056 for the 8-bit form),
  * activations in the weights' type.  Blob, x, y, dy, dx, save and workspace 16-byte aligned.
  *
  * Scratch bytes for up to max_T tokens of any moe_dense_* or moe_i8_ffn call. */
