@@ -46,6 +46,9 @@ struct Product {
 hipError_t launch_product(int type, int layout, int epi, const Product& p, hipStream_t s);
 // the same on the matrix cores: bf16 and 8-bit integers, row strides below 8 MiB
 hipError_t launch_mma(int type, int layout, int epi, const Product& p, hipStream_t s);
+// few tokens (M <= kFewTokens), NT: the weight stream
+constexpr int kFewTokens = 64;
+hipError_t launch_few(int type, int epi, const Product& p, hipStream_t s);
 // rows of cols numbers to codes and scales; x_type MOE_A_F32 / MOE_A_BF16
 hipError_t launch_quantize(const void* x, int x_type, int64_t ld_x, int64_t rows, int32_t cols, int8_t* q,
                            float* scale, hipStream_t s);
