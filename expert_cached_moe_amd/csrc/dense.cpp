@@ -70,6 +70,14 @@ int check_block(moe_ctx* ctx, int32_t T, bool i8) {
     return MOE_OK;
 }
 
+// Whether the few-token kernel quantises x itself: few enough numbers, rows that can be read
+// 16 bytes at a time, offsets below its range.
+bool quantise_inside(const void* x, int x_type, int64_t ld, int32_t T, int32_t K) {
+    const int64_t es = x_type == MOE_A_F32 ? 4 : 2;
+    return T <= 8 && int64_t(T) * K <= kFewQuant && aligned(x, 16) && ld * es % 16 == 0 &&
+           (T == 1 || ld < (int64_t(1) << 25));
+}
+
 int type_of(const moe_config& c) { return c.w_dtype == MOE_W_F32 ? kF32 : kBF16; }
 
 }  // namespace
@@ -121,18 +129,21 @@ int moe_i8_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, c
         return fail(ctx, MOE_EINVAL, "misaligned buffer");
     Product p{};
     p.a = d_x;
+    p.lda = ld_x;
     p.row_scale = d_x_scale;
-    if (!codes) {
+    const bool on_the_way = !codes && quantise_inside(d_x, x_type, ld_x, T, K);
+    if (!codes && !on_the_way) {
         const I8Work w = i8_work(T, K);
         int8_t* q = static_cast<int8_t*>(d_ws) + w.codes;
         float* sc = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + w.scale);
         hipError_t e = launch_quantize(d_x, x_type, ld_x, T, K, q, sc, s);
         if (e != hipSuccess) return hip_fail(ctx, e, "moe_i8_matmul launch");
         p.a = q;
+        p.lda = K;
         p.row_scale = sc;
     }
     p.b = d_w;
-    p.lda = p.ldb = K;
+    p.ldb = K;
     p.M = T;
     p.N = N;
     p.K = K;
@@ -141,7 +152,7 @@ int moe_i8_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, c
     p.out_f32 = y_type == MOE_A_F32;
     p.vec_out = aligned(d_y, p.out_f32 ? 16 : 8) && ld_y % 4 == 0;
     p.col_scale = d_w_scale;
-    hipError_t e = launch_product(kI8, kNT, kScale, p, s);
+    hipError_t e = on_the_way ? launch_few(kI8, kScale, p, s, x_type, true) : launch_product(kI8, kNT, kScale, p, s);
     return e == hipSuccess ? MOE_OK : hip_fail(ctx, e, "moe_i8_matmul launch");
 }
 
@@ -315,9 +326,12 @@ int moe_i8_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob8, vo
     int8_t* hq = reinterpret_cast<int8_t*>(ws + w.hq);
     float* xs = reinterpret_cast<float*>(ws + w.xs);
     float* hs = reinterpret_cast<float*>(ws + w.hs);
-    hipError_t e = launch_quantize(d_x, MOE_A_BF16, c.hidden, T, c.hidden, xq, xs, s);
+    hipError_t e = hipSuccess;
+    const bool x_inside = quantise_inside(d_x, MOE_A_BF16, c.hidden, T, c.hidden);
+    const bool h_inside = quantise_inside(ws + w.h, MOE_A_F32, c.inter, T, c.inter);
     Product p{};
-    p.a = xq;
+    if (!x_inside) e = launch_quantize(d_x, MOE_A_BF16, c.hidden, T, c.hidden, xq, xs, s);
+    p.a = x_inside ? d_x : xq;
     p.b = blob + b.gu;
     p.lda = p.ldb = c.hidden;
     p.M = T;
@@ -327,9 +341,10 @@ int moe_i8_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob8, vo
     p.ldo = c.inter;
     p.row_scale = xs;
     p.col_scale = reinterpret_cast<const float*>(blob + b.gu_scale);
-    if (e == hipSuccess) e = launch_product(kI8, kNT, kGate8, p, s);
-    if (e == hipSuccess) e = launch_quantize(ws + w.h, MOE_A_F32, c.inter, T, c.inter, hq, hs, s);
-    p.a = hq;
+    if (e == hipSuccess)
+        e = x_inside ? launch_few(kI8, kGate8, p, s, MOE_A_BF16, true) : launch_product(kI8, kNT, kGate8, p, s);
+    if (e == hipSuccess && !h_inside) e = launch_quantize(ws + w.h, MOE_A_F32, c.inter, T, c.inter, hq, hs, s);
+    p.a = h_inside ? ws + w.h : static_cast<const void*>(hq);
     p.b = blob + b.d;
     p.lda = p.ldb = c.inter;
     p.N = c.hidden;
@@ -340,7 +355,8 @@ int moe_i8_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob8, vo
     p.vec_out = 1;
     p.row_scale = hs;
     p.col_scale = reinterpret_cast<const float*>(blob + b.d_scale);
-    if (e == hipSuccess) e = launch_product(kI8, kNT, kScale, p, s);
+    if (e == hipSuccess)
+        e = h_inside ? launch_few(kI8, kScale, p, s, MOE_A_F32, true) : launch_product(kI8, kNT, kScale, p, s);
     return e == hipSuccess ? MOE_OK : hip_fail(ctx, e, "moe_i8_ffn launch");
 }
 

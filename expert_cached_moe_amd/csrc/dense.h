@@ -48,7 +48,10 @@ hipError_t launch_product(int type, int layout, int epi, const Product& p, hipSt
 hipError_t launch_mma(int type, int layout, int epi, const Product& p, hipStream_t s);
 // few tokens (M <= kFewTokens), NT: the weight stream
 constexpr int kFewTokens = 64;
-hipError_t launch_few(int type, int epi, const Product& p, hipStream_t s);
+// With quant, a holds numbers of x_type (16-byte aligned rows) that the kernel quantises for
+// itself: integer products of M <= 8 tokens with M * K <= kFewQuant.
+constexpr int kFewQuant = 16384;
+hipError_t launch_few(int type, int epi, const Product& p, hipStream_t s, int x_type = 0, bool quant = false);
 // rows of cols numbers to codes and scales; x_type MOE_A_F32 / MOE_A_BF16
 hipError_t launch_quantize(const void* x, int x_type, int64_t ld_x, int64_t rows, int32_t cols, int8_t* q,
                            float* scale, hipStream_t s);

@@ -1,16 +1,24 @@
-// Products of few tokens (up to 64) with weights contiguous along K: the weight stream.
+// Products of few tokens with weights contiguous along K: the weight stream.
 //
-// With few tokens the time is that of reading the weights once.  A workgroup owns 16 R rows of
+// With few tokens the time is that of reading the weights once.  A workgroup owns 8 R rows of
 // the weights and all tokens; its waves split K among them by 128-byte slices (wave w takes
-// slices w, w + W, ...: together they read whole runs of each row).  A wave loads weights and
-// activations straight into the registers of the 16x16 matrix instructions (16 rows of 64
-// bytes a load, two loads make the lines whole), with kDepth slices in flight; nothing is
-// staged, and the waves meet once, to add their sums in LDS in a fixed order.  The matrix
-// instruction costs the same for 1 token as for 16.
+// slices w, w + W, ...), kDepth slices in flight a wave, and meet once, to add their sums in
+// LDS in a fixed order.
 //
-// QUANT: x comes as numbers and is quantised on the way, by every workgroup for itself: the
-// codes (at most kMaxCodes bytes) are kept in LDS.  That repeats T K conversions in every
-// workgroup but saves a launch and a pass through memory.
+// Weights go straight into the registers of the 16x16 matrix instructions, 8 rows of one whole
+// 128-byte line each a load: lane l holds row l % 8, 16-byte piece (l / 16) + 4 (l % 16 / 8).
+// To the instruction those are 16 rows of 64 bytes: rows 0-7 are the weight rows' first halves,
+// rows 8-15 their second halves.  The activations are held the same way (columns 0-7: 8 tokens'
+// first halves, 8-15 their second halves), so of the 16 x 16 sums the two 8 x 8 blocks on the
+// diagonal are those of the two halves, and are added at the end; the other two are dropped.
+// That leaves half of the instruction's work unused, which a stream does not miss, and needs
+// neither a pass through LDS nor loads of half lines: streaming 201 MB as 16 rows of 64 bytes a
+// load reads 4.0-5.9 TB/s, as 8 whole lines 6.6 TB/s, as 1 KiB of one row 6.7 TB/s (workgroups
+// of 16 rows, non-temporal; of 32 rows 4.9 TB/s).
+//
+// QUANT: x comes as numbers and every workgroup quantises it for itself, into LDS, while its
+// first weights are on the way: T K conversions in each workgroup against a launch and a pass
+// through memory, for T K up to kMaxQuant.
 #include <hip/hip_runtime.h>
 
 #include "dense_common.h"
@@ -24,7 +32,10 @@ using dev::kWave;
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 constexpr uint32_t kOutside = 0xFFFFFFF0u, kRange = 0x80000000u;
-constexpr int kSlice = 128, kDepth = 4;
+constexpr int kSlice = 128, kDepth = 4, kThreads = 512, kWaves = kThreads / kWave;
+enum { kNoQuant = 0, kQuantBF16 = 1, kQuantF32 = 2 };
+constexpr int kMaxQuant = kFewQuant, kQuantVec = kMaxQuant / 8 / kThreads;   // vectors of 8 a thread
+constexpr int kCodePad = 16;             // bytes between the code rows: other banks
 
 __device__ __forceinline__ dev::f32x4 mma(const dev::u32x4& a, const dev::u32x4& b, const dev::f32x4& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -35,116 +46,225 @@ __device__ __forceinline__ i32x4 mma(const dev::u32x4& a, const dev::u32x4& b, c
 template <int TYPE> struct FewAcc { typedef dev::f32x4 T; };
 template <> struct FewAcc<kI8> { typedef i32x4 T; };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, kRange, 0x00027000);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, kRange, 0x00027000);
 }
+constexpr int kStream = 2;               // cache policy of a non-temporal load
+template <int POLICY>
 __device__ __forceinline__ dev::u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    return __builtin_bit_cast(dev::u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+    return __builtin_bit_cast(dev::u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, POLICY));
 }
 
-// MT: 16-token tiles; R: 16-row weight tiles of a workgroup (2 for the gated epilogues: a
-// block of 16 gate rows and its 16 up rows)
-template <int TYPE, int EPI, int MT, int R>
-__global__ void __launch_bounds__(512) k_few(const Product p) {
+// MT: 8-token tiles; R: 8-row weight tiles of a workgroup.  Gated epilogues: R = 2, 8 gate rows
+// and their 8 up rows (16 rows on in the weights).
+template <int TYPE, int EPI, int MT, int R, int QUANT>
+__global__ void __launch_bounds__(kThreads) k_few(const Product p0) {
     typedef typename FewAcc<TYPE>::T Acc;
     constexpr int ES = TYPE == kI8 ? 1 : 2;
     constexpr bool GATE = EPI == kGate || EPI == kGate8;
     static_assert(!GATE || R == 2, "gate and up tiles");
+    static_assert(QUANT == kNoQuant || MT == 1, "x quantised on the way: up to 8 tokens");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, waves = blockDim.x / kWave;
-    const int n0 = blockIdx.x * 16 * R, T = int(p.M);
+    __shared__ uint32_t s_top[8];
+    __shared__ float s_scale[8];
+    Product p = p0;
+    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+    const int T = int(p.M);
     const uint32_t kb = uint32_t(p.K) * ES;
-    const __amdgpu_buffer_rsrc_t rw = rsrc(static_cast<const uint8_t*>(p.b) + int64_t(n0) * p.ldb * ES);
-    const __amdgpu_buffer_rsrc_t rx = rsrc(static_cast<const uint8_t*>(p.a));
+    // first row of tile r; gated: workgroup b has inner indices 8 b .. 8 b + 7
+    const int64_t n0 = GATE ? int64_t(blockIdx.x) / 2 * 32 + blockIdx.x % 2 * 8 : int64_t(blockIdx.x) * 8 * R;
+    const __amdgpu_buffer_rsrc_t rw = rsrc(static_cast<const uint8_t*>(p.b) + n0 * p.ldb * ES);
+    const int l8 = lane % 8;
+    const uint32_t piece = uint32_t(lane / 16 + 4 * (lane % 16 / 8)) * 16;
     uint32_t wo[R], xo[MT];
 #pragma unroll
-    for (int r = 0; r < R; ++r) wo[r] = uint32_t(min(r * 16 + lane % 16, p.N - 1 - n0)) * uint32_t(p.ldb * ES);
+    for (int r = 0; r < R; ++r) {
+        const int64_t left = p.N - 1 - n0;                      // rows past N repeat the last one
+        const int row = r * (GATE ? 16 : 8) + l8;
+        wo[r] = uint32_t(row < left ? row : int(left)) * uint32_t(p.ldb * ES);
+    }
+    // numbers to quantise: vector v of a thread is 8 numbers of row qrow[v]
+    constexpr int NV = QUANT == kNoQuant ? 1 : kQuantVec;
+    uint4 qv[NV][QUANT == kQuantF32 ? 2 : 1];
+    int qrow[NV], qcol[NV];
+    if constexpr (QUANT != kNoQuant) {
+        const int per = p.K / 8;
+        const __amdgpu_buffer_rsrc_t rx = rsrc(p.a);
+        const uint32_t es = QUANT == kQuantF32 ? 4 : 2;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) xo[m] = uint32_t(min(m * 16 + lane % 16, T - 1)) * uint32_t(p.lda * ES);
+        for (int v = 0; v < NV; ++v) {
+            const int i = v * kThreads + tid;
+            qrow[v] = i / per;
+            qcol[v] = i % per * 8;
+            const uint32_t o = qrow[v] < T ? (uint32_t(qrow[v]) * uint32_t(p.lda) + qcol[v]) * es : kOutside;
+#pragma unroll
+            for (int q = 0; q < int(es) / 2; ++q) {
+                const dev::u32x4 u = load16<0>(rx, qrow[v] < T ? o + 16 * q : kOutside);
+                qv[v][q] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+        }
+        if (tid < 8) s_top[tid] = 0;
+    }
+    const __amdgpu_buffer_rsrc_t rx = rsrc(p.a);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) xo[m] = uint32_t(min(m * 8 + l8, T - 1)) * (QUANT != kNoQuant ? p.K + kCodePad : uint32_t(p.lda * ES));
     Acc acc[MT][R];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int r = 0; r < R; ++r) acc[m][r] = Acc{0, 0, 0, 0};
-    const uint32_t stride = uint32_t(waves) * kSlice;
-    for (uint32_t s = wave * kSlice; s < kb; s += stride * kDepth) {
-        dev::u32x4 w[kDepth][2][R], x[kDepth][2][MT];
+    constexpr uint32_t kStride = kWaves * kSlice;
+    dev::u32x4 w[kDepth][R];
+    auto load_w = [&](uint32_t s) {
 #pragma unroll
-        for (int d = 0; d < kDepth; ++d)
+        for (int d = 0; d < kDepth; ++d) {
+            const uint32_t k = s + d * kStride + piece;         // past K: zeros
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t k = s + d * stride + h * 64 + (lane / 16) * 16;
-                const bool in = k < kb;            // past K: both operands read zeros
+            for (int r = 0; r < R; ++r) w[d][r] = load16<kStream>(rw, k < kb ? wo[r] + k : kOutside);
+        }
+    };
+    uint32_t s = wave * kSlice;
+    load_w(s);
+    if constexpr (QUANT != kNoQuant) {
+        float f[NV][8];
 #pragma unroll
-                for (int r = 0; r < R; ++r) w[d][h][r] = load16(rw, in ? wo[r] + k : kOutside);
+        for (int v = 0; v < NV; ++v) {
+            if constexpr (QUANT == kQuantF32) {
+                const uint32_t u[8] = {qv[v][0].x, qv[v][0].y, qv[v][0].z, qv[v][0].w,
+                                       qv[v][1].x, qv[v][1].y, qv[v][1].z, qv[v][1].w};
 #pragma unroll
-                for (int m = 0; m < MT; ++m) x[d][h][m] = load16(rx, in ? xo[m] + k : kOutside);
+                for (int j = 0; j < 8; ++j) f[v][j] = __uint_as_float(u[j]);
+            } else {
+                const uint32_t u[4] = {qv[v][0].x, qv[v][0].y, qv[v][0].z, qv[v][0].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[v][2 * j] = dev::bf16_lo(u[j]), f[v][2 * j + 1] = dev::bf16_hi(u[j]);
             }
+        }
+        __syncthreads();                                        // s_top is clear
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[v][j]) & 0x7FFFFFFFu);
+            const int first = __builtin_amdgcn_readfirstlane(qrow[v]);
+            if (first >= T) break;
+            if (__all(qrow[v] == first)) {                      // one row in the wave: one update
+#pragma unroll
+                for (int d = kWave / 2; d >= 1; d >>= 1) top = max(top, uint32_t(__shfl_xor(int(top), d, kWave)));
+                if (lane == 0) atomicMax(&s_top[first], top);
+            } else if (qrow[v] < T) {
+                atomicMax(&s_top[qrow[v]], top);
+            }
+        }
+        __syncthreads();
+        if (tid < T) s_scale[tid] = row_scale(s_top[tid]);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            if (qrow[v] >= T) break;
+            const float sc = row_scale(s_top[qrow[v]]), inv = inverse_scale(sc);
+            uint32_t c[2] = {0, 0};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) c[j / 4] |= uint32_t(quantize_one(f[v][j], sc, inv) & 255) << (8 * (j % 4));
+            *reinterpret_cast<uint2*>(lds + qrow[v] * (p.K + kCodePad) + qcol[v]) = make_uint2(c[0], c[1]);
+        }
+        __syncthreads();
+        p.row_scale = s_scale;
+    }
+    while (true) {
+        dev::u32x4 x[kDepth][MT];
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+            const uint32_t k = s + d * kStride + piece;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                if constexpr (QUANT != kNoQuant)                // (any codes do past K: the weights are zeros there)
+                    x[d][m] = *reinterpret_cast<const dev::u32x4*>(lds + (k < kb ? xo[m] + k : 0));
+                else
+                    x[d][m] = load16<0>(rx, k < kb ? xo[m] + k : kOutside);
+            }
+        }
 #pragma unroll
         for (int d = 0; d < kDepth; ++d)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int r = 0; r < R; ++r) acc[m][r] = mma(w[d][h][r], x[d][h][m], acc[m][r]);
+                for (int r = 0; r < R; ++r) acc[m][r] = mma(w[d][r], x[d][m], acc[m][r]);
+        s += kStride * kDepth;
+        if (s >= kb) break;
+        load_w(s);
     }
-    Acc* red = reinterpret_cast<Acc*>(lds);        // [wave][m][r][lane]
+    if constexpr (QUANT != kNoQuant) __syncthreads();           // the codes are read; their place takes the sums
+    // sums of the diagonal blocks: lanes 0-7 and 16-23 (rows 0-7, first halves), 40-47 and 56-63
+    // (rows 8-15, second halves) as entry lane % 8 + 8 (lane / 16 % 2) of half lane / 32
+    Acc* red = reinterpret_cast<Acc*>(lds);                     // [wave][half][m][r][16]
+    if ((lane % 16) / 8 == lane / 32) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int r = 0; r < R; ++r) red[((wave * MT + m) * R + r) * kWave + lane] = acc[m][r];
+            for (int r = 0; r < R; ++r)
+                red[(((wave * 2 + lane / 32) * MT + m) * R + r) * 16 + l8 + 8 * (lane / 16 % 2)] = acc[m][r];
+    }
     __syncthreads();
-    constexpr int PER = GATE ? 2 : 1, ITEMS = MT * R / PER;    // results of a wave at a time
-    for (int it = wave; it < ITEMS; it += waves) {
+    constexpr int PER = GATE ? 2 : 1, ITEMS = MT * R / PER * 16;
+    for (int it = tid; it < ITEMS; it += kThreads) {
+        const int tile = it / 16 * PER, ent = it % 16, m = tile / R, r = tile % R;
         Acc sum[PER];
 #pragma unroll
         for (int q = 0; q < PER; ++q) {
-            sum[q] = red[(it * PER + q) * kWave + lane];
-            for (int v = 1; v < waves; ++v) sum[q] += red[(v * MT * R + it * PER + q) * kWave + lane];
+            sum[q] = red[(tile + q) * 16 + ent];
+#pragma unroll
+            for (int v = 1; v < 2 * kWaves; ++v) sum[q] += red[(v * MT * R + tile + q) * 16 + ent];
         }
-        const int m = it * PER / R, r = it * PER % R;
-        const int t = m * 16 + lane % 16, n = n0 + r * 16 + 4 * (lane / 16);
+        const int t = m * 8 + ent % 8;
+        const int64_t n = n0 + r * 8 + 4 * (ent / 8);
         if (t >= T || n >= p.N) continue;
-        if constexpr (EPI == kGate) finish_gate(p, t, n, sum[0], sum[PER - 1]);
-        else if constexpr (EPI == kGate8) finish_gate8(p, t, n, sum[0], sum[PER - 1]);
-        else if constexpr (EPI == kStore) finish_store(p, t, n, sum[0]);
-        else finish_scale(p, t, n, sum[0]);
+        if constexpr (EPI == kGate) finish_gate(p, t, int(n), sum[0], sum[PER - 1]);
+        else if constexpr (EPI == kGate8) finish_gate8(p, t, int(n), sum[0], sum[PER - 1]);
+        else if constexpr (EPI == kStore) finish_store(p, t, int(n), sum[0]);
+        else finish_scale(p, t, int(n), sum[0]);
     }
 }
 
-template <int TYPE, int EPI, int MT, int R>
+template <int TYPE, int EPI, int MT, int R, int QUANT>
 hipError_t launch_few_as(const Product& p, hipStream_t s) {
-    const int64_t groups = (int64_t(p.N) + 16 * R - 1) / (16 * R);
-    const int waves = 8;
-    hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R>), dim3(unsigned(groups)), dim3(waves * kWave),
-                       waves * MT * R * kWave * 16, s, p);
+    constexpr bool GATE = EPI == kGate || EPI == kGate8;
+    const int64_t groups = GATE ? p.N / 16 : (int64_t(p.N) + 8 * R - 1) / (8 * R);
+    const int sums = 2 * kWaves * MT * R * 16 * 16, codes = QUANT ? int(p.M) * (p.K + kCodePad) : 0;
+    hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT>), dim3(unsigned(groups)), dim3(kThreads),
+                       sums > codes ? sums : codes, s, p);
     return hipGetLastError();
 }
 
 template <int TYPE, int EPI>
-hipError_t choose_few(const Product& p, hipStream_t s) {
+hipError_t choose_few(const Product& p, int quant, hipStream_t s) {
     constexpr bool GATE = EPI == kGate || EPI == kGate8;
-    const int mt = int((p.M + 15) / 16);
-    if constexpr (!GATE) {
-        // one row tile a workgroup while that is what fills the chip
-        if (p.N < 16 * 1024 && mt == 1) return launch_few_as<TYPE, EPI, 1, 1>(p, s);
+    const int mt = int((p.M + 7) / 8);
+    if constexpr (TYPE == kI8) {
+        if (quant == kQuantBF16) return launch_few_as<TYPE, EPI, 1, 2, kQuantBF16>(p, s);
+        if (quant == kQuantF32) return launch_few_as<TYPE, EPI, 1, 2, kQuantF32>(p, s);
     }
-    if (mt == 1) return launch_few_as<TYPE, EPI, 1, 2>(p, s);
-    if (mt == 2) return launch_few_as<TYPE, EPI, 2, 2>(p, s);
-    return launch_few_as<TYPE, EPI, 4, 2>(p, s);
+    if constexpr (!GATE) {
+        // 16 rows a workgroup leave CUs idle below N = 4096: 8 then
+        if (p.N < 4096 && mt == 1) return launch_few_as<TYPE, EPI, 1, 1, kNoQuant>(p, s);
+    }
+    if (mt == 1) return launch_few_as<TYPE, EPI, 1, 2, kNoQuant>(p, s);
+    if (mt == 2) return launch_few_as<TYPE, EPI, 2, 2, kNoQuant>(p, s);
+    if (mt <= 4) return launch_few_as<TYPE, EPI, 4, 2, kNoQuant>(p, s);
+    return launch_few_as<TYPE, EPI, 8, 2, kNoQuant>(p, s);
 }
 
 }  // namespace
 
-hipError_t launch_few(int type, int epi, const Product& p, hipStream_t s) {
+hipError_t launch_few(int type, int epi, const Product& p, hipStream_t s, int x_type, bool quant) {
     if (p.M > kFewTokens) return hipErrorInvalidValue;
+    const int q = !quant ? kNoQuant : x_type == MOE_A_F32 ? kQuantF32 : kQuantBF16;
+    if (quant && (type != kI8 || p.M > 8 || p.M * p.K > kFewQuant)) return hipErrorInvalidValue;
     if (type == kI8) {
-        if (epi == kScale) return choose_few<kI8, kScale>(p, s);
-        if (epi == kGate8) return choose_few<kI8, kGate8>(p, s);
+        if (epi == kScale) return choose_few<kI8, kScale>(p, q, s);
+        if (epi == kGate8) return choose_few<kI8, kGate8>(p, q, s);
     } else if (type == kBF16) {
-        if (epi == kStore) return choose_few<kBF16, kStore>(p, s);
-        if (epi == kGate) return choose_few<kBF16, kGate>(p, s);
+        if (epi == kStore) return choose_few<kBF16, kStore>(p, q, s);
+        if (epi == kGate) return choose_few<kBF16, kGate>(p, q, s);
     }
     return hipErrorInvalidValue;
 }
