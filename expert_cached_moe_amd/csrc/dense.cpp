@@ -10,24 +10,29 @@ namespace {
 
 using namespace dense;
 
+std::atomic<int> g_units[64];
+
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 // Workspace of moe_i8_matmul: codes and scales of x.
+constexpr int64_t kSplitTokens = 1024;
 struct I8Work {
-    int64_t codes = 0, scale = 0, bytes = 0;
+    int64_t codes = 0, scale = 0, part = 0, bytes = 0;
 };
 I8Work i8_work(int64_t T, int64_t K) {
     I8Work w;
     if (T < 1) T = 1;
     w.scale = align256(T * K);
-    w.bytes = align256(w.scale + T * 4);
+    w.part = align256(w.scale + T * 4);
+    // (more tokens fill the chip unsplit)
+    w.bytes = w.part + (T > kSplitTokens ? 0 : kPartBytes);
     return w;
 }
 
 // Workspace of the block's calls: the forward pass without a save buffer keeps h, the backward
 // pass dg and du; the 8-bit form the codes of x, h in fp32 and the codes of h.
 struct BlockWork {
-    int64_t xq = 0, xs = 0, h = 0, hq = 0, hs = 0, bytes = 0;
+    int64_t xq = 0, xs = 0, h = 0, hq = 0, hs = 0, part = 0, bytes = 0;
 };
 BlockWork block_work(const moe_config& c, int64_t T) {
     BlockWork w;
@@ -38,7 +43,8 @@ BlockWork block_work(const moe_config& c, int64_t T) {
     w.hq = align256(w.h + T * I * 4);
     w.hs = align256(w.hq + T * I);
     const int64_t i8 = c.w_dtype == MOE_W_BF16 ? align256(w.hs + T * 4) : 0, dgu = align256(T * 2 * I * es);
-    w.bytes = i8 > dgu ? i8 : dgu;
+    w.part = i8 > dgu ? i8 : dgu;
+    w.bytes = w.part + kPartBytes;
     return w;
 }
 
@@ -81,6 +87,18 @@ bool quantise_inside(const void* x, int x_type, int64_t ld, int32_t T, int32_t K
 int type_of(const moe_config& c) { return c.w_dtype == MOE_W_F32 ? kF32 : kBF16; }
 
 }  // namespace
+
+int dense::compute_units() {
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+    n = g_units[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1) n = 256;
+        g_units[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -131,9 +149,11 @@ int moe_i8_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, c
     p.a = d_x;
     p.lda = ld_x;
     p.row_scale = d_x_scale;
+    const I8Work w = i8_work(T, K);
+    p.part = static_cast<uint8_t*>(d_ws) + w.part;
+    p.part_bytes = w.bytes - w.part;
     const bool on_the_way = !codes && quantise_inside(d_x, x_type, ld_x, T, K);
     if (!codes && !on_the_way) {
-        const I8Work w = i8_work(T, K);
         int8_t* q = static_cast<int8_t*>(d_ws) + w.codes;
         float* sc = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + w.scale);
         hipError_t e = launch_quantize(d_x, x_type, ld_x, T, K, q, sc, s);
@@ -184,6 +204,8 @@ int moe_dense_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob, 
     const uint8_t* blob = static_cast<const uint8_t*>(d_blob);
     uint8_t* h = d_save ? static_cast<uint8_t*>(d_save) + save_h_offset(c, T) : static_cast<uint8_t*>(d_ws);
     Product p{};
+    p.part = static_cast<uint8_t*>(d_ws) + block_work(c, T).part;
+    p.part_bytes = kPartBytes;
     p.a = d_x;
     p.b = blob + ctx->lay.gu;
     p.lda = p.ldb = c.hidden;
@@ -233,6 +255,8 @@ int moe_dense_ffn_backward(moe_ctx* ctx, const void* d_dy, const void* d_x, int3
     hipError_t e;
     // dg, du [T][2I] from dh = dy . Wd, which is never stored
     Product p{};
+    p.part = static_cast<uint8_t*>(d_ws) + block_work(c, T).part;
+    p.part_bytes = kPartBytes;
     p.a = d_dy;
     p.lda = H;
     p.b = blob + ctx->lay.d;
@@ -246,6 +270,8 @@ int moe_dense_ffn_backward(moe_ctx* ctx, const void* d_dy, const void* d_x, int3
     if ((e = launch_product(type, kNN, kDGate, p, s)) != hipSuccess) return hip_fail(ctx, e, "moe_dense_ffn_backward launch");
     if (dblob) {
         Product w{};                                   // dWd = dy^T h
+        w.part = p.part;
+        w.part_bytes = p.part_bytes;
         w.a = d_dy;
         w.lda = H;
         w.b = save + save_h_offset(c, T);
@@ -269,7 +295,9 @@ int moe_dense_ffn_backward(moe_ctx* ctx, const void* d_dy, const void* d_x, int3
             return hip_fail(ctx, e, "moe_dense_ffn_backward launch");
     }
     if (d_dx) {
-        Product q{};                                   // dx = dg Wg + du Wu
+        Product q{};
+        q.part = p.part;
+        q.part_bytes = p.part_bytes;                   // dx = dg Wg + du Wu
         q.a = d_ws;
         q.lda = 2 * I;
         q.b = blob + ctx->lay.gu;
@@ -330,6 +358,8 @@ int moe_i8_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob8, vo
     const bool x_inside = quantise_inside(d_x, MOE_A_BF16, c.hidden, T, c.hidden);
     const bool h_inside = quantise_inside(ws + w.h, MOE_A_F32, c.inter, T, c.inter);
     Product p{};
+    p.part = ws + w.part;
+    p.part_bytes = kPartBytes;
     if (!x_inside) e = launch_quantize(d_x, MOE_A_BF16, c.hidden, T, c.hidden, xq, xs, s);
     p.a = x_inside ? d_x : xq;
     p.b = blob + b.gu;

@@ -39,15 +39,28 @@ struct Product {
     int32_t vec_out;            // kScale: rows of out are aligned for stores of four values
     const float* row_scale;     // kScale, kGate8
     const float* col_scale;
+    void* part;                 // scratch for partial sums of part_bytes (0: none)
+    int64_t part_bytes;
     void* gu;                   // kGate: written when not null; kDGate: read; rows of 2 I elements
 };
+
+// Scratch for partial sums: products with few tiles are split along K to fill the chip.
+constexpr int64_t kPartBytes = int64_t(32) << 20;
+// Compute units of the current device.
+int compute_units();
 
 // One product on stream s: type kF32 / kBF16 / kI8, layout kNT / kNN / kTN, epilogue as above.
 hipError_t launch_product(int type, int layout, int epi, const Product& p, hipStream_t s);
 // the same on the matrix cores: bf16 and 8-bit integers, row strides below 8 MiB
 hipError_t launch_mma(int type, int layout, int epi, const Product& p, hipStream_t s);
-// few tokens (M <= kFewTokens), NT: the weight stream
-constexpr int kFewTokens = 64;
+// few tokens, NT: the weight stream.  It takes up to 16 tokens, and up to 32 while the weights
+// are 32 MiB at most: 100003 x 4096 codes take it 90 us at 16 tokens and 101 at 24, the tiles 106
+// and 93-108; a 4096 x 12288 bf16 block 82 and 110 us against 87 and 88; 8192 x 4096 codes 10.7
+// and 13.7 us against 14.6; 2048 x 2048 codes 5.2 and 6.0 against 7.3.
+constexpr int kFewTokens = 32;
+inline bool few_tokens(const Product& p, int es) {
+    return p.M <= 16 || (p.M <= kFewTokens && int64_t(p.N) * p.K * es <= (int64_t(32) << 20));
+}
 // With quant, a holds numbers of x_type (16-byte aligned rows) that the kernel quantises for
 // itself: integer products of M <= 8 tokens with M * K <= kFewQuant.
 constexpr int kFewQuant = 16384;

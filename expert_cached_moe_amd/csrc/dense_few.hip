@@ -16,6 +16,13 @@
 // load reads 4.0-5.9 TB/s, as 8 whole lines 6.6 TB/s, as 1 KiB of one row 6.7 TB/s (workgroups
 // of 16 rows, non-temporal; of 32 rows 4.9 TB/s).
 //
+// WALK (more than 8 tokens): a workgroup walks groups of 8 R rows; the next group's first weights
+// are requested before the sums of the current one are added, and where K is one pass (ONE:
+// kDepth slices a wave) x stays in registers for all groups.  That saves reading x for every
+// group, which from 9 tokens on is as much as the weights (100003 x 4096 codes, 16 tokens: 90
+// against 109 us); up to 8 tokens the registers it takes cost more than it saves (8 tokens: 81
+// against 78 us, 1 token 76 against 64).
+//
 // QUANT: x comes as numbers and every workgroup quantises it for itself, into LDS, while its
 // first weights are on the way: T K conversions in each workgroup against a launch and a pass
 // through memory, for T K up to kMaxQuant.
@@ -55,14 +62,23 @@ __device__ __forceinline__ dev::u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t 
     return __builtin_bit_cast(dev::u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, POLICY));
 }
 
+// Barrier over LDS alone: the next weights stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_s_waitcnt(0xC07F);      // lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // MT: 8-token tiles; R: 8-row weight tiles of a workgroup.  Gated epilogues: R = 2, 8 gate rows
 // and their 8 up rows (16 rows on in the weights).
-template <int TYPE, int EPI, int MT, int R, int QUANT>
-__global__ void __launch_bounds__(kThreads) k_few(const Product p0) {
+template <int TYPE, int EPI, int MT, int R, int QUANT, bool WALK, bool ONE>
+__global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) {
     typedef typename FewAcc<TYPE>::T Acc;
     constexpr int ES = TYPE == kI8 ? 1 : 2;
     constexpr bool GATE = EPI == kGate || EPI == kGate8;
     static_assert(!GATE || R == 2, "gate and up tiles");
+    static_assert(WALK || !ONE, "x is kept for the groups of a walk");
     static_assert(QUANT == kNoQuant || MT == 1, "x quantised on the way: up to 8 tokens");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     __shared__ uint32_t s_top[8];
@@ -71,18 +87,11 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0) {
     const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
     const int T = int(p.M);
     const uint32_t kb = uint32_t(p.K) * ES;
-    // first row of tile r; gated: workgroup b has inner indices 8 b .. 8 b + 7
-    const int64_t n0 = GATE ? int64_t(blockIdx.x) / 2 * 32 + blockIdx.x % 2 * 8 : int64_t(blockIdx.x) * 8 * R;
-    const __amdgpu_buffer_rsrc_t rw = rsrc(static_cast<const uint8_t*>(p.b) + n0 * p.ldb * ES);
     const int l8 = lane % 8;
     const uint32_t piece = uint32_t(lane / 16 + 4 * (lane % 16 / 8)) * 16;
-    uint32_t wo[R], xo[MT];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int64_t left = p.N - 1 - n0;                      // rows past N repeat the last one
-        const int row = r * (GATE ? 16 : 8) + l8;
-        wo[r] = uint32_t(row < left ? row : int(left)) * uint32_t(p.ldb * ES);
-    }
+    // first row of group g; gated: group g has inner indices 8 g .. 8 g + 7
+    auto first_row = [&](int g) { return GATE ? int64_t(g) / 2 * 32 + g % 2 * 8 : int64_t(g) * 8 * R; };
+    uint32_t xo[MT];
     // numbers to quantise: vector v of a thread is 8 numbers of row qrow[v]
     constexpr int NV = QUANT == kNoQuant ? 1 : kQuantVec;
     uint4 qv[NV][QUANT == kQuantF32 ? 2 : 1];
@@ -108,14 +117,17 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0) {
     const __amdgpu_buffer_rsrc_t rx = rsrc(p.a);
 #pragma unroll
     for (int m = 0; m < MT; ++m) xo[m] = uint32_t(min(m * 8 + l8, T - 1)) * (QUANT != kNoQuant ? p.K + kCodePad : uint32_t(p.lda * ES));
-    Acc acc[MT][R];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int r = 0; r < R; ++r) acc[m][r] = Acc{0, 0, 0, 0};
     constexpr uint32_t kStride = kWaves * kSlice;
     dev::u32x4 w[kDepth][R];
-    auto load_w = [&](uint32_t s) {
+    auto load_w = [&](int g, uint32_t s) {
+        const int64_t n0 = first_row(g), left = p.N - 1 - n0;   // rows past N repeat the last one
+        const __amdgpu_buffer_rsrc_t rw = rsrc(static_cast<const uint8_t*>(p.b) + n0 * p.ldb * ES);
+        uint32_t wo[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int row = r * (GATE ? 16 : 8) + l8;
+            wo[r] = uint32_t(row < left ? row : int(left)) * uint32_t(p.ldb * ES);
+        }
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {
             const uint32_t k = s + d * kStride + piece;         // past K: zeros
@@ -123,8 +135,8 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0) {
             for (int r = 0; r < R; ++r) w[d][r] = load16<kStream>(rw, k < kb ? wo[r] + k : kOutside);
         }
     };
-    uint32_t s = wave * kSlice;
-    load_w(s);
+    int g = blockIdx.x;
+    load_w(g, wave * kSlice);
     if constexpr (QUANT != kNoQuant) {
         float f[NV][8];
 #pragma unroll
@@ -170,8 +182,11 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0) {
         __syncthreads();
         p.row_scale = s_scale;
     }
-    while (true) {
-        dev::u32x4 x[kDepth][MT];
+    // LDS: the codes, then two areas of sums, [wave][half][m][r][16]
+    constexpr int kSums = 2 * kWaves * MT * R * 16;
+    Acc* red0 = reinterpret_cast<Acc*>(lds + (QUANT != kNoQuant ? T * (p.K + kCodePad) : 0));
+    dev::u32x4 x[kDepth][MT];
+    auto load_x = [&](uint32_t s) {
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {
             const uint32_t k = s + d * kStride + piece;
@@ -183,45 +198,61 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0) {
                     x[d][m] = load16<0>(rx, k < kb ? xo[m] + k : kOutside);
             }
         }
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int r = 0; r < R; ++r) acc[m][r] = mma(w[d][r], x[d][m], acc[m][r]);
-        s += kStride * kDepth;
-        if (s >= kb) break;
-        load_w(s);
-    }
-    if constexpr (QUANT != kNoQuant) __syncthreads();           // the codes are read; their place takes the sums
-    // sums of the diagonal blocks: lanes 0-7 and 16-23 (rows 0-7, first halves), 40-47 and 56-63
-    // (rows 8-15, second halves) as entry lane % 8 + 8 (lane / 16 % 2) of half lane / 32
-    Acc* red = reinterpret_cast<Acc*>(lds);                     // [wave][half][m][r][16]
-    if ((lane % 16) / 8 == lane / 32) {
+    };
+    if constexpr (ONE) load_x(wave * kSlice);
+    for (int turn = 0; g < groups; ++turn) {
+        const int next = g + int(gridDim.x);
+        const int64_t n0 = first_row(g);
+        Acc acc[MT][R];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                red[(((wave * 2 + lane / 32) * MT + m) * R + r) * 16 + l8 + 8 * (lane / 16 % 2)] = acc[m][r];
-    }
-    __syncthreads();
-    constexpr int PER = GATE ? 2 : 1, ITEMS = MT * R / PER * 16;
-    for (int it = tid; it < ITEMS; it += kThreads) {
-        const int tile = it / 16 * PER, ent = it % 16, m = tile / R, r = tile % R;
-        Acc sum[PER];
+            for (int r = 0; r < R; ++r) acc[m][r] = Acc{0, 0, 0, 0};
+        for (uint32_t s = wave * kSlice;;) {
+            if constexpr (!ONE) load_x(s);
 #pragma unroll
-        for (int q = 0; q < PER; ++q) {
-            sum[q] = red[(tile + q) * 16 + ent];
+            for (int d = 0; d < kDepth; ++d)
 #pragma unroll
-            for (int v = 1; v < 2 * kWaves; ++v) sum[q] += red[(v * MT * R + tile + q) * 16 + ent];
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) acc[m][r] = mma(w[d][r], x[d][m], acc[m][r]);
+            s += kStride * kDepth;
+            if (ONE || s >= kb) break;
+            load_w(g, s);
         }
-        const int t = m * 8 + ent % 8;
-        const int64_t n = n0 + r * 8 + 4 * (ent / 8);
-        if (t >= T || n >= p.N) continue;
-        if constexpr (EPI == kGate) finish_gate(p, t, int(n), sum[0], sum[PER - 1]);
-        else if constexpr (EPI == kGate8) finish_gate8(p, t, int(n), sum[0], sum[PER - 1]);
-        else if constexpr (EPI == kStore) finish_store(p, t, int(n), sum[0]);
-        else finish_scale(p, t, int(n), sum[0]);
+        if (WALK && next < groups) load_w(next, wave * kSlice);
+        // sums of the diagonal blocks: lanes 0-7 and 16-23 (rows 0-7, first halves), 40-47 and
+        // 56-63 (rows 8-15, second halves) as entry lane % 8 + 8 (lane / 16 % 2) of half lane / 32
+        Acc* red = red0 + (turn & 1) * kSums;
+        if ((lane % 16) / 8 == lane / 32) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    red[(((wave * 2 + lane / 32) * MT + m) * R + r) * 16 + l8 + 8 * (lane / 16 % 2)] = acc[m][r];
+        }
+        // (the other area's readers are past it: they met at the barrier before this one)
+        lds_barrier();
+        constexpr int PER = GATE ? 2 : 1, ITEMS = MT * R / PER * 16;
+        for (int it = tid; it < ITEMS; it += kThreads) {
+            const int tile = it / 16 * PER, ent = it % 16, m = tile / R, r = tile % R;
+            Acc sum[PER];
+#pragma unroll
+            for (int q = 0; q < PER; ++q) {
+                sum[q] = red[(tile + q) * 16 + ent];
+#pragma unroll
+                for (int v = 1; v < 2 * kWaves; ++v) sum[q] += red[(v * MT * R + tile + q) * 16 + ent];
+            }
+            const int t = m * 8 + ent % 8;
+            const int64_t n = n0 + r * 8 + 4 * (ent / 8);
+            if (t >= T || n >= p.N) continue;
+            if constexpr (EPI == kGate) finish_gate(p, t, int(n), sum[0], sum[PER - 1]);
+            else if constexpr (EPI == kGate8) finish_gate8(p, t, int(n), sum[0], sum[PER - 1]);
+            else if constexpr (EPI == kStore) finish_store(p, t, int(n), sum[0]);
+            else finish_scale(p, t, int(n), sum[0]);
+        }
+        if (!WALK) break;
+        g = next;
     }
 }
 
@@ -229,9 +260,20 @@ template <int TYPE, int EPI, int MT, int R, int QUANT>
 hipError_t launch_few_as(const Product& p, hipStream_t s) {
     constexpr bool GATE = EPI == kGate || EPI == kGate8;
     const int64_t groups = GATE ? p.N / 16 : (int64_t(p.N) + 8 * R - 1) / (8 * R);
-    const int sums = 2 * kWaves * MT * R * 16 * 16, codes = QUANT ? int(p.M) * (p.K + kCodePad) : 0;
-    hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT>), dim3(unsigned(groups)), dim3(kThreads),
-                       sums > codes ? sums : codes, s, p);
+    constexpr bool WALK = MT > 1;
+    const int lds = (WALK ? 2 : 1) * 2 * kWaves * MT * R * 16 * 16 + (QUANT ? int(p.M) * (p.K + kCodePad) : 0);
+    if constexpr (!WALK) {
+        hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, false, false>), dim3(unsigned(groups)), dim3(kThreads), lds, s,
+                           p, int(groups));
+    } else {
+        // up to four workgroups a CU, each the same number of groups
+        const int64_t most = int64_t(compute_units()) * 4, turns = (groups + most - 1) / most;
+        const dim3 grid(unsigned((groups + turns - 1) / turns));
+        if (p.K * (TYPE == kI8 ? 1 : 2) <= kWaves * kSlice * kDepth)
+            hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, true, true>), grid, dim3(kThreads), lds, s, p, int(groups));
+        else
+            hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, true, false>), grid, dim3(kThreads), lds, s, p, int(groups));
+    }
     return hipGetLastError();
 }
 
@@ -249,8 +291,7 @@ hipError_t choose_few(const Product& p, int quant, hipStream_t s) {
     }
     if (mt == 1) return launch_few_as<TYPE, EPI, 1, 2, kNoQuant>(p, s);
     if (mt == 2) return launch_few_as<TYPE, EPI, 2, 2, kNoQuant>(p, s);
-    if (mt <= 4) return launch_few_as<TYPE, EPI, 4, 2, kNoQuant>(p, s);
-    return launch_few_as<TYPE, EPI, 8, 2, kNoQuant>(p, s);
+    return launch_few_as<TYPE, EPI, 4, 2, kNoQuant>(p, s);
 }
 
 }  // namespace

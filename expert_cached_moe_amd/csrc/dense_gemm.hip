@@ -126,7 +126,8 @@ hipError_t launch_simple(const Product& p, hipStream_t s) {
 hipError_t launch_product(int type, int layout, int epi, const Product& p, hipStream_t s) {
     if (p.M <= 0 || p.N <= 0) return hipSuccess;
     if (type != kF32)
-        return layout == kNT && p.M <= kFewTokens ? launch_few(type, epi, p, s) : launch_mma(type, layout, epi, p, s);
+        return layout == kNT && few_tokens(p, type == kI8 ? 1 : 2) ? launch_few(type, epi, p, s)
+                                                                   : launch_mma(type, layout, epi, p, s);
     if (layout == kNT && epi == kStore) return launch_simple<kF32, kNT, kStore>(p, s);
     if (layout == kNT && epi == kGate) return launch_simple<kF32, kNT, kGate>(p, s);
     if (layout == kNN && epi == kStore) return launch_simple<kF32, kNN, kStore>(p, s);

@@ -63,8 +63,13 @@ __device__ __forceinline__ i32x4 mma(const i32x4& a, const i32x4& b, const i32x4
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
-// permutation of the 32-byte units of row k of an operand that is not contiguous along K
-__device__ __forceinline__ int unit_swz(int k) { return (k & 3) | ((k >> 1) & 4); }
+// permutation of the 32-byte units of row k of an operand that is not contiguous along K: rows
+// of 256 bytes and more all start on the same bank and have 8 units to permute; rows of 128
+// bytes (X = 64) alternate between the halves of the banks and have 4
+template <int X>
+__device__ __forceinline__ int unit_swz(int k) {
+    return X == 64 ? ((k >> 1) & 1) | ((k >> 2) & 2) : (k & 3) | ((k >> 1) & 4);
+}
 
 // One operand's tile: X rows (tokens or weights) by one slice of K, X * 128 bytes in LDS.
 // KC: contiguous along K.
@@ -73,18 +78,20 @@ struct Side {
     static constexpr int Q = X * kSlice / 1024 / NW;      // 1 KiB loads of a wave per slice
     static constexpr int KS = kSlice / ES;                // k in a slice
     static_assert(Q * NW * 1024 == X * kSlice, "loads split over the waves");
-    static_assert(KC || (ES == 2 && X >= 128), "transposing reads: 16-bit elements, 8 units a row");
+    static_assert(KC || ES == 2, "transposing reads: 16-bit elements");
 
     const uint8_t* base;     // (uniform) first row / column of the tile at the next slice to load
     int64_t step;            // bytes from slice to slice
     uint32_t off[Q];         // this lane's offsets from base
 
-    // x0: the tile's first row, n_rows rows in all; ld elements between rows (KC) or between k
-    __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t x0, int64_t n_rows) {
+    // x0: the tile's first row, n_rows rows in all; ld elements between rows (KC) or between k;
+    // first: the first slice to load
+    __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t x0, int64_t n_rows, int first) {
         const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
         const uint32_t ldb = uint32_t(ld) * ES;
         base = static_cast<const uint8_t*>(p) + (KC ? x0 * ld * ES : x0 * ES);
         step = KC ? kSlice : int64_t(KS) * ld * ES;
+        base += first * step;
         const int left = int(n_rows - x0 < X ? n_rows - x0 : X);
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
@@ -95,7 +102,7 @@ struct Side {
             } else {
                 constexpr int CPR = X * ES / 16;          // 16-byte chunks of a k row
                 const int k = (i * 64 + lane) / CPR, c = (i * 64 + lane) % CPR;
-                const int col = (c ^ (unit_swz(k) << 1)) * (16 / ES);
+                const int col = (c ^ (unit_swz<X>(k) << 1)) * (16 / ES);
                 off[q] = uint32_t(k) * ldb + (col < left ? col : 0) * ES;
             }
         }
@@ -141,7 +148,7 @@ struct Reader {
             at[0] = k * (X * 2) + (j % 4) * 8;
             at[1] = at[0] + 32 * (X * 2);
             unit = x0 / 16;
-            f = unit_swz(k);
+            f = unit_swz<X>(k);
         }
     }
     template <class V>
@@ -173,29 +180,55 @@ struct Tile {
     static_assert(FH * 32 == TM && FN * 16 == TN && FN % 2 == 0, "fragments");
 };
 
+// (row tile, column tile) of tile number `tile`: groups of kGroupM row tiles, columns slowest
+__device__ __forceinline__ int2 tile_origin(int tile, int m_tiles, int n_tiles) {
+    const int grp = tile / (kGroupM * n_tiles), in = tile % (kGroupM * n_tiles);
+    const int gm = min(kGroupM, m_tiles - grp * kGroupM);
+    return make_int2(grp * kGroupM + in % gm, in / gm);
+}
+
+// The sums of fragment row i of a wave: lane: row m, columns nb + 16 j .. + 3
+template <int EPI, int FN, class Acc>
+__device__ __forceinline__ void finish_row(const Product& p, int64_t m, int nb, const Acc (&v)[FN]) {
+    if (m >= p.M) return;
+#pragma unroll
+    for (int j = 0; j < FN; j += EPI == kGate || EPI == kGate8 ? 2 : 1) {
+        const int n = nb + j * 16;
+        if (n >= p.N) continue;
+        if constexpr (EPI == kGate) finish_gate(p, m, n, v[j], v[j + 1]);
+        else if constexpr (EPI == kGate8) finish_gate8(p, m, n, v[j], v[j + 1]);
+        else if constexpr (EPI == kStore) finish_store(p, m, n, v[j]);
+        else if constexpr (EPI == kScale) finish_scale(p, m, n, v[j]);
+        else finish_dgate(p, m, n, v[j]);
+    }
+}
+
 template <int TYPE, int LAYOUT, int EPI, class C>
 __global__ void __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::kWavesPerSimd)))
-k_mma(const Product p, int m_tiles, int n_tiles) {
+k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
     typedef typename Frag<TYPE>::V V;
     typedef typename Frag<TYPE>::Acc Acc;
     constexpr int ES = Frag<TYPE>::ES, KS = kSlice / ES;
     constexpr bool AKC = LAYOUT != kTN, BKC = LAYOUT == kNT;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     // tile of this workgroup
-    const int total = m_tiles * n_tiles, per = (total + kXcds - 1) / kXcds;
+    const int tiles = m_tiles * n_tiles, total = tiles * splits, per = (total + kXcds - 1) / kXcds;
     const int lid = int(blockIdx.x % kXcds) * per + int(blockIdx.x / kXcds);
     if (int(blockIdx.x / kXcds) >= per || lid >= total) return;
-    const int grp = lid / (kGroupM * n_tiles), in = lid % (kGroupM * n_tiles);
-    const int gm = min(kGroupM, m_tiles - grp * kGroupM);
-    const int64_t m0 = int64_t(grp * kGroupM + in % gm) * C::BM;
-    const int n0 = in / gm * C::BN;
+    const int split = lid / tiles, tile = lid % tiles;
+    const int2 mn = tile_origin(tile, m_tiles, n_tiles);
+    const int64_t m0 = int64_t(mn.x) * C::BM;
+    const int n0 = mn.y * C::BN;
+    // this workgroup's slices: [first, first + nk)
+    const int all = (p.K + KS - 1) / KS, share = (all + splits - 1) / splits;
+    const int first = split * share, nk = min(share, all - first);
 
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const int wm = wave / C::WN, wn = wave % C::WN;
     Side<C::BM, AKC, ES, C::NW> sa;
     Side<C::BN, BKC, ES, C::NW> sb;
-    sa.init(p.a, p.lda, m0, p.M);
-    sb.init(p.b, p.ldb, n0, p.N);
+    sa.init(p.a, p.lda, m0, p.M, first);
+    sb.init(p.b, p.ldb, n0, p.N, first);
     Reader<C::BM, AKC> ra;
     Reader<C::BN, BKC> rb;
     ra.init(wm * C::TM);
@@ -245,10 +278,9 @@ k_mma(const Product p, int m_tiles, int n_tiles) {
     typedef std::integral_constant<int, RA> NA;
     typedef std::integral_constant<int, RA + RB> NAB;
 
-    const int nk = (p.K + KS - 1) / KS;
     auto issue = [&](int ks) {
         uint8_t* st = lds + (ks & 1) * C::STAGE;
-        const int left = p.K - ks * KS;
+        const int left = p.K - (first + ks) * KS;
         sa.issue(st, left);
         sb.issue(st + C::BM * kSlice, left);
     };
@@ -284,49 +316,93 @@ k_mma(const Product p, int m_tiles, int n_tiles) {
         mul(Q3{});
     }
 
-    // lane: row m0 + wm TM + 16 i + lane % 16, columns n0 + wn TN + 16 j + 4 (lane / 16) .. + 3
+    if (splits > 1) {
+        // partial sums, [split][tile][fragment][thread]
+        Acc* part = static_cast<Acc*>(p.part) + int64_t(lid) * (C::FM * C::FN * C::kThreads) + threadIdx.x;
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i) {
-        const int64_t m = m0 + wm * C::TM + i * 16 + lane % 16;
-        if (m >= p.M) continue;
-        const int nb = n0 + wn * C::TN + 4 * (lane / 16);
-        if constexpr (EPI == kGate || EPI == kGate8) {
+        for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-            for (int j = 0; j < C::FN; j += 2) {
-                if (nb + j * 16 >= p.N) continue;
-                if constexpr (EPI == kGate) finish_gate(p, m, nb + j * 16, acc[i][j], acc[i][j + 1]);
-                else finish_gate8(p, m, nb + j * 16, acc[i][j], acc[i][j + 1]);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < C::FN; ++j) {
-                if (nb + j * 16 >= p.N) continue;
-                if constexpr (EPI == kStore) finish_store(p, m, nb + j * 16, acc[i][j]);
-                else if constexpr (EPI == kScale) finish_scale(p, m, nb + j * 16, acc[i][j]);
-                else finish_dgate(p, m, nb + j * 16, acc[i][j]);
-            }
-        }
+            for (int j = 0; j < C::FN; ++j) part[(i * C::FN + j) * C::kThreads] = acc[i][j];
+        return;
     }
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+        finish_row<EPI>(p, m0 + wm * C::TM + i * 16 + lane % 16, n0 + wn * C::TN + 4 * (lane / 16), acc[i]);
+}
+
+// Adds the splits' partial sums, in order, and finishes: workgroup (tile, fragment row i), the
+// threads as in k_mma.
+template <int TYPE, int EPI, class C>
+__global__ void __launch_bounds__(C::kThreads) k_join(const Product p, int m_tiles, int n_tiles, int splits) {
+    typedef typename Frag<TYPE>::Acc Acc;
+    const int tiles = m_tiles * n_tiles, tile = blockIdx.x, i = blockIdx.y;
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, wm = wave / C::WN, wn = wave % C::WN;
+    const int2 mn = tile_origin(tile, m_tiles, n_tiles);
+    const int64_t m = int64_t(mn.x) * C::BM + wm * C::TM + i * 16 + lane % 16;
+    if (m >= p.M) return;
+    constexpr int64_t kTileAcc = C::FM * C::FN * C::kThreads;
+    const Acc* part = static_cast<const Acc*>(p.part) + int64_t(tile) * kTileAcc + i * C::FN * C::kThreads + threadIdx.x;
+    Acc acc[C::FN];
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) acc[j] = part[j * C::kThreads];
+    for (int s = 1; s < splits; ++s)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) acc[j] += part[int64_t(s) * tiles * kTileAcc + j * C::kThreads];
+    finish_row<EPI>(p, m, mn.y * C::BN + wn * C::TN + 4 * (lane / 16), acc);
 }
 
 typedef Tile<256, 256, 2, 4> Big;
+typedef Tile<128, 128, 2, 2> Mid;
+typedef Tile<64, 64, 2, 2> Small;
 
 template <int TYPE, int LAYOUT, int EPI, class C>
-hipError_t launch(const Product& p, hipStream_t s) {
+hipError_t launch(const Product& p, int splits, hipStream_t s) {
     const int64_t mt = (p.M + C::BM - 1) / C::BM, nt = (p.N + C::BN - 1) / C::BN;
-    if (mt * nt > 0x7FFFFFF0 / kXcds) return hipErrorInvalidValue;
+    if (mt * nt * splits > 0x7FFFFFF0 / kXcds) return hipErrorInvalidValue;
+    if (splits > 1 && mt * nt * splits * C::BM * C::BN * 4 > p.part_bytes) return hipErrorInvalidValue;
     static const hipError_t lds_ok = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_mma<TYPE, LAYOUT, EPI, C>),
                                                          hipFuncAttributeMaxDynamicSharedMemorySize, C::kLdsBytes);
     if (lds_ok != hipSuccess) return lds_ok;
-    const int64_t grid = (mt * nt + kXcds - 1) / kXcds * kXcds;
+    const int64_t grid = (mt * nt * splits + kXcds - 1) / kXcds * kXcds;
     hipLaunchKernelGGL((k_mma<TYPE, LAYOUT, EPI, C>), dim3(unsigned(grid)), dim3(C::kThreads), C::kLdsBytes, s, p,
-                       int(mt), int(nt));
+                       int(mt), int(nt), splits);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || splits == 1) return e;
+    hipLaunchKernelGGL((k_join<TYPE, EPI, C>), dim3(unsigned(mt * nt), C::FM), dim3(C::kThreads), 0, s, p, int(mt), int(nt),
+                       splits);
     return hipGetLastError();
+}
+
+// Tile and split of K.  Times in units of one 256 x 256 slice on one CU.
+struct Choice {
+    int tile, splits;
+};
+Choice plan(const Product& p, int es, int64_t n_cu) {
+    struct { int bm, bn, slots; double slice, start; } const kinds[] = {
+        {256, 256, 1, 1.0, 4.0}, {128, 128, 2, 0.7, 3.0}, {64, 64, 4, 0.6, 3.0}};
+    const int64_t nk = (int64_t(p.K) * es + kSlice - 1) / kSlice;
+    Choice best{0, 1};
+    double best_t = 1e30;
+    for (int c = 0; c < 3; ++c) {
+        const int64_t tiles = (p.M + kinds[c].bm - 1) / kinds[c].bm * ((p.N + kinds[c].bn - 1) / kinds[c].bn);
+        for (int sp = 1; sp <= 32 && sp * 4 <= (nk > 4 ? nk : 4); sp *= 2) {
+            if (sp > 1 && tiles * sp * kinds[c].bm * kinds[c].bn * 4 > p.part_bytes) break;
+            const int64_t share = (nk + sp - 1) / sp;
+            if (share * (sp - 1) >= nk) break;               // every split has slices
+            const int64_t slots = n_cu * kinds[c].slots, rounds = (tiles * sp + slots - 1) / slots;
+            const double t = rounds * (share * kinds[c].slice + kinds[c].start) + (sp > 1 ? 6.0 + 0.25 * sp : 0.0);
+            if (t < best_t) best_t = t, best = Choice{c, sp};
+        }
+    }
+    return best;
 }
 
 template <int TYPE, int LAYOUT, int EPI>
 hipError_t choose(const Product& p, hipStream_t s) {
-    return launch<TYPE, LAYOUT, EPI, Big>(p, s);
+    const Choice c = plan(p, Frag<TYPE>::ES, compute_units());
+    if (c.tile == 0) return launch<TYPE, LAYOUT, EPI, Big>(p, c.splits, s);
+    if (c.tile == 1) return launch<TYPE, LAYOUT, EPI, Mid>(p, c.splits, s);
+    return launch<TYPE, LAYOUT, EPI, Small>(p, c.splits, s);
 }
 
 }  // namespace
