@@ -17,16 +17,28 @@ __device__ __forceinline__ void store4(float* p, float a, float b, float c, floa
     *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
 }
 
-// The sigmoid and silu of the bf16 kernels: hardware exp2 and reciprocal (about one fp32 step
-// each; the results are rounded to bf16, 2^16 times coarser).  e^-z overflows to infinity for
-// very negative z, whose reciprocal is 0.
-__device__ __forceinline__ float sigmoid_fast(float z) {
+__device__ __forceinline__ void load4(float (&v)[4], const uint16_t* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    v[0] = dev::bf16_lo(u.x), v[1] = dev::bf16_hi(u.x), v[2] = dev::bf16_lo(u.y), v[3] = dev::bf16_hi(u.y);
+}
+__device__ __forceinline__ void load4(float (&v)[4], const float* p) {
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+}
+
+// The sigmoid of the block's kernels.  fp32: expf and a division.  bf16: hardware exp2 and
+// reciprocal (about one fp32 step each; the results are rounded to bf16, 2^16 times coarser).
+// Either way e^-z overflows to infinity for very negative z, whose reciprocal is 0.
+template <int TYPE>
+__device__ __forceinline__ float sigmoid_of(float z) {
+    if constexpr (TYPE == kF32) return sigmoid(z);
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
 }
 
 // kStore: out[m][n .. n + 3]
+template <int TYPE>
 __device__ __forceinline__ void finish_store(const Product& p, int64_t m, int n, const dev::f32x4& v) {
-    store4(static_cast<uint16_t*>(p.out) + m * p.ldo + n, v[0], v[1], v[2], v[3]);
+    store4(static_cast<typename Elem<TYPE>::T*>(p.out) + m * p.ldo + n, v[0], v[1], v[2], v[3]);
 }
 
 // kScale: out[m][n .. n + 3] = sums * row scale * column scales; any N, any alignment
@@ -50,16 +62,18 @@ __device__ __forceinline__ void finish_scale(const Product& p, int64_t m, int n,
 }
 
 // kGate: n is the gate column (n % 32 < 16), inner index n / 32 * 16 + n % 16
+template <int TYPE>
 __device__ __forceinline__ void finish_gate(const Product& p, int64_t m, int n, const dev::f32x4& g, const dev::f32x4& u) {
+    typedef typename Elem<TYPE>::T E;
     if (p.gu) {
-        uint16_t* s = static_cast<uint16_t*>(p.gu) + m * p.N + n;
+        E* s = static_cast<E*>(p.gu) + m * p.N + n;
         store4(s, g[0], g[1], g[2], g[3]);
         store4(s + 16, u[0], u[1], u[2], u[3]);
     }
     float h[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = g[j] * sigmoid_fast(g[j]) * u[j];
-    store4(static_cast<uint16_t*>(p.out) + m * p.ldo + n / 32 * 16 + n % 16, h[0], h[1], h[2], h[3]);
+    for (int j = 0; j < 4; ++j) h[j] = g[j] * sigmoid_of<TYPE>(g[j]) * u[j];
+    store4(static_cast<E*>(p.out) + m * p.ldo + n / 32 * 16 + n % 16, h[0], h[1], h[2], h[3]);
 }
 
 // kGate8: the same from integer sums, in fp32 with the full-precision silu (h's codes are
@@ -76,20 +90,20 @@ __device__ __forceinline__ void finish_gate8(const Product& p, int64_t m, int n,
 }
 
 // kDGate: v = dh[m][n .. n + 3], n an inner index
+template <int TYPE>
 __device__ __forceinline__ void finish_dgate(const Product& p, int64_t m, int n, const dev::f32x4& v) {
+    typedef typename Elem<TYPE>::T E;
     const int64_t o = m * 2 * p.N + n / 16 * 32 + n % 16;
-    const uint16_t* gu = static_cast<const uint16_t*>(p.gu) + o;
-    const uint2 gb = *reinterpret_cast<const uint2*>(gu), ub = *reinterpret_cast<const uint2*>(gu + 16);
-    const float g[4] = {dev::bf16_lo(gb.x), dev::bf16_hi(gb.x), dev::bf16_lo(gb.y), dev::bf16_hi(gb.y)};
-    const float u[4] = {dev::bf16_lo(ub.x), dev::bf16_hi(ub.x), dev::bf16_lo(ub.y), dev::bf16_hi(ub.y)};
-    float dg[4], du[4];
+    float g[4], u[4], dg[4], du[4];
+    load4(g, static_cast<const E*>(p.gu) + o);
+    load4(u, static_cast<const E*>(p.gu) + o + 16);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float s = sigmoid_fast(g[j]);
+        const float s = sigmoid_of<TYPE>(g[j]);
         dg[j] = v[j] * u[j] * silu_grad(g[j], s);
         du[j] = v[j] * g[j] * s;
     }
-    uint16_t* d = static_cast<uint16_t*>(p.out) + o;
+    E* d = static_cast<E*>(p.out) + o;
     store4(d, dg[0], dg[1], dg[2], dg[3]);
     store4(d + 16, du[0], du[1], du[2], du[3]);
 }

@@ -47,6 +47,12 @@ constexpr int kCodePad = 16;             // bytes between the code rows: other b
 __device__ __forceinline__ dev::f32x4 mma(const dev::u32x4& a, const dev::u32x4& b, const dev::f32x4& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
+__device__ __forceinline__ dev::f32x4 mma_f32(const dev::u32x4& a, const dev::u32x4& b, dev::f32x4 c) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[q]), __uint_as_float(b[q]), c, 0, 0, 0);
+    return c;
+}
 __device__ __forceinline__ i32x4 mma(const dev::u32x4& a, const dev::u32x4& b, const i32x4& c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
@@ -75,7 +81,7 @@ __device__ __forceinline__ void lds_barrier() {
 template <int TYPE, int EPI, int MT, int R, int QUANT, bool WALK, bool ONE>
 __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) {
     typedef typename FewAcc<TYPE>::T Acc;
-    constexpr int ES = TYPE == kI8 ? 1 : 2;
+    constexpr int ES = TYPE == kI8 ? 1 : TYPE == kBF16 ? 2 : 4;
     constexpr bool GATE = EPI == kGate || EPI == kGate8;
     static_assert(!GATE || R == 2, "gate and up tiles");
     static_assert(WALK || !ONE, "x is kept for the groups of a walk");
@@ -215,7 +221,10 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int r = 0; r < R; ++r) acc[m][r] = mma(w[d][r], x[d][m], acc[m][r]);
+                    for (int r = 0; r < R; ++r) {
+                        if constexpr (TYPE == kF32) acc[m][r] = mma_f32(w[d][r], x[d][m], acc[m][r]);
+                        else acc[m][r] = mma(w[d][r], x[d][m], acc[m][r]);
+                    }
             s += kStride * kDepth;
             if (ONE || s >= kb) break;
             load_w(g, s);
@@ -246,9 +255,9 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
             const int t = m * 8 + ent % 8;
             const int64_t n = n0 + r * 8 + 4 * (ent / 8);
             if (t >= T || n >= p.N) continue;
-            if constexpr (EPI == kGate) finish_gate(p, t, int(n), sum[0], sum[PER - 1]);
+            if constexpr (EPI == kGate) finish_gate<TYPE>(p, t, int(n), sum[0], sum[PER - 1]);
             else if constexpr (EPI == kGate8) finish_gate8(p, t, int(n), sum[0], sum[PER - 1]);
-            else if constexpr (EPI == kStore) finish_store(p, t, int(n), sum[0]);
+            else if constexpr (EPI == kStore) finish_store<TYPE>(p, t, int(n), sum[0]);
             else finish_scale(p, t, int(n), sum[0]);
         }
         if (!WALK) break;
@@ -269,7 +278,7 @@ hipError_t launch_few_as(const Product& p, hipStream_t s) {
         // up to four workgroups a CU, each the same number of groups
         const int64_t most = int64_t(compute_units()) * 4, turns = (groups + most - 1) / most;
         const dim3 grid(unsigned((groups + turns - 1) / turns));
-        if (p.K * (TYPE == kI8 ? 1 : 2) <= kWaves * kSlice * kDepth)
+        if (p.K * (TYPE == kI8 ? 1 : TYPE == kBF16 ? 2 : 4) <= kWaves * kSlice * kDepth)
             hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, true, true>), grid, dim3(kThreads), lds, s, p, int(groups));
         else
             hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, true, false>), grid, dim3(kThreads), lds, s, p, int(groups));
@@ -306,6 +315,9 @@ hipError_t launch_few(int type, int epi, const Product& p, hipStream_t s, int x_
     } else if (type == kBF16) {
         if (epi == kStore) return choose_few<kBF16, kStore>(p, q, s);
         if (epi == kGate) return choose_few<kBF16, kGate>(p, q, s);
+    } else {
+        if (epi == kStore) return choose_few<kF32, kStore>(p, q, s);
+        if (epi == kGate) return choose_few<kF32, kGate>(p, q, s);
     }
     return hipErrorInvalidValue;
 }

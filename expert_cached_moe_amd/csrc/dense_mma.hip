@@ -1,9 +1,11 @@
-// Products of the dense operators on the matrix cores: bf16 and 8-bit integers.
+// Products of the dense operators on the matrix cores: fp32, bf16 and 8-bit integers.
 //
-// C[m][n] = sum_k A(m, k) B(n, k) in tiles of BM x BN.  One K slice is 128 bytes of K (64 bf16
-// or 128 codes), so a row segment of an operand that is contiguous along K is one cache line and
-// both types move the same bytes per slice; the 16x16 matrix instructions take 16 bytes a lane
-// from each operand (32 bf16 or 64 codes of K) in the same time.  Slices are loaded straight
+// C[m][n] = sum_k A(m, k) B(n, k) in tiles of BM x BN.  One K slice is 128 bytes of K (32 fp32,
+// 64 bf16 or 128 codes), so a row segment of an operand that is contiguous along K is one cache
+// line and all types move the same bytes per slice; a fragment is 16 bytes a lane from each
+// operand: one 16x16 matrix instruction for bf16 (32 k) and for codes (64 k) in the same time,
+// four for fp32 (4 k each; which k an instruction takes does not matter while both operands
+// agree), eight times as long.  Slices are loaded straight
 // into two LDS stages by buffer loads; the one barrier of a slice stands before its last quarter,
 // so the loads of a slice have a whole slice's time to land and the matrix instructions of the
 // last quarter cover the first reads of the next slice.
@@ -13,7 +15,9 @@
 // fragment read fall on different banks.  Operands contiguous along the other dimension (the
 // gradients' products) lie as rows of one k; their fragments are read with the transposing LDS
 // read, 4 k of 16 columns a group of 16 lanes, and the 32-byte units of row k are permuted by
-// bits 0, 1 and 3 of k, so the 8 rows that 32 lanes read fall on different banks.
+// bits 0, 1 and 3 of k, so the 8 rows that 32 lanes read fall on different banks.  fp32 reads them
+// 4 bytes a lane instead, 16 columns of one k a group of 16 lanes, 64-byte units permuted by
+// bits 2 and 3 of k.
 //
 // The weights' operand goes first into the instruction, so a lane ends with four consecutive
 // columns of one row: gate and up sums of an inner index are in one lane, and results leave as
@@ -56,6 +60,16 @@ template <> struct Frag<kI8> {
     typedef i32x4 Acc;
     static constexpr int ES = 1;
 };
+template <> struct Frag<kF32> {
+    typedef dev::f32x4 V;
+    typedef dev::f32x4 Acc;
+    static constexpr int ES = 4;
+};
+__device__ __forceinline__ dev::f32x4 mma(const dev::f32x4& a, const dev::f32x4& b, dev::f32x4 c) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[q], b[q], c, 0, 0, 0);
+    return c;
+}
 __device__ __forceinline__ dev::f32x4 mma(const bf16x8& a, const bf16x8& b, const dev::f32x4& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
@@ -66,9 +80,10 @@ __device__ __forceinline__ i32x4 mma(const i32x4& a, const i32x4& b, const i32x4
 // permutation of the 32-byte units of row k of an operand that is not contiguous along K: rows
 // of 256 bytes and more all start on the same bank and have 8 units to permute; rows of 128
 // bytes (X = 64) alternate between the halves of the banks and have 4
-template <int X>
-__device__ __forceinline__ int unit_swz(int k) {
-    return X == 64 ? ((k >> 1) & 1) | ((k >> 2) & 2) : (k & 3) | ((k >> 1) & 4);
+template <int X, int ES>
+__device__ __forceinline__ int chunk_swz(int k) {         // for 16-byte chunks
+    if (ES == 4) return ((k >> 2) & 3) << 2;
+    return (X == 64 ? ((k >> 1) & 1) | ((k >> 2) & 2) : (k & 3) | ((k >> 1) & 4)) << 1;
 }
 
 // One operand's tile: X rows (tokens or weights) by one slice of K, X * 128 bytes in LDS.
@@ -78,7 +93,7 @@ struct Side {
     static constexpr int Q = X * kSlice / 1024 / NW;      // 1 KiB loads of a wave per slice
     static constexpr int KS = kSlice / ES;                // k in a slice
     static_assert(Q * NW * 1024 == X * kSlice, "loads split over the waves");
-    static_assert(KC || ES == 2, "transposing reads: 16-bit elements");
+    static_assert(KC || ES >= 2, "transposing reads: 16-bit elements; fp32 reads single values");
 
     const uint8_t* base;     // (uniform) first row / column of the tile at the next slice to load
     int64_t step;            // bytes from slice to slice
@@ -102,7 +117,7 @@ struct Side {
             } else {
                 constexpr int CPR = X * ES / 16;          // 16-byte chunks of a k row
                 const int k = (i * 64 + lane) / CPR, c = (i * 64 + lane) % CPR;
-                const int col = (c ^ (unit_swz<X>(k) << 1)) * (16 / ES);
+                const int col = (c ^ chunk_swz<X, ES>(k)) * (16 / ES);
                 off[q] = uint32_t(k) * ldb + (col < left ? col : 0) * ES;
             }
         }
@@ -133,34 +148,43 @@ struct Side {
 };
 
 // This lane's fragment reads of one operand: rows x0 + 16 i + lane % 16 of the tile.
-template <int X, bool KC>
+template <int X, bool KC, int ES>
 struct Reader {
     uint32_t at[2];          // KC: byte offset for half-slice 0 and 1
-    int unit, f;             // not KC: first 32-byte unit, its permutation
+    int unit, f;             // not KC: first 16-column unit, its permutation
     __device__ __forceinline__ void init(int x0) {
         const int lane = threadIdx.x % kWave, j = lane % 16, g = lane / 16;
         if constexpr (KC) {
             const int sw = (j >> 1) & 7;
             at[0] = (x0 + j) * kSlice + ((g ^ sw) << 4);
             at[1] = at[0] ^ 64;
-        } else {
-            const int k = 8 * g + j / 4;
+        } else if constexpr (ES == 2) {
+            const int k = 8 * g + j / 4;                      // + 4 for the second read
             at[0] = k * (X * 2) + (j % 4) * 8;
             at[1] = at[0] + 32 * (X * 2);
             unit = x0 / 16;
-            f = unit_swz<X>(k);
+            f = chunk_swz<X, ES>(k) >> 1;
+        } else {
+            const int k = 4 * g;                              // + 0 .. 3
+            at[0] = k * (X * 4) + j * 4;
+            at[1] = at[0] + 16 * (X * 4);
+            unit = x0 / 16;
+            f = chunk_swz<X, ES>(k) >> 2;
         }
     }
     template <class V>
     __device__ __forceinline__ V read(const uint8_t* lds, int half, int i) const {
         if constexpr (KC) {
             return *reinterpret_cast<const V*>(lds + at[half] + i * 16 * kSlice);
-        } else {
+        } else if constexpr (ES == 2) {
             const uint8_t* p = lds + at[half] + (((unit + i) ^ f) << 5);
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
             const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * X * 2));
             typedef __attribute__((ext_vector_type(8))) short s16x8;
             return __builtin_bit_cast(V, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            const float* p = reinterpret_cast<const float*>(lds + at[half] + (((unit + i) ^ f) << 6));
+            return V{p[0], p[X], p[2 * X], p[3 * X]};
         }
     }
 };
@@ -188,18 +212,18 @@ __device__ __forceinline__ int2 tile_origin(int tile, int m_tiles, int n_tiles) 
 }
 
 // The sums of fragment row i of a wave: lane: row m, columns nb + 16 j .. + 3
-template <int EPI, int FN, class Acc>
+template <int TYPE, int EPI, int FN, class Acc>
 __device__ __forceinline__ void finish_row(const Product& p, int64_t m, int nb, const Acc (&v)[FN]) {
     if (m >= p.M) return;
 #pragma unroll
     for (int j = 0; j < FN; j += EPI == kGate || EPI == kGate8 ? 2 : 1) {
         const int n = nb + j * 16;
         if (n >= p.N) continue;
-        if constexpr (EPI == kGate) finish_gate(p, m, n, v[j], v[j + 1]);
+        if constexpr (EPI == kGate) finish_gate<TYPE>(p, m, n, v[j], v[j + 1]);
         else if constexpr (EPI == kGate8) finish_gate8(p, m, n, v[j], v[j + 1]);
-        else if constexpr (EPI == kStore) finish_store(p, m, n, v[j]);
+        else if constexpr (EPI == kStore) finish_store<TYPE>(p, m, n, v[j]);
         else if constexpr (EPI == kScale) finish_scale(p, m, n, v[j]);
-        else finish_dgate(p, m, n, v[j]);
+        else finish_dgate<TYPE>(p, m, n, v[j]);
     }
 }
 
@@ -229,8 +253,8 @@ k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
     Side<C::BN, BKC, ES, C::NW> sb;
     sa.init(p.a, p.lda, m0, p.M, first);
     sb.init(p.b, p.ldb, n0, p.N, first);
-    Reader<C::BM, AKC> ra;
-    Reader<C::BN, BKC> rb;
+    Reader<C::BM, AKC, ES> ra;
+    Reader<C::BN, BKC, ES> rb;
     ra.init(wm * C::TM);
     rb.init(wn * C::TN);
 
@@ -261,7 +285,7 @@ k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
     };
     // matrix instructions of one quarter with the NR LDS reads of the next spread among them
     auto sched = [&](auto nr_) {
-        constexpr int NR = decltype(nr_)::value, NM = C::FH * C::FN;
+        constexpr int NR = decltype(nr_)::value, NM = C::FH * C::FN * (TYPE == kF32 ? 4 : 1);
         constexpr int PAIRS = NR < NM ? NR : NM;
 #pragma unroll
         for (int n = 0; n < PAIRS; ++n) {
@@ -274,7 +298,7 @@ k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
     typedef std::integral_constant<int, 1> Q1;
     typedef std::integral_constant<int, 2> Q2;
     typedef std::integral_constant<int, 3> Q3;
-    constexpr int RA = C::FH * (AKC ? 1 : 2), RB = C::FN * (BKC ? 1 : 2);
+    constexpr int RA = C::FH * (AKC ? 1 : ES), RB = C::FN * (BKC ? 1 : ES);     // LDS reads
     typedef std::integral_constant<int, RA> NA;
     typedef std::integral_constant<int, RA + RB> NAB;
 
@@ -327,7 +351,7 @@ k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
     }
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
-        finish_row<EPI>(p, m0 + wm * C::TM + i * 16 + lane % 16, n0 + wn * C::TN + 4 * (lane / 16), acc[i]);
+        finish_row<TYPE, EPI>(p, m0 + wm * C::TM + i * 16 + lane % 16, n0 + wn * C::TN + 4 * (lane / 16), acc[i]);
 }
 
 // Adds the splits' partial sums, in order, and finishes: workgroup (tile, fragment row i), the
@@ -348,7 +372,7 @@ __global__ void __launch_bounds__(C::kThreads) k_join(const Product p, int m_til
     for (int s = 1; s < splits; ++s)
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) acc[j] += part[int64_t(s) * tiles * kTileAcc + j * C::kThreads];
-    finish_row<EPI>(p, m, mn.y * C::BN + wn * C::TN + 4 * (lane / 16), acc);
+    finish_row<TYPE, EPI>(p, m, mn.y * C::BN + wn * C::TN + 4 * (lane / 16), acc);
 }
 
 typedef Tile<256, 256, 2, 4> Big;
@@ -379,7 +403,7 @@ struct Choice {
 };
 Choice plan(const Product& p, int es, int64_t n_cu) {
     struct { int bm, bn, slots; double slice, start; } const kinds[] = {
-        {256, 256, 1, 1.0, 4.0}, {128, 128, 2, 0.7, 3.0}, {64, 64, 4, 0.6, 3.0}};
+        {256, 256, 1, es == 4 ? 8.5 : 1.0, 4.0}, {128, 128, 2, es == 4 ? 4.4 : 0.7, 3.0}, {64, 64, 4, es == 4 ? 2.4 : 0.6, 3.0}};
     const int64_t nk = (int64_t(p.K) * es + kSlice - 1) / kSlice;
     Choice best{0, 1};
     double best_t = 1e30;
@@ -407,17 +431,20 @@ hipError_t choose(const Product& p, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_mma(int type, int layout, int epi, const Product& p, hipStream_t s) {
+hipError_t launch_product(int type, int layout, int epi, const Product& p, hipStream_t s) {
+    if (p.M <= 0 || p.N <= 0) return hipSuccess;
+    if (layout == kNT && few_tokens(p, type == kI8 ? 1 : type == kBF16 ? 2 : 4)) return launch_few(type, epi, p, s);
     if (type == kI8) {
         if (layout == kNT && epi == kScale) return choose<kI8, kNT, kScale>(p, s);
         if (layout == kNT && epi == kGate8) return choose<kI8, kNT, kGate8>(p, s);
-    } else if (type == kBF16) {
-        if (layout == kNT && epi == kStore) return choose<kBF16, kNT, kStore>(p, s);
-        if (layout == kNT && epi == kGate) return choose<kBF16, kNT, kGate>(p, s);
-        if (layout == kNN && epi == kStore) return choose<kBF16, kNN, kStore>(p, s);
-        if (layout == kNN && epi == kDGate) return choose<kBF16, kNN, kDGate>(p, s);
-        if (layout == kTN && epi == kStore) return choose<kBF16, kTN, kStore>(p, s);
+        return hipErrorInvalidValue;
     }
+    const bool f32 = type == kF32;
+    if (layout == kNT && epi == kStore) return f32 ? choose<kF32, kNT, kStore>(p, s) : choose<kBF16, kNT, kStore>(p, s);
+    if (layout == kNT && epi == kGate) return f32 ? choose<kF32, kNT, kGate>(p, s) : choose<kBF16, kNT, kGate>(p, s);
+    if (layout == kNN && epi == kStore) return f32 ? choose<kF32, kNN, kStore>(p, s) : choose<kBF16, kNN, kStore>(p, s);
+    if (layout == kNN && epi == kDGate) return f32 ? choose<kF32, kNN, kDGate>(p, s) : choose<kBF16, kNN, kDGate>(p, s);
+    if (layout == kTN && epi == kStore) return f32 ? choose<kF32, kTN, kStore>(p, s) : choose<kBF16, kTN, kStore>(p, s);
     return hipErrorInvalidValue;
 }
 
