@@ -170,7 +170,7 @@ int moe_i8_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, c
     p.out = d_y;
     p.ldo = ld_y;
     p.out_f32 = y_type == MOE_A_F32;
-    p.vec_out = aligned(d_y, p.out_f32 ? 16 : 8) && ld_y % 4 == 0;
+    p.vec_out = aligned(d_y, 16) && ld_y % 8 == 0;
     p.col_scale = d_w_scale;
     hipError_t e = on_the_way ? launch_few(kI8, kScale, p, s, x_type, true) : launch_product(kI8, kNT, kScale, p, s);
     return e == hipSuccess ? MOE_OK : hip_fail(ctx, e, "moe_i8_matmul launch");

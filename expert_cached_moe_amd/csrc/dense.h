@@ -36,7 +36,7 @@ struct Product {
     void* out;
     int64_t ldo;                // elements between rows of out
     int32_t out_f32;            // kScale: out is fp32 (else bf16)
-    int32_t vec_out;            // kScale: rows of out are aligned for stores of four values
+    int32_t vec_out;            // kScale: out and its rows are 16-byte aligned for 8 values
     const float* row_scale;     // kScale, kGate8
     const float* col_scale;
     void* part;                 // scratch for partial sums of part_bytes (0: none)

@@ -1,5 +1,5 @@
-// The last steps of a product on four sums of consecutive columns of one row, shared by the
-// matrix-core kernels.  (kGate, kGate8: four gate sums and the four up sums 16 columns on.)
+// The last steps of a product on W (4 or 8) sums of consecutive columns of one row, shared by the
+// product kernels.  For the gated epilogues those are W gate sums, and W up sums 16 columns on.
 #pragma once
 
 #include "dense_common.h"
@@ -9,21 +9,47 @@ namespace dense {
 
 typedef __attribute__((ext_vector_type(4))) int i32x4;
 
-// 4 values to p[0..3] in bf16 or fp32; VEC: p is 8 (16) bytes aligned
-__device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(dev::pack_bf16x2(a, b), dev::pack_bf16x2(c, d));
+// W values to p[0 .. W-1], 4 (fp32) or W (bf16) at a time.  STREAM: past the caches, for results
+// that leave as whole lines and are not read by the next kernel.
+template <int W, bool STREAM = false>
+__device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[W]) {
+    if constexpr (W == 8) {
+        const dev::u32x4 u{dev::pack_bf16x2(v[0], v[1]), dev::pack_bf16x2(v[2], v[3]), dev::pack_bf16x2(v[4], v[5]),
+                           dev::pack_bf16x2(v[6], v[7])};
+        if (STREAM) __builtin_nontemporal_store(u, reinterpret_cast<dev::u32x4*>(p));
+        else *reinterpret_cast<dev::u32x4*>(p) = u;
+    } else
+        *reinterpret_cast<uint2*>(p) = make_uint2(dev::pack_bf16x2(v[0], v[1]), dev::pack_bf16x2(v[2], v[3]));
 }
-__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
-    *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+template <int W, bool STREAM = false>
+__device__ __forceinline__ void store_row(float* p, const float (&v)[W]) {
+#pragma unroll
+    for (int q = 0; q < W; q += 4) {
+        const dev::f32x4 u{v[q], v[q + 1], v[q + 2], v[q + 3]};
+        if (STREAM) __builtin_nontemporal_store(u, reinterpret_cast<dev::f32x4*>(p + q));
+        else *reinterpret_cast<dev::f32x4*>(p + q) = u;
+    }
 }
-
-__device__ __forceinline__ void load4(float (&v)[4], const uint16_t* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    v[0] = dev::bf16_lo(u.x), v[1] = dev::bf16_hi(u.x), v[2] = dev::bf16_lo(u.y), v[3] = dev::bf16_hi(u.y);
+template <int W>
+__device__ __forceinline__ void load_row(float (&v)[W], const uint16_t* p) {
+    uint32_t u[W / 2];
+    if constexpr (W == 8) {
+        const uint4 q = *reinterpret_cast<const uint4*>(p);
+        u[0] = q.x, u[1] = q.y, u[2] = q.z, u[3] = q.w;
+    } else {
+        const uint2 q = *reinterpret_cast<const uint2*>(p);
+        u[0] = q.x, u[1] = q.y;
+    }
+#pragma unroll
+    for (int j = 0; j < W / 2; ++j) v[2 * j] = dev::bf16_lo(u[j]), v[2 * j + 1] = dev::bf16_hi(u[j]);
 }
-__device__ __forceinline__ void load4(float (&v)[4], const float* p) {
-    const float4 u = *reinterpret_cast<const float4*>(p);
-    v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+template <int W>
+__device__ __forceinline__ void load_row(float (&v)[W], const float* p) {
+#pragma unroll
+    for (int q = 0; q < W; q += 4) {
+        const float4 u = *reinterpret_cast<const float4*>(p + q);
+        v[q] = u.x, v[q + 1] = u.y, v[q + 2] = u.z, v[q + 3] = u.w;
+    }
 }
 
 // The sigmoid of the block's kernels.  fp32: expf and a division.  bf16: hardware exp2 and
@@ -35,78 +61,103 @@ __device__ __forceinline__ float sigmoid_of(float z) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
 }
 
-// kStore: out[m][n .. n + 3]
-template <int TYPE>
-__device__ __forceinline__ void finish_store(const Product& p, int64_t m, int n, const dev::f32x4& v) {
-    store4(static_cast<typename Elem<TYPE>::T*>(p.out) + m * p.ldo + n, v[0], v[1], v[2], v[3]);
-}
-
-// kScale: out[m][n .. n + 3] = sums * row scale * column scales; any N, any alignment
-__device__ __forceinline__ void finish_scale(const Product& p, int64_t m, int n, const i32x4& v) {
-    const float rs = p.row_scale[m];
-    float f[4];
+// Scales of the columns a lane finishes (and of the up columns): loaded once, used for every row.
+template <int EPI, int W>
+struct ColumnScales {
+    float s[EPI == kScale || EPI == kGate8 ? W : 1], up[EPI == kGate8 ? W : 1];
+    __device__ __forceinline__ void load(const Product& p, int n) {
+        if constexpr (EPI == kScale || EPI == kGate8) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = float(v[j]) * rs * p.col_scale[n + j < p.N ? n + j : p.N - 1];
-    const int64_t o = m * p.ldo + n;
-    if (p.vec_out && n + 4 <= p.N) {
-        if (p.out_f32) store4(static_cast<float*>(p.out) + o, f[0], f[1], f[2], f[3]);
-        else store4(static_cast<uint16_t*>(p.out) + o, f[0], f[1], f[2], f[3]);
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (n + j < p.N) {
-            if (p.out_f32) put(static_cast<float*>(p.out) + o + j, f[j]);
-            else put(static_cast<uint16_t*>(p.out) + o + j, f[j]);
+            for (int j = 0; j < W; ++j) s[j] = p.col_scale[n + j < p.N ? n + j : p.N - 1];
         }
-}
-
-// kGate: n is the gate column (n % 32 < 16), inner index n / 32 * 16 + n % 16
-template <int TYPE>
-__device__ __forceinline__ void finish_gate(const Product& p, int64_t m, int n, const dev::f32x4& g, const dev::f32x4& u) {
-    typedef typename Elem<TYPE>::T E;
-    if (p.gu) {
-        E* s = static_cast<E*>(p.gu) + m * p.N + n;
-        store4(s, g[0], g[1], g[2], g[3]);
-        store4(s + 16, u[0], u[1], u[2], u[3]);
+        if constexpr (EPI == kGate8) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) up[j] = p.col_scale[n + 16 + j < p.N ? n + 16 + j : p.N - 1];
+        }
     }
-    float h[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = g[j] * sigmoid_of<TYPE>(g[j]) * u[j];
-    store4(static_cast<E*>(p.out) + m * p.ldo + n / 32 * 16 + n % 16, h[0], h[1], h[2], h[3]);
-}
+};
 
-// kGate8: the same from integer sums, in fp32 with the full-precision silu (h's codes are
-// decided on it)
-__device__ __forceinline__ void finish_gate8(const Product& p, int64_t m, int n, const i32x4& g, const i32x4& u) {
-    const float rs = p.row_scale[m];
-    const float4 gs = *reinterpret_cast<const float4*>(p.col_scale + n);
-    const float4 us = *reinterpret_cast<const float4*>(p.col_scale + n + 16);
-    const float gw[4] = {gs.x, gs.y, gs.z, gs.w}, uw[4] = {us.x, us.y, us.z, us.w};
-    float h[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = silu(float(g[j]) * rs * gw[j]) * (float(u[j]) * rs * uw[j]);
-    store4(static_cast<float*>(p.out) + m * p.ldo + n / 32 * 16 + n % 16, h[0], h[1], h[2], h[3]);
-}
-
-// kDGate: v = dh[m][n .. n + 3], n an inner index
-template <int TYPE>
-__device__ __forceinline__ void finish_dgate(const Product& p, int64_t m, int n, const dev::f32x4& v) {
-    typedef typename Elem<TYPE>::T E;
-    const int64_t o = m * 2 * p.N + n / 16 * 32 + n % 16;
-    float g[4], u[4], dg[4], du[4];
-    load4(g, static_cast<const E*>(p.gu) + o);
-    load4(u, static_cast<const E*>(p.gu) + o + 16);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float s = sigmoid_of<TYPE>(g[j]);
-        dg[j] = v[j] * u[j] * silu_grad(g[j], s);
-        du[j] = v[j] * g[j] * s;
+// What finishing row m, columns n .. n + W - 1 reads: its row scale, or its gate and up values.
+// Loaded apart from the finishing, so that a kernel can have the next row's loads ahead of this
+// row's stores (a wait for a load waits for every older store).
+template <int TYPE, int EPI, int W>
+struct RowInputs {
+    float rs, g[EPI == kDGate ? W : 1], u[EPI == kDGate ? W : 1];
+    __device__ __forceinline__ void load(const Product& p, int64_t m, int n) {
+        if constexpr (EPI == kScale || EPI == kGate8) rs = p.row_scale[m];
+        if constexpr (EPI == kDGate) {
+            typedef typename Elem<TYPE>::T E;
+            const E* gu = static_cast<const E*>(p.gu) + m * 2 * p.N + n / 16 * 32 + n % 16;
+            load_row<W>(g, gu);
+            load_row<W>(u, gu + 16);
+        }
     }
-    E* d = static_cast<E*>(p.out) + o;
-    store4(d, dg[0], dg[1], dg[2], dg[3]);
-    store4(d + 16, du[0], du[1], du[2], du[3]);
+};
+
+// Row m, columns n .. n + W - 1 (v; the up sums in u).  n < N; only kScale may reach past N.
+template <int TYPE, int EPI, int W, class S>
+__device__ __forceinline__ void finish(const Product& p, int64_t m, int n, const S (&v)[W], const S (&u)[W],
+                                       const ColumnScales<EPI, W>& cs, const RowInputs<TYPE, EPI, W>& in) {
+    typedef typename Elem<TYPE>::T E;
+    if constexpr (EPI == kStore) {
+        float f[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) f[j] = float(v[j]);
+        store_row<W>(static_cast<E*>(p.out) + m * p.ldo + n, f);
+    } else if constexpr (EPI == kScale) {
+        float f[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) f[j] = float(v[j]) * in.rs * cs.s[j];
+        const int64_t o = m * p.ldo + n;
+        if (p.vec_out && n + W <= p.N) {
+            // (streamed: 8192 x 24576 x 4096 took 690 us against 752, since the results of all CUs,
+            // which leave at the same time, do not crowd the next tiles' operands out of L2)
+            if (p.out_f32) store_row<W, W == 8>(static_cast<float*>(p.out) + o, f);
+            else store_row<W, W == 8>(static_cast<uint16_t*>(p.out) + o, f);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if (n + j < p.N) {
+                if (p.out_f32) put(static_cast<float*>(p.out) + o + j, f[j]);
+                else put(static_cast<uint16_t*>(p.out) + o + j, f[j]);
+            }
+    } else if constexpr (EPI == kGate) {
+        // n is the gate column (n % 32 < 16) of inner index n / 32 * 16 + n % 16
+        float h[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) h[j] = v[j] * sigmoid_of<TYPE>(v[j]) * u[j];
+        if (p.gu) {
+            E* s = static_cast<E*>(p.gu) + m * p.N + n;
+            store_row<W>(s, v);
+            store_row<W>(s + 16, u);
+        }
+        store_row<W>(static_cast<E*>(p.out) + m * p.ldo + n / 32 * 16 + n % 16, h);
+    } else if constexpr (EPI == kGate8) {
+        // the same from integer sums, in fp32 with the full-precision silu (h's codes are decided
+        // on it)
+        float h[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) h[j] = silu(float(v[j]) * in.rs * cs.s[j]) * (float(u[j]) * in.rs * cs.up[j]);
+        store_row<W>(static_cast<float*>(p.out) + m * p.ldo + n / 32 * 16 + n % 16, h);
+    } else {
+        // v = dh, n an inner index
+        const int64_t o = m * 2 * p.N + n / 16 * 32 + n % 16;
+        float dg[W], du[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            const float s = sigmoid_of<TYPE>(in.g[j]);
+            dg[j] = v[j] * in.u[j] * silu_grad(in.g[j], s);
+            du[j] = v[j] * in.g[j] * s;
+        }
+        store_row<W>(static_cast<E*>(p.out) + o, dg);
+        store_row<W>(static_cast<E*>(p.out) + o + 16, du);
+    }
 }
+
+// Columns of one row that take part in W results: the gated epilogues pair two runs of 16.
+template <int EPI>
+constexpr bool kPaired = EPI == kGate || EPI == kGate8;
 
 }  // namespace dense
 }  // namespace moe

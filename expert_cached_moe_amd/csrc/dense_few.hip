@@ -82,7 +82,7 @@ template <int TYPE, int EPI, int MT, int R, int QUANT, bool WALK, bool ONE>
 __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) {
     typedef typename FewAcc<TYPE>::T Acc;
     constexpr int ES = TYPE == kI8 ? 1 : TYPE == kBF16 ? 2 : 4;
-    constexpr bool GATE = EPI == kGate || EPI == kGate8;
+    constexpr bool GATE = kPaired<EPI>;
     static_assert(!GATE || R == 2, "gate and up tiles");
     static_assert(WALK || !ONE, "x is kept for the groups of a walk");
     static_assert(QUANT == kNoQuant || MT == 1, "x quantised on the way: up to 8 tokens");
@@ -255,10 +255,14 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
             const int t = m * 8 + ent % 8;
             const int64_t n = n0 + r * 8 + 4 * (ent / 8);
             if (t >= T || n >= p.N) continue;
-            if constexpr (EPI == kGate) finish_gate<TYPE>(p, t, int(n), sum[0], sum[PER - 1]);
-            else if constexpr (EPI == kGate8) finish_gate8(p, t, int(n), sum[0], sum[PER - 1]);
-            else if constexpr (EPI == kStore) finish_store<TYPE>(p, t, int(n), sum[0]);
-            else finish_scale(p, t, int(n), sum[0]);
+            typename Elem<TYPE>::Acc v[4], u[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = sum[0][e], u[e] = sum[PER - 1][e];
+            ColumnScales<EPI, 4> cs;
+            cs.load(p, int(n));
+            RowInputs<TYPE, EPI, 4> in;
+            in.load(p, t, int(n));
+            finish<TYPE, EPI, 4>(p, t, int(n), v, u, cs, in);
         }
         if (!WALK) break;
         g = next;
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
 
 template <int TYPE, int EPI, int MT, int R, int QUANT>
 hipError_t launch_few_as(const Product& p, hipStream_t s) {
-    constexpr bool GATE = EPI == kGate || EPI == kGate8;
+    constexpr bool GATE = kPaired<EPI>;
     const int64_t groups = GATE ? p.N / 16 : (int64_t(p.N) + 8 * R - 1) / (8 * R);
     constexpr bool WALK = MT > 1;
     const int lds = (WALK ? 2 : 1) * 2 * kWaves * MT * R * 16 * 16 + (QUANT ? int(p.M) * (p.K + kCodePad) : 0);
@@ -288,7 +292,7 @@ hipError_t launch_few_as(const Product& p, hipStream_t s) {
 
 template <int TYPE, int EPI>
 hipError_t choose_few(const Product& p, int quant, hipStream_t s) {
-    constexpr bool GATE = EPI == kGate || EPI == kGate8;
+    constexpr bool GATE = kPaired<EPI>;
     const int mt = int((p.M + 7) / 8);
     if constexpr (TYPE == kI8) {
         if (quant == kQuantBF16) return launch_few_as<TYPE, EPI, 1, 2, kQuantBF16>(p, s);

@@ -30,6 +30,8 @@
 // groups of 8 row tiles, so the tiles in flight on an XCD share operands in its L2.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "dense_common.h"
 #include "dense_epilogue.h"
 
@@ -86,13 +88,23 @@ __device__ __forceinline__ int chunk_swz(int k) {         // for 16-byte chunks
     return (X == 64 ? ((k >> 1) & 1) | ((k >> 2) & 2) : (k & 3) | ((k >> 1) & 4)) << 1;
 }
 
-// One operand's tile: X rows (tokens or weights) by one slice of K, X * 128 bytes in LDS.
+// permutation of the chunks of row r of an operand that is contiguous along K: rows of 128 bytes
+// share the 256 bytes of the banks by two, rows of 64 bytes by four.  (A 16-byte read serves 16
+// lanes at a time, but not 16 consecutive ones: rows 0-3 and 12-15 of one chunk go with rows
+// 4-11 of the next, hence the falling order; the rising one has two-way conflicts.)
+template <int SB>
+__device__ __forceinline__ int row_swz(int r) {
+    return SB == 128 ? (r >> 1) & 7 : -(r >> 2) & 3;
+}
+
+// One operand's tile: X rows (tokens or weights) by one slice of K, X * SB bytes in LDS.
 // KC: contiguous along K.
-template <int X, bool KC, int ES, int NW>
+template <int X, bool KC, int ES, int NW, int SB>
 struct Side {
-    static constexpr int Q = X * kSlice / 1024 / NW;      // 1 KiB loads of a wave per slice
-    static constexpr int KS = kSlice / ES;                // k in a slice
-    static_assert(Q * NW * 1024 == X * kSlice, "loads split over the waves");
+    static constexpr int Q = X * SB / 1024 / NW;          // 1 KiB loads of a wave per slice
+    static constexpr int KS = SB / ES;                    // k in a slice
+    static constexpr int CPS = SB / 16;                   // 16-byte chunks of a row's slice
+    static_assert(Q * NW * 1024 == X * SB, "loads split over the waves");
     static_assert(KC || ES >= 2, "transposing reads: 16-bit elements; fp32 reads single values");
 
     const uint8_t* base;     // (uniform) first row / column of the tile at the next slice to load
@@ -105,14 +117,14 @@ struct Side {
         const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
         const uint32_t ldb = uint32_t(ld) * ES;
         base = static_cast<const uint8_t*>(p) + (KC ? x0 * ld * ES : x0 * ES);
-        step = KC ? kSlice : int64_t(KS) * ld * ES;
+        step = KC ? SB : int64_t(KS) * ld * ES;
         base += first * step;
         const int left = int(n_rows - x0 < X ? n_rows - x0 : X);
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             const int i = wave + NW * q;                  // 1 KiB block of the tile
             if constexpr (KC) {
-                const int r = i * 8 + lane / 8, c = lane % 8 ^ ((r >> 1) & 7);
+                const int r = (i * 64 + lane) / CPS, c = lane % CPS ^ row_swz<SB>(r);
                 off[q] = uint32_t(r < left ? r : left - 1) * ldb + c * 16;
             } else {
                 constexpr int CPR = X * ES / 16;          // 16-byte chunks of a k row
@@ -127,7 +139,7 @@ struct Side {
         const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, i = wave + NW * q;
         bool in;
         if constexpr (KC) {
-            const int r = i * 8 + lane / 8, c = lane % 8 ^ ((r >> 1) & 7);
+            const int r = (i * 64 + lane) / CPS, c = lane % CPS ^ row_swz<SB>(r);
             in = c * (16 / ES) < k_left;
         } else {
             in = (i * 64 + lane) / (X * ES / 16) < k_left;
@@ -148,15 +160,14 @@ struct Side {
 };
 
 // This lane's fragment reads of one operand: rows x0 + 16 i + lane % 16 of the tile.
-template <int X, bool KC, int ES>
+template <int X, bool KC, int ES, int SB>
 struct Reader {
-    uint32_t at[2];          // KC: byte offset for half-slice 0 and 1
+    uint32_t at[2];          // byte offset for the first and second 64 bytes of K
     int unit, f;             // not KC: first 16-column unit, its permutation
     __device__ __forceinline__ void init(int x0) {
         const int lane = threadIdx.x % kWave, j = lane % 16, g = lane / 16;
         if constexpr (KC) {
-            const int sw = (j >> 1) & 7;
-            at[0] = (x0 + j) * kSlice + ((g ^ sw) << 4);
+            at[0] = (x0 + j) * SB + ((g ^ row_swz<SB>(j)) << 4);
             at[1] = at[0] ^ 64;
         } else if constexpr (ES == 2) {
             const int k = 8 * g + j / 4;                      // + 4 for the second read
@@ -175,7 +186,7 @@ struct Reader {
     template <class V>
     __device__ __forceinline__ V read(const uint8_t* lds, int half, int i) const {
         if constexpr (KC) {
-            return *reinterpret_cast<const V*>(lds + at[half] + i * 16 * kSlice);
+            return *reinterpret_cast<const V*>(lds + at[half] + i * 16 * SB);
         } else if constexpr (ES == 2) {
             const uint8_t* p = lds + at[half] + (((unit + i) ^ f) << 5);
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
@@ -199,7 +210,9 @@ template <int BM_, int BN_, int WM_, int WN_>
 struct Tile {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NW = WM * WN, kThreads = NW * kWave;
     static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16, FH = FM / 2;
+    static constexpr int kFinishRow = TN * 4 + 16, kFinishBytes = NW * 2 * 16 * kFinishRow;
     static constexpr int STAGE = (BM + BN) * kSlice, kLdsBytes = 2 * STAGE;
+    static_assert(kLdsBytes >= kFinishBytes, "room for the results");
     static constexpr int kWavesPerSimd = NW * (160 * 1024 / kLdsBytes) / 4 < 2 ? 1 : 2;
     static_assert(FH * 32 == TM && FN * 16 == TN && FN % 2 == 0, "fragments");
 };
@@ -211,21 +224,100 @@ __device__ __forceinline__ int2 tile_origin(int tile, int m_tiles, int n_tiles) 
     return make_int2(grp * kGroupM + in % gm, in / gm);
 }
 
-// The sums of fragment row i of a wave: lane: row m, columns nb + 16 j .. + 3
-template <int TYPE, int EPI, int FN, class Acc>
-__device__ __forceinline__ void finish_row(const Product& p, int64_t m, int nb, const Acc (&v)[FN]) {
-    if (m >= p.M) return;
+// Between LDS writes and reads that pass values from lane to lane of one wave: the LDS takes a
+// wave's operations in order, so only the compiler has to keep them so.
+__device__ __forceinline__ void lanes_in_order() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// The sums of a wave's TM x TN tile, from its rows m0 and columns n0 on.  A lane holds pieces of
+// four columns of 16 rows; written from there, every store instruction would touch 16 rows with
+// 32 bytes each, which is slow.  So 16 rows at a time go through LDS (a wave's own part: no
+// barrier; two places, the next rows are written before the last are read) and come back as 8
+// consecutive columns a lane, whole lines of a few rows an instruction.  Rows lie 4 banks apart.
+// A wait for a load waits for every older store, so the loads of finishing are ahead: column
+// scales and a row scale a lane at the start, gate and up values one pass ahead.  PARTIAL: fp32
+// (or integer) sums to part, row by row.
+template <int TYPE, int EPI, class C, bool PARTIAL, class Acc>
+__device__ __forceinline__ void finish_tile(const Product& p, int64_t m0, int n0, const Acc (&acc)[C::FM][C::FN],
+                                            uint8_t* lds, void* part, int64_t ld_part) {
+    typedef typename Elem<TYPE>::Acc S;
+    constexpr int ROW = C::kFinishRow;
+    constexpr bool PAIR = kPaired<EPI> && !PARTIAL;
+    constexpr int LPR = C::TN / (PAIR ? 16 : 8);             // lanes a row
+    constexpr int RPP = kWave / LPR < 16 ? kWave / LPR : 16; // rows a pass
+    static_assert(16 % RPP == 0, "passes of whole rows");
+    const int lane = threadIdx.x % kWave;
+    uint8_t* st = lds + threadIdx.x / kWave * (2 * 16 * ROW);
+    const int lr = lane / LPR, lc = lane % LPR;
+    // this lane's first column in the tile: 8 lc, or the 8 lc-th gate column
+    const int col = PAIR ? lc / 2 * 32 + lc % 2 * 8 : lc * 8;
+    const int n = n0 + col;
+    const bool in = n < p.N && lr < RPP;
+    constexpr int PASSES = 16 / RPP, ALL = C::FM * PASSES;
+    auto row_of = [&](int k) { return k * RPP + lr % RPP; };    // in the wave's tile
+    auto put_rows = [&](int i) {
+        uint8_t* d = st + (i & 1) * (16 * ROW) + (lane % 16) * ROW + (lane / 16) * 16;
 #pragma unroll
-    for (int j = 0; j < FN; j += EPI == kGate || EPI == kGate8 ? 2 : 1) {
-        const int n = nb + j * 16;
-        if (n >= p.N) continue;
-        if constexpr (EPI == kGate) finish_gate<TYPE>(p, m, n, v[j], v[j + 1]);
-        else if constexpr (EPI == kGate8) finish_gate8(p, m, n, v[j], v[j + 1]);
-        else if constexpr (EPI == kStore) finish_store<TYPE>(p, m, n, v[j]);
-        else if constexpr (EPI == kScale) finish_scale(p, m, n, v[j]);
-        else finish_dgate<TYPE>(p, m, n, v[j]);
+        for (int j = 0; j < C::FN; ++j) *reinterpret_cast<Acc*>(d + j * 64) = acc[i][j];
+    };
+    ColumnScales<EPI, 8> cs;
+    float scales = 0.0f;                                     // lane l: the scale of row l
+    RowInputs<TYPE, EPI, 8> ri[2];
+    auto load_inputs = [&](int k) {
+        if constexpr (EPI == kDGate && !PARTIAL) {
+            const int64_t m = m0 + row_of(k);
+            if (m < p.M && in) ri[k & 1].load(p, m, n);
+        }
+    };
+    if constexpr (!PARTIAL) {
+        cs.load(p, n < p.N ? n : 0);
+        static_assert(C::TM <= kWave, "a row scale a lane");
+        if (EPI == kScale || EPI == kGate8) {
+            const int64_t m = m0 + lane;
+            scales = p.row_scale[m < p.M ? m : p.M - 1];
+        }
+        load_inputs(0);
+    }
+    put_rows(0);
+#pragma unroll
+    for (int k = 0; k < ALL; ++k) {
+        if (k % PASSES == 0) {
+            lanes_in_order();
+            if (k / PASSES + 1 < C::FM) put_rows(k / PASSES + 1);
+        }
+        const uint8_t* row = st + (k / PASSES & 1) * (16 * ROW) + row_of(k) % 16 * ROW + col * 4;
+        const int64_t m = m0 + row_of(k);
+        S v[8], u[8];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const Acc t = *reinterpret_cast<const Acc*>(row + e * 16);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[4 * e + q] = t[q];
+            if constexpr (PAIR) {
+                const Acc w = *reinterpret_cast<const Acc*>(row + 64 + e * 16);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) u[4 * e + q] = w[q];
+            }
+        }
+        if constexpr (!PARTIAL) {
+            if (EPI == kScale || EPI == kGate8) ri[k & 1].rs = __shfl(scales, row_of(k), kWave);
+            if (k + 1 < ALL) load_inputs(k + 1);
+        }
+        if (m >= p.M || !in) continue;
+        if constexpr (PARTIAL) {
+            S* d = static_cast<S*>(part) + m * ld_part + n;
+            *reinterpret_cast<Acc*>(d) = Acc{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<Acc*>(d + 4) = Acc{v[4], v[5], v[6], v[7]};
+        } else {
+            finish<TYPE, EPI, 8>(p, m, n, v, u, cs, ri[k & 1]);
+        }
     }
 }
+
+// Elements between the rows of a partial sum (a multiple of 8 from N up) and of one split.
+__host__ __device__ inline int64_t part_ld(const Product& p) { return (int64_t(p.N) + 7) / 8 * 8; }
 
 template <int TYPE, int LAYOUT, int EPI, class C>
 __global__ void __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::kWavesPerSimd)))
@@ -249,12 +341,12 @@ k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
 
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const int wm = wave / C::WN, wn = wave % C::WN;
-    Side<C::BM, AKC, ES, C::NW> sa;
-    Side<C::BN, BKC, ES, C::NW> sb;
+    Side<C::BM, AKC, ES, C::NW, kSlice> sa;
+    Side<C::BN, BKC, ES, C::NW, kSlice> sb;
     sa.init(p.a, p.lda, m0, p.M, first);
     sb.init(p.b, p.ldb, n0, p.N, first);
-    Reader<C::BM, AKC, ES> ra;
-    Reader<C::BN, BKC, ES> rb;
+    Reader<C::BM, AKC, ES, kSlice> ra;
+    Reader<C::BN, BKC, ES, kSlice> rb;
     ra.init(wm * C::TM);
     rb.init(wn * C::TN);
 
@@ -340,42 +432,177 @@ k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
         mul(Q3{});
     }
 
-    if (splits > 1) {
-        // partial sums, [split][tile][fragment][thread]
-        Acc* part = static_cast<Acc*>(p.part) + int64_t(lid) * (C::FM * C::FN * C::kThreads) + threadIdx.x;
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-            for (int j = 0; j < C::FN; ++j) part[(i * C::FN + j) * C::kThreads] = acc[i][j];
-        return;
-    }
+    __syncthreads();                                         // the stages are read
+    const int64_t mw = m0 + wm * C::TM;
+    const int nw = n0 + wn * C::TN;
+    if (splits > 1)
+        finish_tile<TYPE, EPI, C, true>(p, mw, nw, acc, lds,
+                                        static_cast<typename Elem<TYPE>::Acc*>(p.part) + split * p.M * part_ld(p), part_ld(p));
+    else
+        finish_tile<TYPE, EPI, C, false>(p, mw, nw, acc, lds, nullptr, 0);
+}
+
+// Counts of s_waitcnt: vector memory operations that may be in flight, LDS operations (15: any).
+constexpr int wait_for(int vm, int lgkm) { return (vm & 15) | (7 << 4) | (lgkm << 8) | ((vm >> 4) << 14); }
+__device__ __forceinline__ void fence_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// The 256 x 256 tile: 8 waves, two on each SIMD, in two groups that take turns.  While one group
+// runs the matrix instructions of half a slice (32 of them, 512 cycles of the matrix unit), the
+// other reads its fragments of the next half from LDS; a barrier ends each turn, and the groups
+// run half a period apart.  So the matrix units always have a wave whose operands are in
+// registers: with loads left out this runs at the rate of the matrix instructions alone.
+//
+// What then decides is that a turn's loads do not outlast it: the CU's path from memory takes 512
+// cycles for 32 KiB, so a slice's 64 KiB have to be spread over its four turns.  The operands lie
+// in a ring of five 32 KiB places (all of the LDS), B and A of a slice by turns.  In its first
+// reading turn of slice s a group requests its share of A of slice s + 1, in the second that of B
+// of slice s + 2: the places are those of slice s - 1.  (Both in the first turn, two stages:
+// 1.25 times the time of the loop.)
+struct Turns {
+    static constexpr int BM = 256, BN = 256, WM = 4, WN = 2, NW = 8, kThreads = 512;
+    static constexpr int TM = 64, TN = 128, FM = 4, FN = 8;
+    static constexpr int kFinishRow = TN * 4 + 16, kFinishBytes = NW * 2 * 16 * kFinishRow;
+    static constexpr int PLACE = 256 * kSlice, kPlaces = 5, kLdsBytes = kPlaces * PLACE;
+    static_assert(kLdsBytes >= kFinishBytes && kLdsBytes <= 160 * 1024, "LDS of a CU");
+};
+
+template <int TYPE, int LAYOUT, int EPI>
+__global__ void __launch_bounds__(Turns::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
+k_mma_turns(const Product p, int m_tiles, int n_tiles, int splits) {
+    typedef Turns C;
+    typedef typename Frag<TYPE>::V V;
+    typedef typename Frag<TYPE>::Acc Acc;
+    constexpr int ES = Frag<TYPE>::ES, KS = kSlice / ES;
+    constexpr bool AKC = LAYOUT != kTN, BKC = LAYOUT == kNT;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int tiles = m_tiles * n_tiles, total = tiles * splits, per = (total + kXcds - 1) / kXcds;
+    const int lid = int(blockIdx.x % kXcds) * per + int(blockIdx.x / kXcds);
+    if (int(blockIdx.x / kXcds) >= per || lid >= total) return;
+    const int split = lid / tiles, tile = lid % tiles;
+    const int2 mn = tile_origin(tile, m_tiles, n_tiles);
+    const int64_t m0 = int64_t(mn.x) * C::BM;
+    const int n0 = mn.y * C::BN;
+    const int all = (p.K + KS - 1) / KS, share = (all + splits - 1) / splits;
+    const int first = split * share, n = min(share, all - first);
+
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    const bool second = __builtin_amdgcn_readfirstlane(wave) >= 4;    // (SIMD i has waves i and i + 4)
+    Side<C::BM, AKC, ES, C::NW, kSlice> sa;
+    Side<C::BN, BKC, ES, C::NW, kSlice> sb;
+    sa.init(p.a, p.lda, m0, p.M, first);
+    sb.init(p.b, p.ldb, n0, p.N, first);
+    constexpr int kLoads = decltype(sb)::Q;                   // a wave's loads of B of a slice
+    Reader<C::BM, AKC, ES, kSlice> ra;
+    Reader<C::BN, BKC, ES, kSlice> rb;
+    ra.init(wm * C::TM);
+    rb.init(wn * C::TN);
+    Acc acc[C::FM][C::FN];
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
-        finish_row<TYPE, EPI>(p, m0 + wm * C::TM + i * 16 + lane % 16, n0 + wn * C::TN + 4 * (lane / 16), acc[i]);
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) acc[i][j] = Acc{0, 0, 0, 0};
+
+    int left_a = p.K - first * KS, left_b = left_a;           // k from the next slice to request on
+    auto place = [&](int u) { return lds + (u >= C::kPlaces ? u - C::kPlaces : u) * C::PLACE; };
+    auto issue_a = [&](int u) {
+        sa.issue(place(u), left_a);
+        left_a -= KS;
+    };
+    auto issue_b = [&](int u) {
+        sb.issue(place(u), left_b);
+        left_b -= KS;
+    };
+    // all but the newest B has landed: B of the slice after next, where there is one
+    auto landed = [&](bool newest, auto lgkm_) {
+        constexpr int lgkm = decltype(lgkm_)::value;
+        if (newest) __builtin_amdgcn_s_waitcnt(wait_for(kLoads, lgkm));
+        else __builtin_amdgcn_s_waitcnt(wait_for(0, lgkm));
+    };
+    typedef std::integral_constant<int, 0> AlsoLds;
+    typedef std::integral_constant<int, 15> NotLds;
+    issue_b(0);
+    issue_a(1);
+    if (n > 1) issue_b(2);
+    landed(n > 1, NotLds{});
+    fence_barrier();
+    if (second) fence_barrier();                              // half a period behind
+    int u = 0;                                                // B's place, A's is the next
+    for (int j = 0; j < n; ++j) {
+        const uint8_t *pb = place(u), *pa = place(u + 1);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            V fa[C::FM], fb[C::FN];
+#pragma unroll
+            for (int i = 0; i < C::FN; ++i) fb[i] = rb.template read<V>(pb, half, i);
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i) fa[i] = ra.template read<V>(pa, half, i);
+            if (half == 0 && j + 1 < n) issue_a(u + 3);
+            if (half == 1 && j + 2 < n) issue_b(u + 4);
+            // slice j + 1 has landed at the end of the slice's last turn: a reading turn of the
+            // second group, a computing turn of the first
+            if (half == 1 && second) landed(j + 2 < n, AlsoLds{});
+            else __builtin_amdgcn_s_waitcnt(wait_for(63, 0));
+            fence_barrier();
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                for (int k = 0; k < C::FN; ++k) acc[i][k] = mma(fb[k], fa[i], acc[i][k]);
+            __builtin_amdgcn_s_setprio(0);
+            if (half == 1 && !second) landed(j + 2 < n, NotLds{});
+            fence_barrier();
+        }
+        u = u + 2 >= C::kPlaces ? u + 2 - C::kPlaces : u + 2;
+    }
+    if (!second) fence_barrier();
+
+    const int64_t mw = m0 + wm * C::TM;
+    const int nw = n0 + wn * C::TN;
+    if (splits > 1)
+        finish_tile<TYPE, EPI, C, true>(p, mw, nw, acc, lds,
+                                        static_cast<typename Elem<TYPE>::Acc*>(p.part) + split * p.M * part_ld(p), part_ld(p));
+    else
+        finish_tile<TYPE, EPI, C, false>(p, mw, nw, acc, lds, nullptr, 0);
 }
 
-// Adds the splits' partial sums, in order, and finishes: workgroup (tile, fragment row i), the
-// threads as in k_mma.
-template <int TYPE, int EPI, class C>
-__global__ void __launch_bounds__(C::kThreads) k_join(const Product p, int m_tiles, int n_tiles, int splits) {
-    typedef typename Frag<TYPE>::Acc Acc;
-    const int tiles = m_tiles * n_tiles, tile = blockIdx.x, i = blockIdx.y;
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, wm = wave / C::WN, wn = wave % C::WN;
-    const int2 mn = tile_origin(tile, m_tiles, n_tiles);
-    const int64_t m = int64_t(mn.x) * C::BM + wm * C::TM + i * 16 + lane % 16;
-    if (m >= p.M) return;
-    constexpr int64_t kTileAcc = C::FM * C::FN * C::kThreads;
-    const Acc* part = static_cast<const Acc*>(p.part) + int64_t(tile) * kTileAcc + i * C::FN * C::kThreads + threadIdx.x;
-    Acc acc[C::FN];
+// Adds the splits' partial sums, in order, and finishes: 8 columns (or 8 pairs) of a row a thread.
+template <int TYPE, int EPI>
+__global__ void __launch_bounds__(256) k_join(const Product p, int splits) {
+    typedef typename Elem<TYPE>::Acc S;
+    typedef typename Frag<TYPE>::Acc V4;
+    constexpr bool PAIR = kPaired<EPI>;
+    const int64_t ld = part_ld(p), units = PAIR ? p.N / 16 : ld / 8, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= p.M * units) return;
+    const int64_t m = i / units;
+    const int k = int(i % units), n = PAIR ? k / 2 * 32 + k % 2 * 8 : k * 8;
+    ColumnScales<EPI, 8> cs;
+    cs.load(p, n);
+    S v[8], u[8];
+    auto add = [&](S (&t)[8], int col) {
+        const S* part = static_cast<const S*>(p.part) + m * ld + col;
+        V4 a = *reinterpret_cast<const V4*>(part), b = *reinterpret_cast<const V4*>(part + 4);
+        for (int s = 1; s < splits; ++s) {
+            part += p.M * ld;
+            a += *reinterpret_cast<const V4*>(part);
+            b += *reinterpret_cast<const V4*>(part + 4);
+        }
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j) acc[j] = part[j * C::kThreads];
-    for (int s = 1; s < splits; ++s)
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j) acc[j] += part[int64_t(s) * tiles * kTileAcc + j * C::kThreads];
-    finish_row<TYPE, EPI>(p, m, mn.y * C::BN + wn * C::TN + 4 * (lane / 16), acc);
+        for (int e = 0; e < 4; ++e) t[e] = a[e], t[4 + e] = b[e];
+    };
+    add(v, n);
+    if constexpr (PAIR) add(u, n + 16);
+    RowInputs<TYPE, EPI, 8> in;
+    in.load(p, m, n);
+    finish<TYPE, EPI, 8>(p, m, n, v, u, cs, in);
 }
 
-typedef Tile<256, 256, 2, 4> Big;
 typedef Tile<128, 128, 2, 2> Mid;
 typedef Tile<64, 64, 2, 2> Small;
 
@@ -383,17 +610,24 @@ template <int TYPE, int LAYOUT, int EPI, class C>
 hipError_t launch(const Product& p, int splits, hipStream_t s) {
     const int64_t mt = (p.M + C::BM - 1) / C::BM, nt = (p.N + C::BN - 1) / C::BN;
     if (mt * nt * splits > 0x7FFFFFF0 / kXcds) return hipErrorInvalidValue;
-    if (splits > 1 && mt * nt * splits * C::BM * C::BN * 4 > p.part_bytes) return hipErrorInvalidValue;
-    static const hipError_t lds_ok = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_mma<TYPE, LAYOUT, EPI, C>),
-                                                         hipFuncAttributeMaxDynamicSharedMemorySize, C::kLdsBytes);
+    if (splits > 1 && p.M * part_ld(p) * splits * 4 > p.part_bytes) return hipErrorInvalidValue;
+    constexpr bool TURNS = std::is_same<C, Turns>::value;
+    const void* f;
+    if constexpr (TURNS) f = reinterpret_cast<const void*>(&k_mma_turns<TYPE, LAYOUT, EPI>);
+    else f = reinterpret_cast<const void*>(&k_mma<TYPE, LAYOUT, EPI, C>);
+    static const hipError_t lds_ok = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, C::kLdsBytes);
     if (lds_ok != hipSuccess) return lds_ok;
     const int64_t grid = (mt * nt * splits + kXcds - 1) / kXcds * kXcds;
-    hipLaunchKernelGGL((k_mma<TYPE, LAYOUT, EPI, C>), dim3(unsigned(grid)), dim3(C::kThreads), C::kLdsBytes, s, p,
-                       int(mt), int(nt), splits);
+    if constexpr (TURNS)
+        hipLaunchKernelGGL((k_mma_turns<TYPE, LAYOUT, EPI>), dim3(unsigned(grid)), dim3(C::kThreads), C::kLdsBytes, s, p,
+                           int(mt), int(nt), splits);
+    else
+        hipLaunchKernelGGL((k_mma<TYPE, LAYOUT, EPI, C>), dim3(unsigned(grid)), dim3(C::kThreads), C::kLdsBytes, s, p,
+                           int(mt), int(nt), splits);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || splits == 1) return e;
-    hipLaunchKernelGGL((k_join<TYPE, EPI, C>), dim3(unsigned(mt * nt), C::FM), dim3(C::kThreads), 0, s, p, int(mt), int(nt),
-                       splits);
+    const int64_t items = p.M * (kPaired<EPI> ? p.N / 16 : part_ld(p) / 8);
+    hipLaunchKernelGGL((k_join<TYPE, EPI>), dim3(unsigned((items + 255) / 256)), dim3(256), 0, s, p, splits);
     return hipGetLastError();
 }
 
@@ -410,7 +644,7 @@ Choice plan(const Product& p, int es, int64_t n_cu) {
     for (int c = 0; c < 3; ++c) {
         const int64_t tiles = (p.M + kinds[c].bm - 1) / kinds[c].bm * ((p.N + kinds[c].bn - 1) / kinds[c].bn);
         for (int sp = 1; sp <= 32 && sp * 4 <= (nk > 4 ? nk : 4); sp *= 2) {
-            if (sp > 1 && tiles * sp * kinds[c].bm * kinds[c].bn * 4 > p.part_bytes) break;
+            if (sp > 1 && p.M * part_ld(p) * sp * 4 > p.part_bytes) break;
             const int64_t share = (nk + sp - 1) / sp;
             if (share * (sp - 1) >= nk) break;               // every split has slices
             const int64_t slots = n_cu * kinds[c].slots, rounds = (tiles * sp + slots - 1) / slots;
@@ -424,7 +658,7 @@ Choice plan(const Product& p, int es, int64_t n_cu) {
 template <int TYPE, int LAYOUT, int EPI>
 hipError_t choose(const Product& p, hipStream_t s) {
     const Choice c = plan(p, Frag<TYPE>::ES, compute_units());
-    if (c.tile == 0) return launch<TYPE, LAYOUT, EPI, Big>(p, c.splits, s);
+    if (c.tile == 0) return launch<TYPE, LAYOUT, EPI, Turns>(p, c.splits, s);
     if (c.tile == 1) return launch<TYPE, LAYOUT, EPI, Mid>(p, c.splits, s);
     return launch<TYPE, LAYOUT, EPI, Small>(p, c.splits, s);
 }
