@@ -169,10 +169,10 @@ int moe_i8_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, c
     p.K = K;
     p.out = d_y;
     p.ldo = ld_y;
-    p.out_f32 = y_type == MOE_A_F32;
     p.vec_out = aligned(d_y, 16) && ld_y % 8 == 0;
     p.col_scale = d_w_scale;
-    hipError_t e = on_the_way ? launch_few(kI8, kScale, p, s, x_type, true) : launch_product(kI8, kNT, kScale, p, s);
+    const int epi = y_type == MOE_A_F32 ? kScale32 : kScale;
+    hipError_t e = on_the_way ? launch_few(kI8, epi, p, s, x_type, true) : launch_product(kI8, kNT, epi, p, s);
     return e == hipSuccess ? MOE_OK : hip_fail(ctx, e, "moe_i8_matmul launch");
 }
 
@@ -381,7 +381,6 @@ int moe_i8_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob8, vo
     p.K = c.inter;
     p.out = d_y;
     p.ldo = c.hidden;
-    p.out_f32 = 0;
     p.vec_out = 1;
     p.row_scale = hs;
     p.col_scale = reinterpret_cast<const float*>(blob + b.d_scale);

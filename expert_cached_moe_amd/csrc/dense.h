@@ -21,9 +21,10 @@ enum { kNT = 0, kNN = 1, kTN = 2 };
 // What becomes of the sums.
 enum {
     kStore = 0,   // out[m][n] = acc, rounded to the operands' type
-    kScale = 1,   // out[m][n] = acc * row_scale[m] * col_scale[n] (integer products)
+    kScale = 1,   // out[m][n] = acc * row_scale[m] * col_scale[n] (integer products), rounded to bf16
     kGate = 2,    // columns are interleaved gate / up: out[m][i] = silu(g) * u; gu[m][n] = acc if kept
     kGate8 = 3,   // the same from integer sums and scales, out in fp32
+    kScale32 = 5, // as kScale, out in fp32
     kDGate = 4,   // acc = dh[m][i]: out[m][..] = dg, du interleaved, from gu (pre-activations)
 };
 
@@ -35,9 +36,8 @@ struct Product {
     int32_t N, K;
     void* out;
     int64_t ldo;                // elements between rows of out
-    int32_t out_f32;            // kScale: out is fp32 (else bf16)
-    int32_t vec_out;            // kScale: out and its rows are 16-byte aligned for 8 values
-    const float* row_scale;     // kScale, kGate8
+    int32_t vec_out;            // kScale, kScale32: out and its rows are 16-byte aligned for 8 values
+    const float* row_scale;     // integer products
     const float* col_scale;
     void* part;                 // scratch for partial sums of part_bytes (0: none)
     int64_t part_bytes;

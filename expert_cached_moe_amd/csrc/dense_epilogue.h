@@ -2,6 +2,8 @@
 // product kernels.  For the gated epilogues those are W gate sums, and W up sums 16 columns on.
 #pragma once
 
+#include <type_traits>
+
 #include "dense_common.h"
 
 namespace moe {
@@ -61,12 +63,18 @@ __device__ __forceinline__ float sigmoid_of(float z) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
 }
 
+// Epilogues of integer products, and those whose results are one scaled number a column.
+template <int EPI>
+constexpr bool kScaled = EPI == kScale || EPI == kScale32 || EPI == kGate8;
+template <int EPI>
+constexpr bool kPlainScale = EPI == kScale || EPI == kScale32;
+
 // Scales of the columns a lane finishes (and of the up columns): loaded once, used for every row.
 template <int EPI, int W>
 struct ColumnScales {
-    float s[EPI == kScale || EPI == kGate8 ? W : 1], up[EPI == kGate8 ? W : 1];
+    float s[kScaled<EPI> ? W : 1], up[EPI == kGate8 ? W : 1];
     __device__ __forceinline__ void load(const Product& p, int n) {
-        if constexpr (EPI == kScale || EPI == kGate8) {
+        if constexpr (kScaled<EPI>) {
 #pragma unroll
             for (int j = 0; j < W; ++j) s[j] = p.col_scale[n + j < p.N ? n + j : p.N - 1];
         }
@@ -84,7 +92,7 @@ template <int TYPE, int EPI, int W>
 struct RowInputs {
     float rs, g[EPI == kDGate ? W : 1], u[EPI == kDGate ? W : 1];
     __device__ __forceinline__ void load(const Product& p, int64_t m, int n) {
-        if constexpr (EPI == kScale || EPI == kGate8) rs = p.row_scale[m];
+        if constexpr (kScaled<EPI>) rs = p.row_scale[m];
         if constexpr (EPI == kDGate) {
             typedef typename Elem<TYPE>::T E;
             const E* gu = static_cast<const E*>(p.gu) + m * 2 * p.N + n / 16 * 32 + n % 16;
@@ -94,8 +102,9 @@ struct RowInputs {
     }
 };
 
-// Row m, columns n .. n + W - 1 (v; the up sums in u).  n < N; only kScale may reach past N.
-template <int TYPE, int EPI, int W, class S>
+// Row m, columns n .. n + W - 1 (v; the up sums in u).  n < N; only kScale, kScale32 may reach
+// past N.  STREAM: results past the caches.
+template <int TYPE, int EPI, int W, bool STREAM, class S>
 __device__ __forceinline__ void finish(const Product& p, int64_t m, int n, const S (&v)[W], const S (&u)[W],
                                        const ColumnScales<EPI, W>& cs, const RowInputs<TYPE, EPI, W>& in) {
     typedef typename Elem<TYPE>::T E;
@@ -104,24 +113,19 @@ __device__ __forceinline__ void finish(const Product& p, int64_t m, int n, const
 #pragma unroll
         for (int j = 0; j < W; ++j) f[j] = float(v[j]);
         store_row<W>(static_cast<E*>(p.out) + m * p.ldo + n, f);
-    } else if constexpr (EPI == kScale) {
+    } else if constexpr (kPlainScale<EPI>) {
+        typedef typename std::conditional<EPI == kScale32, float, uint16_t>::type O;
         float f[W];
 #pragma unroll
         for (int j = 0; j < W; ++j) f[j] = float(v[j]) * in.rs * cs.s[j];
-        const int64_t o = m * p.ldo + n;
+        O* o = static_cast<O*>(p.out) + m * p.ldo + n;
         if (p.vec_out && n + W <= p.N) {
-            // (streamed: 8192 x 24576 x 4096 took 690 us against 752, since the results of all CUs,
-            // which leave at the same time, do not crowd the next tiles' operands out of L2)
-            if (p.out_f32) store_row<W, W == 8>(static_cast<float*>(p.out) + o, f);
-            else store_row<W, W == 8>(static_cast<uint16_t*>(p.out) + o, f);
+            store_row<W, STREAM>(o, f);
             return;
         }
 #pragma unroll
         for (int j = 0; j < W; ++j)
-            if (n + j < p.N) {
-                if (p.out_f32) put(static_cast<float*>(p.out) + o + j, f[j]);
-                else put(static_cast<uint16_t*>(p.out) + o + j, f[j]);
-            }
+            if (n + j < p.N) put(o + j, f[j]);
     } else if constexpr (EPI == kGate) {
         // n is the gate column (n % 32 < 16) of inner index n / 32 * 16 + n % 16
         float h[W];
@@ -139,7 +143,7 @@ __device__ __forceinline__ void finish(const Product& p, int64_t m, int n, const
         float h[W];
 #pragma unroll
         for (int j = 0; j < W; ++j) h[j] = silu(float(v[j]) * in.rs * cs.s[j]) * (float(u[j]) * in.rs * cs.up[j]);
-        store_row<W>(static_cast<float*>(p.out) + m * p.ldo + n / 32 * 16 + n % 16, h);
+        store_row<W, STREAM>(static_cast<float*>(p.out) + m * p.ldo + n / 32 * 16 + n % 16, h);
     } else {
         // v = dh, n an inner index
         const int64_t o = m * 2 * p.N + n / 16 * 32 + n % 16;

@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
             cs.load(p, int(n));
             RowInputs<TYPE, EPI, 4> in;
             in.load(p, t, int(n));
-            finish<TYPE, EPI, 4>(p, t, int(n), v, u, cs, in);
+            finish<TYPE, EPI, 4, false>(p, t, int(n), v, u, cs, in);
         }
         if (!WALK) break;
         g = next;
@@ -315,6 +315,7 @@ hipError_t launch_few(int type, int epi, const Product& p, hipStream_t s, int x_
     if (quant && (type != kI8 || p.M > 8 || p.M * p.K > kFewQuant)) return hipErrorInvalidValue;
     if (type == kI8) {
         if (epi == kScale) return choose_few<kI8, kScale>(p, q, s);
+        if (epi == kScale32) return choose_few<kI8, kScale32>(p, q, s);
         if (epi == kGate8) return choose_few<kI8, kGate8>(p, q, s);
     } else if (type == kBF16) {
         if (epi == kStore) return choose_few<kBF16, kStore>(p, q, s);

@@ -200,9 +200,12 @@ struct Reader {
     }
 };
 
+// Counts of s_waitcnt: vector memory operations that may be in flight, LDS operations (15: any).
+constexpr int wait_for(int vm, int lgkm) { return (vm & 15) | (7 << 4) | (lgkm << 8) | ((vm >> 4) << 14); }
+
 // Barrier that hands loaded slices over: every wave waits for its own loads first.
 __device__ __forceinline__ void barrier_loads() {
-    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_s_waitcnt(wait_for(0, 0));
     __syncthreads();
 }
 
@@ -234,8 +237,11 @@ __device__ __forceinline__ void lanes_in_order() {
 // The sums of a wave's TM x TN tile, from its rows m0 and columns n0 on.  A lane holds pieces of
 // four columns of 16 rows; written from there, every store instruction would touch 16 rows with
 // 32 bytes each, which is slow.  So 16 rows at a time go through LDS (a wave's own part: no
-// barrier; two places, the next rows are written before the last are read) and come back as 8
-// consecutive columns a lane, whole lines of a few rows an instruction.  Rows lie 4 banks apart.
+// barrier; two places, the next rows are written before the last are read) and come back as W
+// consecutive columns a lane (16 bytes of the result), whole lines of a few rows an instruction.
+// Rows lie 4 banks apart.  Results of integer products are streamed (8192 x 24576 x 4096 took
+// 690 us against 752: the results of all CUs, which leave at the same time, do not crowd the next
+// tiles' operands out of L2); the block's are read by the next product.
 // A wait for a load waits for every older store, so the loads of finishing are ahead: column
 // scales and a row scale a lane at the start, gate and up values one pass ahead.  PARTIAL: fp32
 // (or integer) sums to part, row by row.
@@ -245,14 +251,15 @@ __device__ __forceinline__ void finish_tile(const Product& p, int64_t m0, int n0
     typedef typename Elem<TYPE>::Acc S;
     constexpr int ROW = C::kFinishRow;
     constexpr bool PAIR = kPaired<EPI> && !PARTIAL;
-    constexpr int LPR = C::TN / (PAIR ? 16 : 8);             // lanes a row
+    constexpr int W = TYPE == kF32 || EPI == kGate8 || EPI == kScale32 || PARTIAL ? 4 : 8;
+    constexpr int LPR = C::TN / (PAIR ? 2 * W : W);          // lanes a row
     constexpr int RPP = kWave / LPR < 16 ? kWave / LPR : 16; // rows a pass
     static_assert(16 % RPP == 0, "passes of whole rows");
     const int lane = threadIdx.x % kWave;
     uint8_t* st = lds + threadIdx.x / kWave * (2 * 16 * ROW);
     const int lr = lane / LPR, lc = lane % LPR;
-    // this lane's first column in the tile: 8 lc, or the 8 lc-th gate column
-    const int col = PAIR ? lc / 2 * 32 + lc % 2 * 8 : lc * 8;
+    // this lane's first column in the tile: W lc, or the W lc-th gate column
+    const int col = PAIR ? lc * W / 16 * 32 + lc * W % 16 : lc * W;
     const int n = n0 + col;
     const bool in = n < p.N && lr < RPP;
     constexpr int PASSES = 16 / RPP, ALL = C::FM * PASSES;
@@ -262,9 +269,9 @@ __device__ __forceinline__ void finish_tile(const Product& p, int64_t m0, int n0
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) *reinterpret_cast<Acc*>(d + j * 64) = acc[i][j];
     };
-    ColumnScales<EPI, 8> cs;
+    ColumnScales<EPI, W> cs;
     float scales = 0.0f;                                     // lane l: the scale of row l
-    RowInputs<TYPE, EPI, 8> ri[2];
+    RowInputs<TYPE, EPI, W> ri[2];
     auto load_inputs = [&](int k) {
         if constexpr (EPI == kDGate && !PARTIAL) {
             const int64_t m = m0 + row_of(k);
@@ -274,7 +281,7 @@ __device__ __forceinline__ void finish_tile(const Product& p, int64_t m0, int n0
     if constexpr (!PARTIAL) {
         cs.load(p, n < p.N ? n : 0);
         static_assert(C::TM <= kWave, "a row scale a lane");
-        if (EPI == kScale || EPI == kGate8) {
+        if (kScaled<EPI>) {
             const int64_t m = m0 + lane;
             scales = p.row_scale[m < p.M ? m : p.M - 1];
         }
@@ -289,9 +296,9 @@ __device__ __forceinline__ void finish_tile(const Product& p, int64_t m0, int n0
         }
         const uint8_t* row = st + (k / PASSES & 1) * (16 * ROW) + row_of(k) % 16 * ROW + col * 4;
         const int64_t m = m0 + row_of(k);
-        S v[8], u[8];
+        S v[W], u[W];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < W / 4; ++e) {
             const Acc t = *reinterpret_cast<const Acc*>(row + e * 16);
 #pragma unroll
             for (int q = 0; q < 4; ++q) v[4 * e + q] = t[q];
@@ -302,16 +309,15 @@ __device__ __forceinline__ void finish_tile(const Product& p, int64_t m0, int n0
             }
         }
         if constexpr (!PARTIAL) {
-            if (EPI == kScale || EPI == kGate8) ri[k & 1].rs = __shfl(scales, row_of(k), kWave);
+            if (kScaled<EPI>) ri[k & 1].rs = __shfl(scales, row_of(k), kWave);
             if (k + 1 < ALL) load_inputs(k + 1);
         }
         if (m >= p.M || !in) continue;
         if constexpr (PARTIAL) {
             S* d = static_cast<S*>(part) + m * ld_part + n;
             *reinterpret_cast<Acc*>(d) = Acc{v[0], v[1], v[2], v[3]};
-            *reinterpret_cast<Acc*>(d + 4) = Acc{v[4], v[5], v[6], v[7]};
         } else {
-            finish<TYPE, EPI, 8>(p, m, n, v, u, cs, ri[k & 1]);
+            finish<TYPE, EPI, W, kScaled<EPI>>(p, m, n, v, u, cs, ri[k & 1]);
         }
     }
 }
@@ -394,11 +400,12 @@ k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
     typedef std::integral_constant<int, RA> NA;
     typedef std::integral_constant<int, RA + RB> NAB;
 
-    auto issue = [&](int ks) {
-        uint8_t* st = lds + (ks & 1) * C::STAGE;
-        const int left = p.K - (first + ks) * KS;
+    int left = p.K - first * KS;                              // k from the next slice to request on
+    auto issue = [&](int stage) {
+        uint8_t* st = lds + stage * C::STAGE;
         sa.issue(st, left);
         sb.issue(st + C::BM * kSlice, left);
+        left -= KS;
     };
     issue(0);
     barrier_loads();
@@ -416,7 +423,7 @@ k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
         sched(NAB{});
         sched(NA{});
         barrier_loads();       // slice ks is read by every wave, slice ks + 1 has landed
-        if (ks + 2 < nk) issue(ks + 2);
+        if (ks + 2 < nk) issue(ks & 1);
         read(lds + ((ks + 1) & 1) * C::STAGE, Q0{});
         mul(Q3{});
         sched(NAB{});
@@ -431,7 +438,6 @@ k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
         mul(Q2{});
         mul(Q3{});
     }
-
     __syncthreads();                                         // the stages are read
     const int64_t mw = m0 + wm * C::TM;
     const int nw = n0 + wn * C::TN;
@@ -442,8 +448,6 @@ k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
         finish_tile<TYPE, EPI, C, false>(p, mw, nw, acc, lds, nullptr, 0);
 }
 
-// Counts of s_waitcnt: vector memory operations that may be in flight, LDS operations (15: any).
-constexpr int wait_for(int vm, int lgkm) { return (vm & 15) | (7 << 4) | (lgkm << 8) | ((vm >> 4) << 14); }
 __device__ __forceinline__ void fence_barrier() {
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
@@ -588,6 +592,7 @@ __global__ void __launch_bounds__(256) k_join(const Product p, int splits) {
     auto add = [&](S (&t)[8], int col) {
         const S* part = static_cast<const S*>(p.part) + m * ld + col;
         V4 a = *reinterpret_cast<const V4*>(part), b = *reinterpret_cast<const V4*>(part + 4);
+#pragma unroll 4
         for (int s = 1; s < splits; ++s) {
             part += p.M * ld;
             a += *reinterpret_cast<const V4*>(part);
@@ -600,11 +605,11 @@ __global__ void __launch_bounds__(256) k_join(const Product p, int splits) {
     if constexpr (PAIR) add(u, n + 16);
     RowInputs<TYPE, EPI, 8> in;
     in.load(p, m, n);
-    finish<TYPE, EPI, 8>(p, m, n, v, u, cs, in);
+    finish<TYPE, EPI, 8, false>(p, m, n, v, u, cs, in);
 }
 
-typedef Tile<128, 128, 2, 2> Mid;
-typedef Tile<64, 64, 2, 2> Small;
+typedef Tile<128, 128, 2, 2> Mid;            // two workgroups a CU
+typedef Tile<64, 64, 2, 2> Small;            // four
 
 template <int TYPE, int LAYOUT, int EPI, class C>
 hipError_t launch(const Product& p, int splits, hipStream_t s) {
@@ -631,24 +636,34 @@ hipError_t launch(const Product& p, int splits, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Tile and split of K.  Times in units of one 256 x 256 slice on one CU.
+// Tile and split of K: the least of the times that a model fitted to measurements gives, in us.
+// A slice takes `slice` and `more` for each further workgroup on its CU (up to `slots`), a tile
+// `tile` to start and finish; a split costs a second kernel and its partial sums both ways.
+// Measured (8-bit codes, whole call): 300 x 4096 x 4096: 256-tiles 40 us, 128 20, 64 13.6, 128
+// split in two 23; 2000 x 4096 x 4096: 45, 34, 50; 1024 x 8192 x 8192: 72, 63, 93; 100 x 8192 x
+// 4096: 64-tiles 19, split in two 16.6, in eight 21.  Three and more slices in flight instead of
+// two changed none of them by more than a few percent.  fp32: eight times the matrix time.
 struct Choice {
     int tile, splits;
 };
 Choice plan(const Product& p, int es, int64_t n_cu) {
-    struct { int bm, bn, slots; double slice, start; } const kinds[] = {
-        {256, 256, 1, es == 4 ? 8.5 : 1.0, 4.0}, {128, 128, 2, es == 4 ? 4.4 : 0.7, 3.0}, {64, 64, 4, es == 4 ? 2.4 : 0.6, 3.0}};
+    struct Kind { int bm, bn, slots; double slice, more, tile; };
+    static const Kind half[] = {{256, 256, 1, 1.3, 0.0, 6.0}, {128, 128, 2, 0.68, 0.28, 3.0}, {64, 64, 4, 0.36, 0.13, 1.5}};
+    static const Kind fp32[] = {{256, 256, 1, 8.6, 0.0, 6.0}, {128, 128, 2, 2.3, 2.1, 3.0}, {64, 64, 4, 0.65, 0.55, 1.5}};
+    const Kind* kinds = es == 4 ? fp32 : half;
     const int64_t nk = (int64_t(p.K) * es + kSlice - 1) / kSlice;
     Choice best{0, 1};
     double best_t = 1e30;
     for (int c = 0; c < 3; ++c) {
-        const int64_t tiles = (p.M + kinds[c].bm - 1) / kinds[c].bm * ((p.N + kinds[c].bn - 1) / kinds[c].bn);
+        const Kind& k = kinds[c];
+        const int64_t tiles = (p.M + k.bm - 1) / k.bm * ((p.N + k.bn - 1) / k.bn);
         for (int sp = 1; sp <= 32 && sp * 4 <= (nk > 4 ? nk : 4); sp *= 2) {
-            if (sp > 1 && p.M * part_ld(p) * sp * 4 > p.part_bytes) break;
-            const int64_t share = (nk + sp - 1) / sp;
+            const int64_t sums = p.M * part_ld(p) * sp, share = (nk + sp - 1) / sp;
+            if (sp > 1 && sums * 4 > p.part_bytes) break;
             if (share * (sp - 1) >= nk) break;               // every split has slices
-            const int64_t slots = n_cu * kinds[c].slots, rounds = (tiles * sp + slots - 1) / slots;
-            const double t = rounds * (share * kinds[c].slice + kinds[c].start) + (sp > 1 ? 6.0 + 0.25 * sp : 0.0);
+            const int64_t groups = tiles * sp, rounds = (groups + n_cu * k.slots - 1) / (n_cu * k.slots);
+            const int64_t on_cu = (groups + n_cu - 1) / n_cu < k.slots ? (groups + n_cu - 1) / n_cu : k.slots;
+            const double t = rounds * (share * (k.slice + k.more * (on_cu - 1)) + k.tile) + (sp > 1 ? 3.0 + sums * 1.4e-6 : 0.0);
             if (t < best_t) best_t = t, best = Choice{c, sp};
         }
     }
@@ -670,6 +685,7 @@ hipError_t launch_product(int type, int layout, int epi, const Product& p, hipSt
     if (layout == kNT && few_tokens(p, type == kI8 ? 1 : type == kBF16 ? 2 : 4)) return launch_few(type, epi, p, s);
     if (type == kI8) {
         if (layout == kNT && epi == kScale) return choose<kI8, kNT, kScale>(p, s);
+        if (layout == kNT && epi == kScale32) return choose<kI8, kNT, kScale32>(p, s);
         if (layout == kNT && epi == kGate8) return choose<kI8, kNT, kGate8>(p, s);
         return hipErrorInvalidValue;
     }

@@ -1,11 +1,14 @@
 // Row quantisation to 8-bit integers: scale = max|row| / 127, code = row / scale to the nearest
 // integer (ties to even, decided on the exact quotient).
 //
-// One workgroup a row.  The row is read once: up to kHold vectors of 8 numbers a thread stay
-// in registers between the maximum and the codes (rows up to 16384 numbers with 256 threads);
-// longer rows read what is beyond again.  Bound by memory: it reads the numbers and writes one
+// One workgroup a row.  The row is read once: up to HOLD vectors of 8 numbers a thread stay in
+// registers between the maximum and the codes; longer rows read what is beyond again.  HOLD is
+// the least that holds the row (its registers decide how many rows are in flight); rows too few
+// to fill the chip take 1024 threads each.  Bound by memory: it reads the numbers and writes one
 // byte for each.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "dense_common.h"
 
@@ -13,7 +16,7 @@ namespace moe {
 namespace dense {
 namespace {
 
-constexpr int kThreads = 256, kHold = 8, kVec = 8;
+constexpr int kVec = 8;
 
 // 8 numbers of a row from index i (in bounds, since cols is a multiple of 16)
 template <bool BF16, bool VEC>
@@ -54,7 +57,7 @@ __device__ __forceinline__ void store8(int8_t* q, const float (&v)[kVec], float 
     *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
 }
 
-template <bool BF16, bool VEC>
+template <bool BF16, bool VEC, int kThreads, int kHold>
 __global__ void __launch_bounds__(kThreads) k_quantize_rows(const void* __restrict__ x, int64_t ld, int64_t rows,
                                                             int cols, int8_t* __restrict__ q,
                                                             float* __restrict__ scale) {
@@ -109,6 +112,36 @@ __global__ void __launch_bounds__(256) k_zero(uint4* p, int64_t n) {
 
 }  // namespace
 
+namespace {
+template <bool BF16, bool VEC>
+void launch_rows(const void* x, int64_t ld, int64_t rows, int cols, int8_t* q, float* scale, hipStream_t s) {
+    const dim3 grid(unsigned(rows < (1 << 20) ? rows : (1 << 20)));
+    auto go = [&](auto threads_, auto hold_) {
+        constexpr int THREADS = decltype(threads_)::value, HOLD = decltype(hold_)::value;
+        hipLaunchKernelGGL((k_quantize_rows<BF16, VEC, THREADS, HOLD>), grid, dim3(THREADS), 0, s, x, ld, rows, cols, q,
+                           scale);
+    };
+    typedef std::integral_constant<int, 256> Some;
+    typedef std::integral_constant<int, 1024> Many;
+    typedef std::integral_constant<int, 1> H1;
+    typedef std::integral_constant<int, 2> H2;
+    typedef std::integral_constant<int, 4> H4;
+    if (rows <= 512 && cols > 256 * kVec) {
+        if (cols <= 1024 * kVec) go(Many{}, H1{});
+        else if (cols <= 1024 * kVec * 2) go(Many{}, H2{});
+        else go(Many{}, H4{});
+    } else if (cols <= 256 * kVec) {
+        go(Some{}, H1{});
+    } else if (cols <= 256 * kVec * 2) {
+        go(Some{}, H2{});
+    } else if (cols <= 256 * kVec * 4) {
+        go(Some{}, H4{});
+    } else {
+        go(Many{}, H2{});
+    }
+}
+}  // namespace
+
 hipError_t launch_quantize(const void* x, int x_type, int64_t ld_x, int64_t rows, int32_t cols, int8_t* q,
                            float* scale, hipStream_t s) {
     if (rows <= 0) return hipSuccess;
@@ -116,11 +149,10 @@ hipError_t launch_quantize(const void* x, int x_type, int64_t ld_x, int64_t rows
     const int es = bf16 ? 2 : 4;
     // 16-byte loads when every row starts on 16 bytes
     const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld_x * es % 16 == 0;
-    const dim3 grid(unsigned(rows < (1 << 20) ? rows : (1 << 20))), block(kThreads);
-    if (bf16 && vec) hipLaunchKernelGGL((k_quantize_rows<true, true>), grid, block, 0, s, x, ld_x, rows, cols, q, scale);
-    else if (bf16) hipLaunchKernelGGL((k_quantize_rows<true, false>), grid, block, 0, s, x, ld_x, rows, cols, q, scale);
-    else if (vec) hipLaunchKernelGGL((k_quantize_rows<false, true>), grid, block, 0, s, x, ld_x, rows, cols, q, scale);
-    else hipLaunchKernelGGL((k_quantize_rows<false, false>), grid, block, 0, s, x, ld_x, rows, cols, q, scale);
+    if (bf16 && vec) launch_rows<true, true>(x, ld_x, rows, cols, q, scale, s);
+    else if (bf16) launch_rows<true, false>(x, ld_x, rows, cols, q, scale, s);
+    else if (vec) launch_rows<false, true>(x, ld_x, rows, cols, q, scale, s);
+    else launch_rows<false, false>(x, ld_x, rows, cols, q, scale, s);
     return hipGetLastError();
 }
 
