@@ -76,14 +76,14 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// MT: 8-token tiles; R: 8-row weight tiles of a workgroup.  Gated epilogues: R = 2, 8 gate rows
-// and their 8 up rows (16 rows on in the weights).
+// MT: 8-token tiles; R: 8-row weight tiles of a workgroup.  Gated epilogues: R / 2 tiles of gate
+// rows, then those of their up rows (16 rows on in the weights).
 template <int TYPE, int EPI, int MT, int R, int QUANT, bool WALK, bool ONE>
 __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) {
     typedef typename FewAcc<TYPE>::T Acc;
     constexpr int ES = TYPE == kI8 ? 1 : TYPE == kBF16 ? 2 : 4;
     constexpr bool GATE = kPaired<EPI>;
-    static_assert(!GATE || R == 2, "gate and up tiles");
+    static_assert(!GATE || R == 2 || R == 4, "gate and up tiles");
     static_assert(WALK || !ONE, "x is kept for the groups of a walk");
     static_assert(QUANT == kNoQuant || MT == 1, "x quantised on the way: up to 8 tokens");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -95,8 +95,9 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
     const uint32_t kb = uint32_t(p.K) * ES;
     const int l8 = lane % 8;
     const uint32_t piece = uint32_t(lane / 16 + 4 * (lane % 16 / 8)) * 16;
-    // first row of group g; gated: group g has inner indices 8 g .. 8 g + 7
-    auto first_row = [&](int g) { return GATE ? int64_t(g) / 2 * 32 + g % 2 * 8 : int64_t(g) * 8 * R; };
+    // first row of group g, and of its tile r from there; gated: a group has 4 R inner indices
+    auto first_row = [&](int g) { return GATE && R == 2 ? int64_t(g) / 2 * 32 + g % 2 * 8 : int64_t(g) * 8 * R; };
+    auto tile_row = [](int r) { return GATE ? r / (R / 2) * 16 + r % (R / 2) * 8 : r * 8; };
     uint32_t xo[MT];
     // numbers to quantise: vector v of a thread is 8 numbers of row qrow[v]
     constexpr int NV = QUANT == kNoQuant ? 1 : kQuantVec;
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
         uint32_t wo[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int row = r * (GATE ? 16 : 8) + l8;
+            const int row = tile_row(r) + l8;
             wo[r] = uint32_t(row < left ? row : int(left)) * uint32_t(p.ldb * ES);
         }
 #pragma unroll
@@ -242,15 +243,16 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
         }
         // (the other area's readers are past it: they met at the barrier before this one)
         lds_barrier();
-        constexpr int PER = GATE ? 2 : 1, ITEMS = MT * R / PER * 16;
+        constexpr int PER = GATE ? 2 : 1, RES = R / PER, ITEMS = MT * RES * 16;    // RES: tiles of results
         for (int it = tid; it < ITEMS; it += kThreads) {
-            const int tile = it / 16 * PER, ent = it % 16, m = tile / R, r = tile % R;
+            const int ent = it % 16, m = it / 16 / RES, r = it / 16 % RES;
             Acc sum[PER];
 #pragma unroll
             for (int q = 0; q < PER; ++q) {
-                sum[q] = red[(tile + q) * 16 + ent];
+                const int tile = m * R + r + q * RES;
+                sum[q] = red[tile * 16 + ent];
 #pragma unroll
-                for (int v = 1; v < 2 * kWaves; ++v) sum[q] += red[(v * MT * R + tile + q) * 16 + ent];
+                for (int v = 1; v < 2 * kWaves; ++v) sum[q] += red[(v * MT * R + tile) * 16 + ent];
             }
             const int t = m * 8 + ent % 8;
             const int64_t n = n0 + r * 8 + 4 * (ent / 8);
@@ -272,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
 template <int TYPE, int EPI, int MT, int R, int QUANT>
 hipError_t launch_few_as(const Product& p, hipStream_t s) {
     constexpr bool GATE = kPaired<EPI>;
-    const int64_t groups = GATE ? p.N / 16 : (int64_t(p.N) + 8 * R - 1) / (8 * R);
+    const int64_t groups = (int64_t(p.N) + 8 * R - 1) / (8 * R);
     constexpr bool WALK = MT > 1;
     const int lds = (WALK ? 2 : 1) * 2 * kWaves * MT * R * 16 * 16 + (QUANT ? int(p.M) * (p.K + kCodePad) : 0);
     if constexpr (!WALK) {
@@ -302,7 +304,14 @@ hipError_t choose_few(const Product& p, int quant, hipStream_t s) {
         // 16 rows a workgroup leave CUs idle below N = 4096: 8 then
         if (p.N < 4096 && mt == 1) return launch_few_as<TYPE, EPI, 1, 1, kNoQuant>(p, s);
     }
-    if (mt == 1) return launch_few_as<TYPE, EPI, 1, 2, kNoQuant>(p, s);
+    if (mt == 1) {
+        // Every workgroup reads all of x: 32 rows a workgroup halve that, which pays from a few
+        // tokens on where the rows still fill the chip (8 tokens: 100003 x 4096 codes 70.5 us
+        // against 78, 8192 x 4096 8.4 against 9.5; 4096 x 4096 7.4 against 6.4; 1 token 66
+        // against 64.5).
+        if (p.M > 2 && p.N >= 8192) return launch_few_as<TYPE, EPI, 1, 4, kNoQuant>(p, s);
+        return launch_few_as<TYPE, EPI, 1, 2, kNoQuant>(p, s);
+    }
     if (mt == 2) return launch_few_as<TYPE, EPI, 2, 2, kNoQuant>(p, s);
     return launch_few_as<TYPE, EPI, 4, 2, kNoQuant>(p, s);
 }
