@@ -23,6 +23,11 @@
 // against 109 us); up to 8 tokens the registers it takes cost more than it saves (8 tokens: 81
 // against 78 us, 1 token 76 against 64).
 //
+// AHEAD (K of several passes, up to 16 rows a workgroup): the next pass's weights and activations
+// are requested before the current one's products, in registers of their own (1 token, 100003 x
+// 8192 codes 118 us against 139, 4096 x 12288 11.2 against 12.5; with 32 rows the registers cost
+// more: 8 tokens, 50003 x 8192 87 against 81).
+//
 // QUANT: x comes as numbers and every workgroup quantises it for itself, into LDS, while its
 // first weights are on the way: T K conversions in each workgroup against a launch and a pass
 // through memory, for T K up to kMaxQuant.
@@ -78,13 +83,14 @@ __device__ __forceinline__ void lds_barrier() {
 
 // MT: 8-token tiles; R: 8-row weight tiles of a workgroup.  Gated epilogues: R / 2 tiles of gate
 // rows, then those of their up rows (16 rows on in the weights).
-template <int TYPE, int EPI, int MT, int R, int QUANT, bool WALK, bool ONE>
+template <int TYPE, int EPI, int MT, int R, int QUANT, bool WALK, bool ONE, bool AHEAD>
 __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) {
     typedef typename FewAcc<TYPE>::T Acc;
     constexpr int ES = TYPE == kI8 ? 1 : TYPE == kBF16 ? 2 : 4;
     constexpr bool GATE = kPaired<EPI>;
     static_assert(!GATE || R == 2 || R == 4, "gate and up tiles");
     static_assert(WALK || !ONE, "x is kept for the groups of a walk");
+    static_assert(!AHEAD || !WALK, "a walk has its next group ahead");
     static_assert(QUANT == kNoQuant || MT == 1, "x quantised on the way: up to 8 tokens");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     __shared__ uint32_t s_top[8];
@@ -125,8 +131,8 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
 #pragma unroll
     for (int m = 0; m < MT; ++m) xo[m] = uint32_t(min(m * 8 + l8, T - 1)) * (QUANT != kNoQuant ? p.K + kCodePad : uint32_t(p.lda * ES));
     constexpr uint32_t kStride = kWaves * kSlice;
-    dev::u32x4 w[kDepth][R];
-    auto load_w = [&](int g, uint32_t s) {
+    dev::u32x4 w[AHEAD ? 2 : 1][kDepth][R];
+    auto load_w = [&](dev::u32x4 (&w)[kDepth][R], int g, uint32_t s) {
         const int64_t n0 = first_row(g), left = p.N - 1 - n0;   // rows past N repeat the last one
         const __amdgpu_buffer_rsrc_t rw = rsrc(static_cast<const uint8_t*>(p.b) + n0 * p.ldb * ES);
         uint32_t wo[R];
@@ -142,8 +148,23 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
             for (int r = 0; r < R; ++r) w[d][r] = load16<kStream>(rw, k < kb ? wo[r] + k : kOutside);
         }
     };
+    dev::u32x4 x[AHEAD ? 2 : 1][kDepth][MT];
+    auto load_x = [&](dev::u32x4 (&x)[kDepth][MT], uint32_t s) {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+            const uint32_t k = s + d * kStride + piece;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                if constexpr (QUANT != kNoQuant)                // (any codes do past K: the weights are zeros there)
+                    x[d][m] = *reinterpret_cast<const dev::u32x4*>(lds + (k < kb ? xo[m] + k : 0));
+                else
+                    x[d][m] = load16<0>(rx, k < kb ? xo[m] + k : kOutside);
+            }
+        }
+    };
     int g = blockIdx.x;
-    load_w(g, wave * kSlice);
+    if constexpr (AHEAD && QUANT == kNoQuant) load_x(x[0], wave * kSlice);
+    load_w(w[0], g, wave * kSlice);
     if constexpr (QUANT != kNoQuant) {
         float f[NV][8];
 #pragma unroll
@@ -192,21 +213,7 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
     // LDS: the codes, then two areas of sums, [wave][half][m][r][16]
     constexpr int kSums = 2 * kWaves * MT * R * 16;
     Acc* red0 = reinterpret_cast<Acc*>(lds + (QUANT != kNoQuant ? T * (p.K + kCodePad) : 0));
-    dev::u32x4 x[kDepth][MT];
-    auto load_x = [&](uint32_t s) {
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-            const uint32_t k = s + d * kStride + piece;
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if constexpr (QUANT != kNoQuant)                // (any codes do past K: the weights are zeros there)
-                    x[d][m] = *reinterpret_cast<const dev::u32x4*>(lds + (k < kb ? xo[m] + k : 0));
-                else
-                    x[d][m] = load16<0>(rx, k < kb ? xo[m] + k : kOutside);
-            }
-        }
-    };
-    if constexpr (ONE) load_x(wave * kSlice);
+    if constexpr (ONE) load_x(x[0], wave * kSlice);
     for (int turn = 0; g < groups; ++turn) {
         const int next = g + int(gridDim.x);
         const int64_t n0 = first_row(g);
@@ -215,8 +222,7 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int r = 0; r < R; ++r) acc[m][r] = Acc{0, 0, 0, 0};
-        for (uint32_t s = wave * kSlice;;) {
-            if constexpr (!ONE) load_x(s);
+        auto products = [&](const dev::u32x4 (&w)[kDepth][R], const dev::u32x4 (&x)[kDepth][MT]) {
 #pragma unroll
             for (int d = 0; d < kDepth; ++d)
 #pragma unroll
@@ -226,11 +232,28 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
                         if constexpr (TYPE == kF32) acc[m][r] = mma_f32(w[d][r], x[d][m], acc[m][r]);
                         else acc[m][r] = mma(w[d][r], x[d][m], acc[m][r]);
                     }
-            s += kStride * kDepth;
-            if (ONE || s >= kb) break;
-            load_w(g, s);
+        };
+        constexpr uint32_t kPass = kStride * kDepth;
+        if constexpr (AHEAD) {
+            if constexpr (QUANT != kNoQuant) load_x(x[0], wave * kSlice);
+            for (uint32_t s = wave * kSlice;; s += 2 * kPass) {
+                if (s + kPass < kb) load_x(x[1], s + kPass), load_w(w[1], g, s + kPass);
+                products(w[0], x[0]);
+                if (s + kPass >= kb) break;
+                if (s + 2 * kPass < kb) load_x(x[0], s + 2 * kPass), load_w(w[0], g, s + 2 * kPass);
+                products(w[1], x[1]);
+                if (s + 2 * kPass >= kb) break;
+            }
+        } else {
+            for (uint32_t s = wave * kSlice;;) {
+                if constexpr (!ONE) load_x(x[0], s);
+                products(w[0], x[0]);
+                s += kPass;
+                if (ONE || s >= kb) break;
+                load_w(w[0], g, s);
+            }
         }
-        if (WALK && next < groups) load_w(next, wave * kSlice);
+        if (WALK && next < groups) load_w(w[0], next, wave * kSlice);
         // sums of the diagonal blocks: lanes 0-7 and 16-23 (rows 0-7, first halves), 40-47 and
         // 56-63 (rows 8-15, second halves) as entry lane % 8 + 8 (lane / 16 % 2) of half lane / 32
         Acc* red = red0 + (turn & 1) * kSums;
@@ -277,17 +300,23 @@ hipError_t launch_few_as(const Product& p, hipStream_t s) {
     const int64_t groups = (int64_t(p.N) + 8 * R - 1) / (8 * R);
     constexpr bool WALK = MT > 1;
     const int lds = (WALK ? 2 : 1) * 2 * kWaves * MT * R * 16 * 16 + (QUANT ? int(p.M) * (p.K + kCodePad) : 0);
+    const bool one = p.K * (TYPE == kI8 ? 1 : TYPE == kBF16 ? 2 : 4) <= kWaves * kSlice * kDepth;
     if constexpr (!WALK) {
-        hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, false, false>), dim3(unsigned(groups)), dim3(kThreads), lds, s,
-                           p, int(groups));
+        constexpr bool AHEAD = R <= 2;
+        if (one || !AHEAD)
+            hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, false, false, false>), dim3(unsigned(groups)),
+                               dim3(kThreads), lds, s, p, int(groups));
+        else
+            hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, false, false, AHEAD>), dim3(unsigned(groups)),
+                               dim3(kThreads), lds, s, p, int(groups));
     } else {
         // up to four workgroups a CU, each the same number of groups
         const int64_t most = int64_t(compute_units()) * 4, turns = (groups + most - 1) / most;
         const dim3 grid(unsigned((groups + turns - 1) / turns));
-        if (p.K * (TYPE == kI8 ? 1 : TYPE == kBF16 ? 2 : 4) <= kWaves * kSlice * kDepth)
-            hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, true, true>), grid, dim3(kThreads), lds, s, p, int(groups));
+        if (one)
+            hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, true, true, false>), grid, dim3(kThreads), lds, s, p, int(groups));
         else
-            hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, true, false>), grid, dim3(kThreads), lds, s, p, int(groups));
+            hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, true, false, false>), grid, dim3(kThreads), lds, s, p, int(groups));
     }
     return hipGetLastError();
 }
