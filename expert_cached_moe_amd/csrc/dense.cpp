@@ -48,7 +48,12 @@ BlockWork block_work(const moe_config& c, int64_t T) {
     return w;
 }
 
-int64_t save_h_offset(const moe_config& c, int64_t T) { return align256(T * 2 * c.inter * act_bytes(c)); }
+// What the forward pass saves: pre-activations [T][2I] (fp32, or for bf16 24 bits: the upper 16 in
+// one array, the lower 8 in another), then h [T][I].
+int64_t save_low_offset(const moe_config& c, int64_t T) { return align256(T * 2 * c.inter * act_bytes(c)); }
+int64_t save_h_offset(const moe_config& c, int64_t T) {
+    return align256(save_low_offset(c, T) + (c.w_dtype == MOE_W_F32 ? 0 : T * 2 * c.inter));
+}
 
 struct Blob8 {
     int64_t gu = 0, d = 0, gu_scale = 0, d_scale = 0, bytes = 0;
@@ -215,6 +220,7 @@ int moe_dense_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob, 
     p.out = h;
     p.ldo = c.inter;
     p.gu = d_save;
+    p.gu_low = d_save ? static_cast<uint8_t*>(d_save) + save_low_offset(c, T) : nullptr;
     hipError_t e = launch_product(type, kNT, kGate, p, s);
     if (e != hipSuccess) return hip_fail(ctx, e, "moe_dense_ffn launch");
     p.a = h;
@@ -267,6 +273,7 @@ int moe_dense_ffn_backward(moe_ctx* ctx, const void* d_dy, const void* d_x, int3
     p.out = d_ws;
     p.ldo = 2 * I;
     p.gu = const_cast<uint8_t*>(save);
+    p.gu_low = const_cast<uint8_t*>(save) + save_low_offset(c, T);
     if ((e = launch_product(type, kNN, kDGate, p, s)) != hipSuccess) return hip_fail(ctx, e, "moe_dense_ffn_backward launch");
     if (dblob) {
         Product w{};                                   // dWd = dy^T h

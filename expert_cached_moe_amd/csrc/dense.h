@@ -42,6 +42,7 @@ struct Product {
     void* part;                 // scratch for partial sums of part_bytes (0: none)
     int64_t part_bytes;
     void* gu;                   // kGate: written when not null; kDGate: read; rows of 2 I elements
+    uint8_t* gu_low;            // bf16: their lower 8 of 24 bits
 };
 
 // Scratch for partial sums: products with few tiles are split along K to fill the chip.

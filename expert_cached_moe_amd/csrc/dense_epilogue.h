@@ -54,6 +54,55 @@ __device__ __forceinline__ void load_row(float (&v)[W], const float* p) {
     }
 }
 
+// Pre-activations kept for the backward pass.  fp32: as they are.  bf16 contexts: the upper 24
+// bits of the fp32 sums (16 fraction bits), 16 in one array and 8 in another of the same shape.
+// Rounded to bf16 they would be a third rounding of that size in the gradients, after those of
+// dg, du and of the result (relative error of dWg and dx 0.0030 against 0.0023); all 32 bits
+// would cost another third of the bytes.
+template <int W>
+__device__ __forceinline__ void keep_row(float* p, uint8_t*, int64_t i, const float (&v)[W]) {
+    store_row<W>(p + i, v);
+}
+template <int W>
+__device__ __forceinline__ void keep_row(uint16_t* hi, uint8_t* lo, int64_t i, const float (&v)[W]) {
+    uint32_t h[W / 2], l[W / 4];
+#pragma unroll
+    for (int j = 0; j < W / 2; ++j) {
+        const uint32_t a = __float_as_uint(v[2 * j]), b = __float_as_uint(v[2 * j + 1]);
+        h[j] = __builtin_amdgcn_perm(b, a, 0x07060302);              // upper halves
+        const uint32_t two = __builtin_amdgcn_perm(b, a, 0x0C0C0501);  // their next bytes
+        l[j / 2] = j % 2 ? l[j / 2] | two << 16 : two;
+    }
+    if constexpr (W == 8) {
+        *reinterpret_cast<uint4*>(hi + i) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint2*>(lo + i) = make_uint2(l[0], l[1]);
+    } else {
+        *reinterpret_cast<uint2*>(hi + i) = make_uint2(h[0], h[1]);
+        *reinterpret_cast<uint32_t*>(lo + i) = l[0];
+    }
+}
+template <int W>
+__device__ __forceinline__ void kept_row(float (&v)[W], const float* p, const uint8_t*, int64_t i) {
+    load_row<W>(v, p + i);
+}
+template <int W>
+__device__ __forceinline__ void kept_row(float (&v)[W], const uint16_t* hi, const uint8_t* lo, int64_t i) {
+    uint32_t h[W / 2], l[W / 4];
+    if constexpr (W == 8) {
+        const uint4 q = *reinterpret_cast<const uint4*>(hi + i);
+        const uint2 r = *reinterpret_cast<const uint2*>(lo + i);
+        h[0] = q.x, h[1] = q.y, h[2] = q.z, h[3] = q.w, l[0] = r.x, l[1] = r.y;
+    } else {
+        const uint2 q = *reinterpret_cast<const uint2*>(hi + i);
+        h[0] = q.x, h[1] = q.y, l[0] = *reinterpret_cast<const uint32_t*>(lo + i);
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        const uint32_t up = j % 2 ? h[j / 2] & 0xFFFF0000u : h[j / 2] << 16;
+        v[j] = __uint_as_float(up | (l[j / 4] >> (8 * (j % 4)) & 255u) << 8);
+    }
+}
+
 // The sigmoid of the block's kernels.  fp32: expf and a division.  bf16: hardware exp2 and
 // reciprocal (about one fp32 step each; the results are rounded to bf16, 2^16 times coarser).
 // Either way e^-z overflows to infinity for very negative z, whose reciprocal is 0.
@@ -95,9 +144,9 @@ struct RowInputs {
         if constexpr (kScaled<EPI>) rs = p.row_scale[m];
         if constexpr (EPI == kDGate) {
             typedef typename Elem<TYPE>::T E;
-            const E* gu = static_cast<const E*>(p.gu) + m * 2 * p.N + n / 16 * 32 + n % 16;
-            load_row<W>(g, gu);
-            load_row<W>(u, gu + 16);
+            const int64_t i = m * 2 * p.N + n / 16 * 32 + n % 16;
+            kept_row<W>(g, static_cast<const E*>(p.gu), p.gu_low, i);
+            kept_row<W>(u, static_cast<const E*>(p.gu), p.gu_low, i + 16);
         }
     }
 };
@@ -132,9 +181,8 @@ __device__ __forceinline__ void finish(const Product& p, int64_t m, int n, const
 #pragma unroll
         for (int j = 0; j < W; ++j) h[j] = v[j] * sigmoid_of<TYPE>(v[j]) * u[j];
         if (p.gu) {
-            E* s = static_cast<E*>(p.gu) + m * p.N + n;
-            store_row<W>(s, v);
-            store_row<W>(s + 16, u);
+            keep_row<W>(static_cast<E*>(p.gu), p.gu_low, m * p.N + n, v);
+            keep_row<W>(static_cast<E*>(p.gu), p.gu_low, m * p.N + n + 16, u);
         }
         store_row<W>(static_cast<E*>(p.out) + m * p.ldo + n / 32 * 16 + n % 16, h);
     } else if constexpr (EPI == kGate8) {

@@ -371,8 +371,9 @@ int moe_i8_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, c
  * Scratch bytes for up to max_T tokens of any moe_dense_* or moe_i8_ffn call. */
 int64_t moe_dense_workspace_bytes(const moe_config* cfg, int32_t max_T);
 /* Bytes a training step keeps from the forward to the backward pass for T tokens: the
- * pre-activations Wg x and Wu x ([T][2I], interleaved like the blob's rows) and
- * h = silu(Wg x) * (Wu x) ([T][I]), each rounded once to the activation type. */
+ * pre-activations Wg x and Wu x ([T][2I], interleaved like the blob's rows; fp32, or the upper
+ * 24 bits of it for bf16 weights) and h = silu(Wg x) * (Wu x) ([T][I], rounded once to the
+ * activation type). */
 int64_t moe_dense_save_bytes(const moe_config* cfg, int32_t T);
 /* Forward pass of T tokens (async on s): d_x [T][H], d_blob, d_y [T][H].  d_save
  * (moe_dense_save_bytes of the same T) is written when not NULL; y does not depend on it.

@@ -11,6 +11,7 @@ import numpy as np
 
 F32_HALF = 2.0 ** -24
 HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+KEPT = {"f32": 0.0, "bf16": 2.0 ** -15}          # pre-activations: fp32 cut after 16 fraction bits
 # exp, the reciprocal and the products of the sigmoid: a few steps each, and the argument's own
 # rounding times its size (|z| <= 88 before the result is 0 or 1)
 SIGMOID_REL = 2.0 ** -17
@@ -102,7 +103,7 @@ def block_bounds(dy, x, wg, wu, wd, dtype):
     sp = s + g * s * (1 - s)
     dh = dy @ wd
     adh, ed = np.abs(dh), _gamma(H) * (ady @ awd)
-    egs, eus = eg + (ag + eg) * half, eu + (au + eu) * half             # as saved
+    egs, eus = eg + (ag + eg) * KEPT[dtype], eu + (au + eu) * KEPT[dtype]             # as saved
     asp = np.abs(sp)
     # silu'' lies in (-0.1, 0.5]; silu' is a sum of terms of size s and s |g|
     esp = 0.5 * egs + SIGMOID_REL * (s + (ag + egs) * s)

@@ -85,7 +85,7 @@ def test_sizes():
     assert B.moe_i8_workspace_bytes(3, 64) >= 3 * 64 + 3 * 4
     assert B.moe_i8_workspace_bytes(0, 16) > 0
     assert B.moe_i8_workspace_bytes(2 ** 31 - 1, 131056) > 2 ** 31 * 131056 * 0.99
-    assert B.moe_dense_save_bytes(cfg, 5) >= 5 * 3 * 64 * 2
+    assert B.moe_dense_save_bytes(cfg, 5) >= 5 * (2 * 64 * 3 + 64 * 2)
     assert B.moe_dense_workspace_bytes(cfg, 5) >= 5 * (128 + 64 * 4 + 64 + 8)
     assert B.moe_i8_blob_bytes(cfg) >= 3 * 128 * 64 + 4 * (2 * 64 + 128)
     for K in (0, 8, 24, -16, 131072):
