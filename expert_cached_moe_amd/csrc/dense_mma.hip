@@ -89,22 +89,17 @@ __device__ __forceinline__ int chunk_swz(int k) {         // for 16-byte chunks
 }
 
 // permutation of the chunks of row r of an operand that is contiguous along K: rows of 128 bytes
-// share the 256 bytes of the banks by two, rows of 64 bytes by four.  (A 16-byte read serves 16
-// lanes at a time, but not 16 consecutive ones: rows 0-3 and 12-15 of one chunk go with rows
-// 4-11 of the next, hence the falling order; the rising one has two-way conflicts.)
-template <int SB>
-__device__ __forceinline__ int row_swz(int r) {
-    return SB == 128 ? (r >> 1) & 7 : -(r >> 2) & 3;
-}
+// share the 256 bytes of the banks by two
+__device__ __forceinline__ int row_swz(int r) { return (r >> 1) & 7; }
 
-// One operand's tile: X rows (tokens or weights) by one slice of K, X * SB bytes in LDS.
+// One operand's tile: X rows (tokens or weights) by one slice of K, X * 128 bytes in LDS.
 // KC: contiguous along K.
-template <int X, bool KC, int ES, int NW, int SB>
+template <int X, bool KC, int ES, int NW>
 struct Side {
-    static constexpr int Q = X * SB / 1024 / NW;          // 1 KiB loads of a wave per slice
-    static constexpr int KS = SB / ES;                    // k in a slice
-    static constexpr int CPS = SB / 16;                   // 16-byte chunks of a row's slice
-    static_assert(Q * NW * 1024 == X * SB, "loads split over the waves");
+    static constexpr int Q = X * kSlice / 1024 / NW;          // 1 KiB loads of a wave per slice
+    static constexpr int KS = kSlice / ES;                    // k in a slice
+    static constexpr int CPS = kSlice / 16;                   // 16-byte chunks of a row's slice
+    static_assert(Q * NW * 1024 == X * kSlice, "loads split over the waves");
     static_assert(KC || ES >= 2, "transposing reads: 16-bit elements; fp32 reads single values");
 
     const uint8_t* base;     // (uniform) first row / column of the tile at the next slice to load
@@ -117,14 +112,14 @@ struct Side {
         const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
         const uint32_t ldb = uint32_t(ld) * ES;
         base = static_cast<const uint8_t*>(p) + (KC ? x0 * ld * ES : x0 * ES);
-        step = KC ? SB : int64_t(KS) * ld * ES;
+        step = KC ? kSlice : int64_t(KS) * ld * ES;
         base += first * step;
         const int left = int(n_rows - x0 < X ? n_rows - x0 : X);
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             const int i = wave + NW * q;                  // 1 KiB block of the tile
             if constexpr (KC) {
-                const int r = (i * 64 + lane) / CPS, c = lane % CPS ^ row_swz<SB>(r);
+                const int r = (i * 64 + lane) / CPS, c = lane % CPS ^ row_swz(r);
                 off[q] = uint32_t(r < left ? r : left - 1) * ldb + c * 16;
             } else {
                 constexpr int CPR = X * ES / 16;          // 16-byte chunks of a k row
@@ -139,7 +134,7 @@ struct Side {
         const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, i = wave + NW * q;
         bool in;
         if constexpr (KC) {
-            const int r = (i * 64 + lane) / CPS, c = lane % CPS ^ row_swz<SB>(r);
+            const int r = (i * 64 + lane) / CPS, c = lane % CPS ^ row_swz(r);
             in = c * (16 / ES) < k_left;
         } else {
             in = (i * 64 + lane) / (X * ES / 16) < k_left;
@@ -159,15 +154,55 @@ struct Side {
     }
 };
 
+// Transposing reads of N fragments from the LDS offsets at[i] and, for their second halves,
+// at[i] + OFF.  In assembly, with their wait: the compiler takes the builtin to depend on every
+// load into LDS in flight and waits for all of them first, which undoes the requests ahead.
+template <int OFF>
+__device__ __forceinline__ void read_transposed(const uint32_t (&at)[1], s16x4 (&lo)[1], s16x4 (&hi)[1]) {
+    asm volatile("ds_read_b64_tr_b16 %0, %2\n\tds_read_b64_tr_b16 %1, %2 offset:%3\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(lo[0]), "=&v"(hi[0]) : "v"(at[0]), "n"(OFF) : "memory");
+}
+template <int OFF>
+__device__ __forceinline__ void read_transposed(const uint32_t (&at)[2], s16x4 (&lo)[2], s16x4 (&hi)[2]) {
+    asm volatile("ds_read_b64_tr_b16 %0, %4\n\tds_read_b64_tr_b16 %1, %4 offset:%6\n\t"
+                 "ds_read_b64_tr_b16 %2, %5\n\tds_read_b64_tr_b16 %3, %5 offset:%6\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]) : "v"(at[0]), "v"(at[1]), "n"(OFF) : "memory");
+}
+template <int OFF>
+__device__ __forceinline__ void read_transposed(const uint32_t (&at)[4], s16x4 (&lo)[4], s16x4 (&hi)[4]) {
+    asm volatile("ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %8 offset:%12\n\t"
+                 "ds_read_b64_tr_b16 %2, %9\n\tds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
+                 "ds_read_b64_tr_b16 %4, %10\n\tds_read_b64_tr_b16 %5, %10 offset:%12\n\t"
+                 "ds_read_b64_tr_b16 %6, %11\n\tds_read_b64_tr_b16 %7, %11 offset:%12\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]), "=&v"(lo[3]), "=&v"(hi[3])
+                 : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(OFF) : "memory");
+}
+template <int OFF>
+__device__ __forceinline__ void read_transposed(const uint32_t (&at)[8], s16x4 (&lo)[8], s16x4 (&hi)[8]) {
+    asm volatile("ds_read_b64_tr_b16 %0, %16\n\tds_read_b64_tr_b16 %1, %16 offset:%24\n\t"
+                 "ds_read_b64_tr_b16 %2, %17\n\tds_read_b64_tr_b16 %3, %17 offset:%24\n\t"
+                 "ds_read_b64_tr_b16 %4, %18\n\tds_read_b64_tr_b16 %5, %18 offset:%24\n\t"
+                 "ds_read_b64_tr_b16 %6, %19\n\tds_read_b64_tr_b16 %7, %19 offset:%24\n\t"
+                 "ds_read_b64_tr_b16 %8, %20\n\tds_read_b64_tr_b16 %9, %20 offset:%24\n\t"
+                 "ds_read_b64_tr_b16 %10, %21\n\tds_read_b64_tr_b16 %11, %21 offset:%24\n\t"
+                 "ds_read_b64_tr_b16 %12, %22\n\tds_read_b64_tr_b16 %13, %22 offset:%24\n\t"
+                 "ds_read_b64_tr_b16 %14, %23\n\tds_read_b64_tr_b16 %15, %23 offset:%24\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]), "=&v"(lo[3]),
+                   "=&v"(hi[3]), "=&v"(lo[4]), "=&v"(hi[4]), "=&v"(lo[5]), "=&v"(hi[5]), "=&v"(lo[6]), "=&v"(hi[6]),
+                   "=&v"(lo[7]), "=&v"(hi[7])
+                 : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]), "v"(at[6]), "v"(at[7]), "n"(OFF)
+                 : "memory");
+}
+
 // This lane's fragment reads of one operand: rows x0 + 16 i + lane % 16 of the tile.
-template <int X, bool KC, int ES, int SB>
+template <int X, bool KC, int ES>
 struct Reader {
     uint32_t at[2];          // byte offset for the first and second 64 bytes of K
     int unit, f;             // not KC: first 16-column unit, its permutation
     __device__ __forceinline__ void init(int x0) {
         const int lane = threadIdx.x % kWave, j = lane % 16, g = lane / 16;
         if constexpr (KC) {
-            at[0] = (x0 + j) * SB + ((g ^ row_swz<SB>(j)) << 4);
+            at[0] = (x0 + j) * kSlice + ((g ^ row_swz(j)) << 4);
             at[1] = at[0] ^ 64;
         } else if constexpr (ES == 2) {
             const int k = 8 * g + j / 4;                      // + 4 for the second read
@@ -183,19 +218,29 @@ struct Reader {
             f = chunk_swz<X, ES>(k) >> 2;
         }
     }
-    template <class V>
-    __device__ __forceinline__ V read(const uint8_t* lds, int half, int i) const {
+    // fragments first .. first + N - 1 of half-slice `half`
+    template <int N, class V>
+    __device__ __forceinline__ void read(const uint8_t* lds, int half, int first, V (&v)[N]) const {
         if constexpr (KC) {
-            return *reinterpret_cast<const V*>(lds + at[half] + i * 16 * SB);
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = *reinterpret_cast<const V*>(lds + at[half] + (first + i) * 16 * kSlice);
         } else if constexpr (ES == 2) {
-            const uint8_t* p = lds + at[half] + (((unit + i) ^ f) << 5);
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * X * 2));
+            const uint32_t base = uint32_t(reinterpret_cast<uintptr_t>((lds_void*)(lds + at[half])));
+            uint32_t from[N];
+            s16x4 lo[N], hi[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) from[i] = base + (uint32_t((unit + first + i) ^ f) << 5);
+            read_transposed<4 * X * 2>(from, lo, hi);
             typedef __attribute__((ext_vector_type(8))) short s16x8;
-            return __builtin_bit_cast(V, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[i] = __builtin_bit_cast(V, __builtin_shufflevector(lo[i], hi[i], 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
-            const float* p = reinterpret_cast<const float*>(lds + at[half] + (((unit + i) ^ f) << 6));
-            return V{p[0], p[X], p[2 * X], p[3 * X]};
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float* p = reinterpret_cast<const float*>(lds + at[half] + (((unit + first + i) ^ f) << 6));
+                v[i] = V{p[0], p[X], p[2 * X], p[3 * X]};
+            }
         }
     }
 };
@@ -347,12 +392,12 @@ k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
 
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const int wm = wave / C::WN, wn = wave % C::WN;
-    Side<C::BM, AKC, ES, C::NW, kSlice> sa;
-    Side<C::BN, BKC, ES, C::NW, kSlice> sb;
+    Side<C::BM, AKC, ES, C::NW> sa;
+    Side<C::BN, BKC, ES, C::NW> sb;
     sa.init(p.a, p.lda, m0, p.M, first);
     sb.init(p.b, p.ldb, n0, p.N, first);
-    Reader<C::BM, AKC, ES, kSlice> ra;
-    Reader<C::BN, BKC, ES, kSlice> rb;
+    Reader<C::BM, AKC, ES> ra;
+    Reader<C::BN, BKC, ES> rb;
     ra.init(wm * C::TM);
     rb.init(wn * C::TN);
 
@@ -366,12 +411,8 @@ k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
     // quarter s of a slice: half-slice s / 2 of K, half s % 2 of the wave's rows
     auto read = [&](const uint8_t* st, auto s_) {
         constexpr int s = decltype(s_)::value;
-#pragma unroll
-        for (int i = 0; i < C::FH; ++i) fa[s % 2][i] = ra.template read<V>(st, s / 2, (s % 2) * C::FH + i);
-        if constexpr (s % 2 == 0) {
-#pragma unroll
-            for (int j = 0; j < C::FN; ++j) fb[s / 2][j] = rb.template read<V>(st + C::BM * kSlice, s / 2, j);
-        }
+        ra.read(st, s / 2, (s % 2) * C::FH, fa[s % 2]);
+        if constexpr (s % 2 == 0) rb.read(st + C::BM * kSlice, s / 2, 0, fb[s / 2]);
     };
     auto mul = [&](auto s_) {
         constexpr int s = decltype(s_)::value;
@@ -498,13 +539,13 @@ k_mma_turns(const Product p, int m_tiles, int n_tiles, int splits) {
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const int wm = wave / C::WN, wn = wave % C::WN;
     const bool second = __builtin_amdgcn_readfirstlane(wave) >= 4;    // (SIMD i has waves i and i + 4)
-    Side<C::BM, AKC, ES, C::NW, kSlice> sa;
-    Side<C::BN, BKC, ES, C::NW, kSlice> sb;
+    Side<C::BM, AKC, ES, C::NW> sa;
+    Side<C::BN, BKC, ES, C::NW> sb;
     sa.init(p.a, p.lda, m0, p.M, first);
     sb.init(p.b, p.ldb, n0, p.N, first);
     constexpr int kLoads = decltype(sb)::Q;                   // a wave's loads of B of a slice
-    Reader<C::BM, AKC, ES, kSlice> ra;
-    Reader<C::BN, BKC, ES, kSlice> rb;
+    Reader<C::BM, AKC, ES> ra;
+    Reader<C::BN, BKC, ES> rb;
     ra.init(wm * C::TM);
     rb.init(wn * C::TN);
     Acc acc[C::FM][C::FN];
@@ -543,12 +584,13 @@ k_mma_turns(const Product p, int m_tiles, int n_tiles, int splits) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             V fa[C::FM], fb[C::FN];
-#pragma unroll
-            for (int i = 0; i < C::FN; ++i) fb[i] = rb.template read<V>(pb, half, i);
-#pragma unroll
-            for (int i = 0; i < C::FM; ++i) fa[i] = ra.template read<V>(pa, half, i);
+            // (reads that the compiler waits for later, loads, then reads with their wait)
+            if (AKC) ra.read(pa, half, 0, fa);
+            if (BKC) rb.read(pb, half, 0, fb);
             if (half == 0 && j + 1 < n) issue_a(u + 3);
             if (half == 1 && j + 2 < n) issue_b(u + 4);
+            if (!AKC) ra.read(pa, half, 0, fa);
+            if (!BKC) rb.read(pb, half, 0, fb);
             // slice j + 1 has landed at the end of the slice's last turn: a reading turn of the
             // second group, a computing turn of the first
             if (half == 1 && second) landed(j + 2 < n, AlsoLds{});
