@@ -194,6 +194,32 @@ __device__ __forceinline__ void read_transposed(const uint32_t (&at)[8], s16x4 (
                  : "memory");
 }
 
+// The same of two operands at once: 8 fragments of the one, 4 of the other.
+template <int OFF, int OFF2>
+__device__ __forceinline__ void read_transposed(const uint32_t (&at)[8], s16x4 (&lo)[8], s16x4 (&hi)[8],
+                                                const uint32_t (&at2)[4], s16x4 (&lo2)[4], s16x4 (&hi2)[4]) {
+    asm volatile("ds_read_b64_tr_b16 %0, %24\n\tds_read_b64_tr_b16 %1, %24 offset:%36\n\t"
+                 "ds_read_b64_tr_b16 %2, %25\n\tds_read_b64_tr_b16 %3, %25 offset:%36\n\t"
+                 "ds_read_b64_tr_b16 %4, %26\n\tds_read_b64_tr_b16 %5, %26 offset:%36\n\t"
+                 "ds_read_b64_tr_b16 %6, %27\n\tds_read_b64_tr_b16 %7, %27 offset:%36\n\t"
+                 "ds_read_b64_tr_b16 %8, %28\n\tds_read_b64_tr_b16 %9, %28 offset:%36\n\t"
+                 "ds_read_b64_tr_b16 %10, %29\n\tds_read_b64_tr_b16 %11, %29 offset:%36\n\t"
+                 "ds_read_b64_tr_b16 %12, %30\n\tds_read_b64_tr_b16 %13, %30 offset:%36\n\t"
+                 "ds_read_b64_tr_b16 %14, %31\n\tds_read_b64_tr_b16 %15, %31 offset:%36\n\t"
+                 "ds_read_b64_tr_b16 %16, %32\n\tds_read_b64_tr_b16 %17, %32 offset:%37\n\t"
+                 "ds_read_b64_tr_b16 %18, %33\n\tds_read_b64_tr_b16 %19, %33 offset:%37\n\t"
+                 "ds_read_b64_tr_b16 %20, %34\n\tds_read_b64_tr_b16 %21, %34 offset:%37\n\t"
+                 "ds_read_b64_tr_b16 %22, %35\n\tds_read_b64_tr_b16 %23, %35 offset:%37\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]),
+                   "=&v"(lo[3]), "=&v"(hi[3]), "=&v"(lo[4]), "=&v"(hi[4]), "=&v"(lo[5]), "=&v"(hi[5]),
+                   "=&v"(lo[6]), "=&v"(hi[6]), "=&v"(lo[7]), "=&v"(hi[7]), "=&v"(lo2[0]), "=&v"(hi2[0]),
+                   "=&v"(lo2[1]), "=&v"(hi2[1]), "=&v"(lo2[2]), "=&v"(hi2[2]), "=&v"(lo2[3]), "=&v"(hi2[3])
+                 : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]),
+                   "v"(at[6]), "v"(at[7]), "v"(at2[0]), "v"(at2[1]), "v"(at2[2]), "v"(at2[3]), "n"(OFF), "n"(OFF2)
+                 : "memory");
+}
+
 // This lane's fragment reads of one operand: rows x0 + 16 i + lane % 16 of the tile.
 template <int X, bool KC, int ES>
 struct Reader {
@@ -218,6 +244,22 @@ struct Reader {
             f = chunk_swz<X, ES>(k) >> 2;
         }
     }
+    // transposing reads: LDS offsets of fragments first .. first + N - 1, the offset of their
+    // second halves, and the halves as one fragment
+    static constexpr int kSecond = 4 * X * 2;
+    template <int N>
+    __device__ __forceinline__ void offsets(const uint8_t* lds, int half, int first, uint32_t (&from)[N]) const {
+        const uint32_t base = uint32_t(reinterpret_cast<uintptr_t>((lds_void*)(lds + at[half])));
+#pragma unroll
+        for (int i = 0; i < N; ++i) from[i] = base + (uint32_t((unit + first + i) ^ f) << 5);
+    }
+    template <int N, class V>
+    static __device__ __forceinline__ void join(const s16x4 (&lo)[N], const s16x4 (&hi)[N], V (&v)[N]) {
+        typedef __attribute__((ext_vector_type(8))) short s16x8;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = __builtin_bit_cast(V, __builtin_shufflevector(lo[i], hi[i], 0, 1, 2, 3, 4, 5, 6, 7));
+    }
     // fragments first .. first + N - 1 of half-slice `half`
     template <int N, class V>
     __device__ __forceinline__ void read(const uint8_t* lds, int half, int first, V (&v)[N]) const {
@@ -225,16 +267,11 @@ struct Reader {
 #pragma unroll
             for (int i = 0; i < N; ++i) v[i] = *reinterpret_cast<const V*>(lds + at[half] + (first + i) * 16 * kSlice);
         } else if constexpr (ES == 2) {
-            const uint32_t base = uint32_t(reinterpret_cast<uintptr_t>((lds_void*)(lds + at[half])));
             uint32_t from[N];
             s16x4 lo[N], hi[N];
-#pragma unroll
-            for (int i = 0; i < N; ++i) from[i] = base + (uint32_t((unit + first + i) ^ f) << 5);
-            read_transposed<4 * X * 2>(from, lo, hi);
-            typedef __attribute__((ext_vector_type(8))) short s16x8;
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                v[i] = __builtin_bit_cast(V, __builtin_shufflevector(lo[i], hi[i], 0, 1, 2, 3, 4, 5, 6, 7));
+            offsets(lds, half, first, from);
+            read_transposed<kSecond>(from, lo, hi);
+            join(lo, hi, v);
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -519,30 +556,28 @@ struct Turns {
 
 template <int TYPE, int LAYOUT, int EPI>
 __global__ void __launch_bounds__(Turns::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
-k_mma_turns(const Product p, int m_tiles, int n_tiles, int splits) {
+k_mma_turns(const Product p, int m_tiles, int n_tiles) {
     typedef Turns C;
     typedef typename Frag<TYPE>::V V;
     typedef typename Frag<TYPE>::Acc Acc;
     constexpr int ES = Frag<TYPE>::ES, KS = kSlice / ES;
     constexpr bool AKC = LAYOUT != kTN, BKC = LAYOUT == kNT;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    const int tiles = m_tiles * n_tiles, total = tiles * splits, per = (total + kXcds - 1) / kXcds;
-    const int lid = int(blockIdx.x % kXcds) * per + int(blockIdx.x / kXcds);
-    if (int(blockIdx.x / kXcds) >= per || lid >= total) return;
-    const int split = lid / tiles, tile = lid % tiles;
+    const int tiles = m_tiles * n_tiles, per = (tiles + kXcds - 1) / kXcds;
+    const int tile = int(blockIdx.x % kXcds) * per + int(blockIdx.x / kXcds);
+    if (int(blockIdx.x / kXcds) >= per || tile >= tiles) return;
     const int2 mn = tile_origin(tile, m_tiles, n_tiles);
     const int64_t m0 = int64_t(mn.x) * C::BM;
     const int n0 = mn.y * C::BN;
-    const int all = (p.K + KS - 1) / KS, share = (all + splits - 1) / splits;
-    const int first = split * share, n = min(share, all - first);
+    const int n = (p.K + KS - 1) / KS;                        // slices
 
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const int wm = wave / C::WN, wn = wave % C::WN;
     const bool second = __builtin_amdgcn_readfirstlane(wave) >= 4;    // (SIMD i has waves i and i + 4)
     Side<C::BM, AKC, ES, C::NW> sa;
     Side<C::BN, BKC, ES, C::NW> sb;
-    sa.init(p.a, p.lda, m0, p.M, first);
-    sb.init(p.b, p.ldb, n0, p.N, first);
+    sa.init(p.a, p.lda, m0, p.M, 0);
+    sb.init(p.b, p.ldb, n0, p.N, 0);
     constexpr int kLoads = decltype(sb)::Q;                   // a wave's loads of B of a slice
     Reader<C::BM, AKC, ES> ra;
     Reader<C::BN, BKC, ES> rb;
@@ -554,7 +589,7 @@ k_mma_turns(const Product p, int m_tiles, int n_tiles, int splits) {
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) acc[i][j] = Acc{0, 0, 0, 0};
 
-    int left_a = p.K - first * KS, left_b = left_a;           // k from the next slice to request on
+    int left_a = p.K, left_b = left_a;           // k from the next slice to request on
     auto place = [&](int u) { return lds + (u >= C::kPlaces ? u - C::kPlaces : u) * C::PLACE; };
     auto issue_a = [&](int u) {
         sa.issue(place(u), left_a);
@@ -589,8 +624,18 @@ k_mma_turns(const Product p, int m_tiles, int n_tiles, int splits) {
             if (BKC) rb.read(pb, half, 0, fb);
             if (half == 0 && j + 1 < n) issue_a(u + 3);
             if (half == 1 && j + 2 < n) issue_b(u + 4);
-            if (!AKC) ra.read(pa, half, 0, fa);
-            if (!BKC) rb.read(pb, half, 0, fb);
+            if constexpr (!AKC && !BKC && ES == 2) {          // one wait for both
+                uint32_t ta[C::FM], tb[C::FN];
+                s16x4 la[C::FM], ha[C::FM], lb[C::FN], hb[C::FN];
+                ra.offsets(pa, half, 0, ta);
+                rb.offsets(pb, half, 0, tb);
+                read_transposed<decltype(rb)::kSecond, decltype(ra)::kSecond>(tb, lb, hb, ta, la, ha);
+                ra.join(la, ha, fa);
+                rb.join(lb, hb, fb);
+            } else {
+                if (!AKC) ra.read(pa, half, 0, fa);
+                if (!BKC) rb.read(pb, half, 0, fb);
+            }
             // slice j + 1 has landed at the end of the slice's last turn: a reading turn of the
             // second group, a computing turn of the first
             if (half == 1 && second) landed(j + 2 < n, AlsoLds{});
@@ -609,13 +654,7 @@ k_mma_turns(const Product p, int m_tiles, int n_tiles, int splits) {
     }
     if (!second) fence_barrier();
 
-    const int64_t mw = m0 + wm * C::TM;
-    const int nw = n0 + wn * C::TN;
-    if (splits > 1)
-        finish_tile<TYPE, EPI, C, true>(p, mw, nw, acc, lds,
-                                        static_cast<typename Elem<TYPE>::Acc*>(p.part) + split * p.M * part_ld(p), part_ld(p));
-    else
-        finish_tile<TYPE, EPI, C, false>(p, mw, nw, acc, lds, nullptr, 0);
+    finish_tile<TYPE, EPI, C, false>(p, m0 + wm * C::TM, n0 + wn * C::TN, acc, lds, nullptr, 0);
 }
 
 // Adds the splits' partial sums, in order, and finishes: 8 columns (or 8 pairs) of a row a thread.
@@ -667,7 +706,7 @@ hipError_t launch(const Product& p, int splits, hipStream_t s) {
     const int64_t grid = (mt * nt * splits + kXcds - 1) / kXcds * kXcds;
     if constexpr (TURNS)
         hipLaunchKernelGGL((k_mma_turns<TYPE, LAYOUT, EPI>), dim3(unsigned(grid)), dim3(C::kThreads), C::kLdsBytes, s, p,
-                           int(mt), int(nt), splits);
+                           int(mt), int(nt));
     else
         hipLaunchKernelGGL((k_mma<TYPE, LAYOUT, EPI, C>), dim3(unsigned(grid)), dim3(C::kThreads), C::kLdsBytes, s, p,
                            int(mt), int(nt), splits);
@@ -701,7 +740,8 @@ Choice plan(const Product& p, int es, int64_t n_cu) {
         const int64_t tiles = (p.M + k.bm - 1) / k.bm * ((p.N + k.bn - 1) / k.bn);
         for (int sp = 1; sp <= 32 && sp * 4 <= (nk > 4 ? nk : 4); sp *= 2) {
             const int64_t sums = p.M * part_ld(p) * sp, share = (nk + sp - 1) / sp;
-            if (sp > 1 && sums * 4 > p.part_bytes) break;
+            // (256-tiles that could be split and still fill the chip would need more scratch)
+            if (sp > 1 && (sums * 4 > p.part_bytes || c == 0)) break;
             if (share * (sp - 1) >= nk) break;               // every split has slices
             const int64_t groups = tiles * sp, rounds = (groups + n_cu * k.slots - 1) / (n_cu * k.slots);
             const int64_t on_cu = (groups + n_cu - 1) / n_cu < k.slots ? (groups + n_cu - 1) / n_cu : k.slots;

@@ -309,6 +309,80 @@ def test_block(B, T, H, I, w):
     _check("dwd", f64(dd), ref_dd, bounds["dwd"])
 
 
+@pytest.mark.parametrize("T,H,I", [(4100, 4160, 4128), (2600, 8192, 2080)])
+def test_block_large(B, T, H, I):
+    """Sizes that fill the chip with the largest tiles, with edges in each dimension: 48 rows of y
+    and dx, and the gradients of 48 inner indices, against the formulas."""
+    rng = np.random.default_rng(T)
+    x, dy, wg, wu, wd = _block_inputs(rng, T, H, I, BF16)
+    with Ctx(B, H, I, BF16) as c:
+        blob = _blob(B, c, wg, wu, wd)
+        work = torch.full((B.moe_dense_workspace_bytes(c.cfg, T),), 0xFF, dtype=torch.uint8, device="cuda")
+        save = torch.full((B.moe_dense_save_bytes(c.cfg, T),), 0xFF, dtype=torch.uint8, device="cuda")
+        y, dx = Guarded(T * H, torch.bfloat16), Guarded(T * H, torch.bfloat16)
+        grad = Guarded(blob.numel(), torch.uint8)
+        B.moe_dense_ffn(c.p, x, T, blob, save, y.t, work)
+        B.moe_dense_ffn_backward(c.p, dy, x, T, blob, save, dx.t, grad.t, work)
+        torch.cuda.synchronize()
+        for g in (y, dx, grad):
+            g.check()
+        assert torch.isfinite(y.t.float()).all() and torch.isfinite(dx.t.float()).all()
+        gu, d = _views(grad.t, H, I, torch.bfloat16)
+        assert torch.isfinite(gu.float()).all() and torch.isfinite(d.float()).all()
+    rows = np.unique(np.r_[0, 255, 256, T - 1, rng.integers(0, T, 44)])
+    r = torch.from_numpy(rows).cuda()
+    args = [f64(t) for t in (x[r], wg, wu, wd)]
+    bounds = D.block_bounds(f64(dy[r]), *args, "bf16")
+    _check("y", f64(y.t.view(T, H)[r]), D.block(*args)[0], bounds["y"])
+    _check("dx", f64(dx.t.view(T, H)[r]), D.block_backward(f64(dy[r]), *args)[0], bounds["dx"])
+    inner = np.unique(np.r_[0, 127, 128, I - 1, rng.integers(0, I, 44)])
+    k = torch.from_numpy(inner).cuda()
+    args = [f64(t) for t in (x, wg[k], wu[k], wd[:, k].contiguous())]
+    bounds = D.block_bounds(f64(dy), *args, "bf16")
+    _, rg, ru, rd = D.block_backward(f64(dy), *args)
+    at = k // 16 * 32 + k % 16
+    _check("dwg", f64(gu[at]), rg, bounds["dwg"])
+    _check("dwu", f64(gu[at + 16]), ru, bounds["dwu"])
+    _check("dwd", f64(d[:, k]), rd, bounds["dwd"])
+
+
+@pytest.mark.parametrize("T,N,K,y_type", [(4100, 4099, 4112, BF16), (4097, 8195, 144, F32), (8200, 2056, 1040, BF16)])
+def test_i8_matmul_large(B, T, N, K, y_type):
+    rng = np.random.default_rng(T + N)
+    x = normal(rng, (T, K), BF16)
+    wq = rng.integers(-128, 128, (N, K), dtype=np.int8)
+    ws = (rng.random(N) * 0.01 + 1e-4).astype(np.float32)
+    with Ctx(B) as c:
+        got = f64(_matmul(B, c, x, BF16, K, None, T, torch.from_numpy(wq).cuda(), torch.from_numpy(ws).cuda(), N, K, y_type, N))
+    rows = np.unique(np.r_[0, 255, 256, T - 1, rng.integers(0, T, 60)])
+    ref = D.i8_matmul(*D.quantize_rows(f64(x)[rows]), wq, ws)
+    _check("y", got[rows], ref, D.i8_bound(ref, NAME[y_type]))
+    cols = np.unique(np.r_[0, 255, 256, N - 1, rng.integers(0, N, 30)])
+    ref = D.i8_matmul(*D.quantize_rows(f64(x)), wq[cols], ws[cols])
+    _check("y", got[:, cols], ref, D.i8_bound(ref, NAME[y_type]))
+
+
+def test_i8_block_large(B):
+    """Every row of the 8-bit block at sizes of the largest tiles: relative error in the 2-norm.
+    The result's rounding is 2^-8 of each value at most; codes that differ are few (h's quotient
+    within 2^-10 of a border) and move a row by less than 2^-8 of its norm."""
+    T, H, I = 4100, 2112, 4128
+    rng = np.random.default_rng(6)
+    x, _, wg, wu, wd = _block_inputs(rng, T, H, I, BF16)
+    with Ctx(B, H, I) as c:
+        b8 = torch.empty(B.moe_i8_blob_bytes(c.cfg), dtype=torch.uint8, device="cuda")
+        B.moe_i8_pack(c.p, _blob(B, c, wg, wu, wd), b8)
+        work = torch.full((B.moe_dense_workspace_bytes(c.cfg, T),), 0xFF, dtype=torch.uint8, device="cuda")
+        y = Guarded(T * H, torch.bfloat16)
+        B.moe_i8_ffn(c.p, x, T, b8, y.t, work)
+        torch.cuda.synchronize()
+        y.check()
+    rows = np.unique(np.r_[0, 255, 256, T - 1, rng.integers(0, T, 120)])
+    ref, _ = D.i8_block(f64(x)[rows], *[v for w in (wg, wu, wd) for v in D.quantize_rows(f64(w))])
+    err = np.linalg.norm(f64(y.t).reshape(T, H)[rows] - ref, axis=1) / np.linalg.norm(ref, axis=1)
+    assert (err <= 2.0 ** -7).all(), err.max()
+
+
 @pytest.mark.parametrize("w", [BF16, F32])
 def test_block_backward_partial_outputs(B, w):
     """dx alone, the weights' gradient alone: the same bits as both together, and nothing else
