@@ -174,7 +174,7 @@ int moe_i8_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, c
     p.K = K;
     p.out = d_y;
     p.ldo = ld_y;
-    p.vec_out = aligned(d_y, 16) && ld_y % 8 == 0;
+    p.vec_out = y_type == MOE_A_F32 || (aligned(d_y, 4) && ld_y % 2 == 0);
     p.col_scale = d_w_scale;
     const int epi = y_type == MOE_A_F32 ? kScale32 : kScale;
     hipError_t e = on_the_way ? launch_few(kI8, epi, p, s, x_type, true) : launch_product(kI8, kNT, epi, p, s);

@@ -36,7 +36,7 @@ struct Product {
     int32_t N, K;
     void* out;
     int64_t ldo;                // elements between rows of out
-    int32_t vec_out;            // kScale, kScale32: out and its rows are 16-byte aligned for 8 values
+    int32_t vec_out;            // kScale, kScale32: every even column lies on 4 bytes
     const float* row_scale;     // integer products
     const float* col_scale;
     void* part;                 // scratch for partial sums of part_bytes (0: none)

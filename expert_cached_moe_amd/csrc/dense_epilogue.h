@@ -11,25 +11,29 @@ namespace dense {
 
 typedef __attribute__((ext_vector_type(4))) int i32x4;
 
-// W values to p[0 .. W-1], 4 (fp32) or W (bf16) at a time.  STREAM: past the caches, for results
+// Four 32-bit words that lie on a 4-byte boundary: enough for a 16-byte store to memory.
+typedef uint32_t __attribute__((ext_vector_type(4), aligned(4))) words4;
+typedef uint32_t __attribute__((ext_vector_type(2), aligned(4))) words2;
+
+// W values to p[0 .. W-1], 4 (fp32) or W (bf16, on a 4-byte boundary) at a time.  STREAM: past the caches, for results
 // that leave as whole lines and are not read by the next kernel.
 template <int W, bool STREAM = false>
 __device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[W]) {
     if constexpr (W == 8) {
         const dev::u32x4 u{dev::pack_bf16x2(v[0], v[1]), dev::pack_bf16x2(v[2], v[3]), dev::pack_bf16x2(v[4], v[5]),
                            dev::pack_bf16x2(v[6], v[7])};
-        if (STREAM) __builtin_nontemporal_store(u, reinterpret_cast<dev::u32x4*>(p));
-        else *reinterpret_cast<dev::u32x4*>(p) = u;
+        if (STREAM) __builtin_nontemporal_store(words4(u), reinterpret_cast<words4*>(p));
+        else *reinterpret_cast<words4*>(p) = u;
     } else
-        *reinterpret_cast<uint2*>(p) = make_uint2(dev::pack_bf16x2(v[0], v[1]), dev::pack_bf16x2(v[2], v[3]));
+        *reinterpret_cast<words2*>(p) = words2{dev::pack_bf16x2(v[0], v[1]), dev::pack_bf16x2(v[2], v[3])};
 }
 template <int W, bool STREAM = false>
 __device__ __forceinline__ void store_row(float* p, const float (&v)[W]) {
 #pragma unroll
     for (int q = 0; q < W; q += 4) {
-        const dev::f32x4 u{v[q], v[q + 1], v[q + 2], v[q + 3]};
-        if (STREAM) __builtin_nontemporal_store(u, reinterpret_cast<dev::f32x4*>(p + q));
-        else *reinterpret_cast<dev::f32x4*>(p + q) = u;
+        const words4 u = __builtin_bit_cast(dev::u32x4, dev::f32x4{v[q], v[q + 1], v[q + 2], v[q + 3]});
+        if (STREAM) __builtin_nontemporal_store(u, reinterpret_cast<words4*>(p + q));
+        else *reinterpret_cast<words4*>(p + q) = u;
     }
 }
 template <int W>

@@ -657,36 +657,36 @@ k_mma_turns(const Product p, int m_tiles, int n_tiles) {
     finish_tile<TYPE, EPI, C, false>(p, m0 + wm * C::TM, n0 + wn * C::TN, acc, lds, nullptr, 0);
 }
 
-// Adds the splits' partial sums, in order, and finishes: 8 columns (or 8 pairs) of a row a thread.
+// Adds the splits' partial sums, in order, and finishes: 4 columns (or 4 pairs) of a row a thread.
 template <int TYPE, int EPI>
 __global__ void __launch_bounds__(256) k_join(const Product p, int splits) {
     typedef typename Elem<TYPE>::Acc S;
     typedef typename Frag<TYPE>::Acc V4;
     constexpr bool PAIR = kPaired<EPI>;
-    const int64_t ld = part_ld(p), units = PAIR ? p.N / 16 : ld / 8, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t ld = part_ld(p), units = PAIR ? p.N / 8 : ld / 4, i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i >= p.M * units) return;
     const int64_t m = i / units;
-    const int k = int(i % units), n = PAIR ? k / 2 * 32 + k % 2 * 8 : k * 8;
-    ColumnScales<EPI, 8> cs;
+    const int k = int(i % units), n = PAIR ? k / 4 * 32 + k % 4 * 4 : k * 4;
+    if (n >= p.N) return;
+    ColumnScales<EPI, 4> cs;
     cs.load(p, n);
-    S v[8], u[8];
-    auto add = [&](S (&t)[8], int col) {
+    RowInputs<TYPE, EPI, 4> in;
+    in.load(p, m, n);
+    S v[4], u[4];
+    auto add = [&](S (&t)[4], int col) {
         const S* part = static_cast<const S*>(p.part) + m * ld + col;
-        V4 a = *reinterpret_cast<const V4*>(part), b = *reinterpret_cast<const V4*>(part + 4);
-#pragma unroll 4
+        V4 a = *reinterpret_cast<const V4*>(part);
+#pragma unroll 8
         for (int s = 1; s < splits; ++s) {
             part += p.M * ld;
             a += *reinterpret_cast<const V4*>(part);
-            b += *reinterpret_cast<const V4*>(part + 4);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) t[e] = a[e], t[4 + e] = b[e];
+        for (int e = 0; e < 4; ++e) t[e] = a[e];
     };
     add(v, n);
     if constexpr (PAIR) add(u, n + 16);
-    RowInputs<TYPE, EPI, 8> in;
-    in.load(p, m, n);
-    finish<TYPE, EPI, 8, false>(p, m, n, v, u, cs, in);
+    finish<TYPE, EPI, 4, false>(p, m, n, v, u, cs, in);
 }
 
 typedef Tile<128, 128, 2, 2> Mid;            // two workgroups a CU
@@ -712,8 +712,10 @@ hipError_t launch(const Product& p, int splits, hipStream_t s) {
                            int(mt), int(nt), splits);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || splits == 1) return e;
-    const int64_t items = p.M * (kPaired<EPI> ? p.N / 16 : part_ld(p) / 8);
-    hipLaunchKernelGGL((k_join<TYPE, EPI>), dim3(unsigned((items + 255) / 256)), dim3(256), 0, s, p, splits);
+    // (few results: more workgroups of one wave)
+    const int64_t items = p.M * (kPaired<EPI> ? p.N / 8 : part_ld(p) / 4);
+    const int threads = items < 256 * 1024 ? 64 : 256;
+    hipLaunchKernelGGL((k_join<TYPE, EPI>), dim3(unsigned((items + threads - 1) / threads)), dim3(threads), 0, s, p, splits);
     return hipGetLastError();
 }
 
