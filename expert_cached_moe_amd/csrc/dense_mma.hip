@@ -5,10 +5,15 @@
 // line and all types move the same bytes per slice; a fragment is 16 bytes a lane from each
 // operand: one 16x16 matrix instruction for bf16 (32 k) and for codes (64 k) in the same time,
 // four for fp32 (4 k each; which k an instruction takes does not matter while both operands
-// agree), eight times as long.  Slices are loaded straight
-// into two LDS stages by buffer loads; the one barrier of a slice stands before its last quarter,
-// so the loads of a slice have a whole slice's time to land and the matrix instructions of the
-// last quarter cover the first reads of the next slice.
+// agree), eight times as long.  Slices are loaded straight into LDS by buffer loads.
+//
+// Two kernels: k_mma_turns on 256 x 256 tiles, k_mma on 128 x 128 and 64 x 64 ones, where larger
+// tiles would leave CUs idle; with few of those, K is split over workgroups and k_join adds the
+// parts.  Measured (8,192 tokens, kernel times): 4096 outputs of 12288 in bf16 551 us, 1.50
+// PFLOP/s, the matrix units busy 80% of the cycles at 1.8 GHz, where power holds the clock;
+// gate and up of the 4096 x 12288 block 1.20 ms, 1.37 PFLOP/s; its gradients 0.69, 1.36 and
+// 1.21 ms (dWd, dWgu, dx), 1.18-1.36 PFLOP/s; 24576 outputs of 4096 in 8 bits 617 us, 2.67
+// POP/s.  A library product of 8192^3 reaches 1.45 PFLOP/s and 2.36 POP/s on the same card.
 //
 // Operands contiguous along K lie in LDS as rows of 128 bytes, 16-byte chunk c of row r at slot
 // c ^ ((r >> 1) & 7): two rows share a 256-byte window of the banks, so the 16 rows of a
@@ -20,8 +25,7 @@
 // bits 2 and 3 of k.
 //
 // The weights' operand goes first into the instruction, so a lane ends with four consecutive
-// columns of one row: gate and up sums of an inner index are in one lane, and results leave as
-// 8 or 16 bytes a lane.
+// columns of one row, and gate and up sums of an inner index are in one lane.
 //
 // Rows past M or N are read from the last row (their sums are dropped), and the part of the last
 // slice past K is zeros: a buffer load whose offset is out of range writes zeros to LDS.
@@ -30,6 +34,7 @@
 // groups of 8 row tiles, so the tiles in flight on an XCD share operands in its L2.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "dense_common.h"
@@ -79,11 +84,12 @@ __device__ __forceinline__ i32x4 mma(const i32x4& a, const i32x4& b, const i32x4
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
-// permutation of the 32-byte units of row k of an operand that is not contiguous along K: rows
-// of 256 bytes and more all start on the same bank and have 8 units to permute; rows of 128
-// bytes (X = 64) alternate between the halves of the banks and have 4
+// permutation (of 16-byte chunks, by whole 32-byte units) of row k of an operand that is not
+// contiguous along K: rows of 256 bytes and more all start on the same bank and have 8 units to
+// permute; rows of 128 bytes (X = 64) alternate between the halves of the banks and have 4.
+// fp32: by 64-byte units.
 template <int X, int ES>
-__device__ __forceinline__ int chunk_swz(int k) {         // for 16-byte chunks
+__device__ __forceinline__ int chunk_swz(int k) {
     if (ES == 4) return ((k >> 2) & 3) << 2;
     return (X == 64 ? ((k >> 1) & 1) | ((k >> 2) & 2) : (k & 3) | ((k >> 1) & 4)) << 1;
 }
@@ -297,7 +303,7 @@ struct Tile {
     static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16, FH = FM / 2;
     static constexpr int kFinishRow = TN * 4 + 16, kFinishBytes = NW * 2 * 16 * kFinishRow;
     static constexpr int STAGE = (BM + BN) * kSlice, kLdsBytes = 2 * STAGE;
-    static_assert(kLdsBytes >= kFinishBytes, "room for the results");
+    static_assert(kLdsBytes >= kFinishBytes && kLdsBytes <= 64 * 1024, "room for the results");
     static constexpr int kWavesPerSimd = NW * (160 * 1024 / kLdsBytes) / 4 < 2 ? 1 : 2;
     static_assert(FH * 32 == TM && FN * 16 == TN && FN % 2 == 0, "fragments");
 };
@@ -404,9 +410,12 @@ __device__ __forceinline__ void finish_tile(const Product& p, int64_t m0, int n0
     }
 }
 
-// Elements between the rows of a partial sum (a multiple of 8 from N up) and of one split.
+// Elements between the rows of a partial sum: a multiple of 8 from N up.
 __host__ __device__ inline int64_t part_ld(const Product& p) { return (int64_t(p.N) + 7) / 8 * 8; }
 
+// 128 x 128 and 64 x 64 tiles: 4 waves, two LDS stages.  The one barrier of a slice stands before
+// its last quarter, so the loads of a slice have a whole slice's time to land and the matrix
+// instructions of the last quarter cover the first reads of the next slice.
 template <int TYPE, int LAYOUT, int EPI, class C>
 __global__ void __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::kWavesPerSimd)))
 k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
@@ -460,9 +469,12 @@ k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
                 acc[(s % 2) * C::FH + i][j] = mma(fb[s / 2][j], fa[s % 2][i], acc[(s % 2) * C::FH + i][j]);
     };
     // matrix instructions of one quarter with the NR LDS reads of the next spread among them
+    // (transposing reads wait for themselves)
+    constexpr bool kHinted = (AKC && BKC) || ES != 2;
     auto sched = [&](auto nr_) {
         constexpr int NR = decltype(nr_)::value, NM = C::FH * C::FN * (TYPE == kF32 ? 4 : 1);
         constexpr int PAIRS = NR < NM ? NR : NM;
+        if constexpr (!kHinted) return;
 #pragma unroll
         for (int n = 0; n < PAIRS; ++n) {
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
@@ -589,7 +601,7 @@ k_mma_turns(const Product p, int m_tiles, int n_tiles) {
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) acc[i][j] = Acc{0, 0, 0, 0};
 
-    int left_a = p.K, left_b = left_a;           // k from the next slice to request on
+    int left_a = p.K, left_b = p.K;                           // k from the next slice to request on
     auto place = [&](int u) { return lds + (u >= C::kPlaces ? u - C::kPlaces : u) * C::PLACE; };
     auto issue_a = [&](int u) {
         sa.issue(place(u), left_a);
@@ -692,24 +704,35 @@ __global__ void __launch_bounds__(256) k_join(const Product p, int splits) {
 typedef Tile<128, 128, 2, 2> Mid;            // two workgroups a CU
 typedef Tile<64, 64, 2, 2> Small;            // four
 
+// Lets a kernel use more than 64 KiB of LDS, once on each device.
+hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 template <int TYPE, int LAYOUT, int EPI, class C>
 hipError_t launch(const Product& p, int splits, hipStream_t s) {
     const int64_t mt = (p.M + C::BM - 1) / C::BM, nt = (p.N + C::BN - 1) / C::BN;
     if (mt * nt * splits > 0x7FFFFFF0 / kXcds) return hipErrorInvalidValue;
     if (splits > 1 && p.M * part_ld(p) * splits * 4 > p.part_bytes) return hipErrorInvalidValue;
-    constexpr bool TURNS = std::is_same<C, Turns>::value;
-    const void* f;
-    if constexpr (TURNS) f = reinterpret_cast<const void*>(&k_mma_turns<TYPE, LAYOUT, EPI>);
-    else f = reinterpret_cast<const void*>(&k_mma<TYPE, LAYOUT, EPI, C>);
-    static const hipError_t lds_ok = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, C::kLdsBytes);
-    if (lds_ok != hipSuccess) return lds_ok;
-    const int64_t grid = (mt * nt * splits + kXcds - 1) / kXcds * kXcds;
-    if constexpr (TURNS)
-        hipLaunchKernelGGL((k_mma_turns<TYPE, LAYOUT, EPI>), dim3(unsigned(grid)), dim3(C::kThreads), C::kLdsBytes, s, p,
-                           int(mt), int(nt));
-    else
-        hipLaunchKernelGGL((k_mma<TYPE, LAYOUT, EPI, C>), dim3(unsigned(grid)), dim3(C::kThreads), C::kLdsBytes, s, p,
-                           int(mt), int(nt), splits);
+    const unsigned grid = unsigned((mt * nt * splits + kXcds - 1) / kXcds * kXcds);
+    if constexpr (std::is_same<C, Turns>::value) {
+        const auto kernel = &k_mma_turns<TYPE, LAYOUT, EPI>;
+        static std::atomic<uint64_t> allowed{0};
+        hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), C::kLdsBytes, allowed);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(kernel, dim3(grid), dim3(C::kThreads), C::kLdsBytes, s, p, int(mt), int(nt));
+        return hipGetLastError();
+    } else {
+        hipLaunchKernelGGL((k_mma<TYPE, LAYOUT, EPI, C>), dim3(grid), dim3(C::kThreads), C::kLdsBytes, s, p, int(mt),
+                           int(nt), splits);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || splits == 1) return e;
     // (few results: more workgroups of one wave)
@@ -722,10 +745,10 @@ hipError_t launch(const Product& p, int splits, hipStream_t s) {
 // Tile and split of K: the least of the times that a model fitted to measurements gives, in us.
 // A slice takes `slice` and `more` for each further workgroup on its CU (up to `slots`), a tile
 // `tile` to start and finish; a split costs a second kernel and its partial sums both ways.
-// Measured (8-bit codes, whole call): 300 x 4096 x 4096: 256-tiles 40 us, 128 20, 64 13.6, 128
-// split in two 23; 2000 x 4096 x 4096: 45, 34, 50; 1024 x 8192 x 8192: 72, 63, 93; 100 x 8192 x
-// 4096: 64-tiles 19, split in two 16.6, in eight 21.  Three and more slices in flight instead of
-// two changed none of them by more than a few percent.  fp32: eight times the matrix time.
+// Measured (8-bit codes, whole call): 300 x 4096 x 4096: 256-tiles 40 us, 128 20, 64 13, 128
+// split in two 23; 2000 x 4096 x 4096: 44, 34, 50; 1024 x 8192 x 8192: 74, 63, 94; 100 x 8192 x
+// 4096: 64-tiles 19, split in two 16.6, in eight 21.  fp32: eight times the matrix time.  Four
+// stages instead of two on the smaller tiles, and 256 x 128 tiles in turns, gained nothing.
 struct Choice {
     int tile, splits;
 };
