@@ -1,6 +1,7 @@
 // Entry points of the dense operators: 8-bit integer products, and the dense gated block with
 // its backward pass and its 8-bit form.  Contracts in include/moe.h; the kernels are in
-// dense_quant.hip and dense_gemm.hip.
+// dense_quant.hip, dense_few.hip and
+// dense_mma.hip.
 #include <hip/hip_runtime.h>
 
 #include "dense.h"
@@ -14,7 +15,8 @@ std::atomic<int> g_units[64];
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// Workspace of moe_i8_matmul: codes and scales of x.
+// Workspace of moe_i8_matmul: codes and scales of x, and partial sums of calls with few tokens
+// (more than kSplitTokens fill the chip unsplit).
 constexpr int64_t kSplitTokens = 1024;
 struct I8Work {
     int64_t codes = 0, scale = 0, part = 0, bytes = 0;
@@ -24,7 +26,6 @@ I8Work i8_work(int64_t T, int64_t K) {
     if (T < 1) T = 1;
     w.scale = align256(T * K);
     w.part = align256(w.scale + T * 4);
-    // (more tokens fill the chip unsplit)
     w.bytes = w.part + (T > kSplitTokens ? 0 : kPartBytes);
     return w;
 }
@@ -69,9 +70,11 @@ Blob8 blob8_layout(const moe_config& c) {
 }
 
 constexpr int kMaxWidth = 1 << 20;    // H and I: row offsets inside a tile stay below 2 GiB
+constexpr int kMaxCount = 1 << 24;    // tokens, outputs, columns: the threads of a launch fit 32 bits
 
 int check_block(moe_ctx* ctx, int32_t T, bool i8) {
     if (T < 0) return fail(ctx, MOE_EINVAL, "T < 0");
+    if (T > kMaxCount) return fail(ctx, MOE_ESHAPE, "T above 2^24");
     if (ctx->cfg.hidden > kMaxWidth || ctx->cfg.inter > kMaxWidth)
         return fail(ctx, MOE_ESHAPE, "the dense block takes H and I up to 2^20");
     if (i8 && ctx->cfg.w_dtype != MOE_W_BF16)
@@ -114,7 +117,9 @@ extern "C" {
 int64_t moe_i8_workspace_bytes(int32_t max_T, int32_t K) {
     if (max_T < 0) return MOE_EINVAL;
     if (K < 16 || K % 16 || K > kMaxKI8) return MOE_ESHAPE;
-    return i8_work(max_T, K).bytes;
+    // (fewer tokens may need more: the partial sums)
+    const int64_t most = i8_work(max_T, K).bytes, few = i8_work(max_T < kSplitTokens ? max_T : kSplitTokens, K).bytes;
+    return most > few ? most : few;
 }
 
 int moe_i8_quantize(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, int32_t rows, int32_t cols,
@@ -122,7 +127,8 @@ int moe_i8_quantize(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x,
     if (!ctx) return MOE_EINVAL;
     if (rows < 0) return fail(ctx, MOE_EINVAL, "rows < 0");
     if (x_type != MOE_A_F32 && x_type != MOE_A_BF16) return fail(ctx, MOE_EINVAL, "x must be fp32 or bf16");
-    if (cols < 16 || cols % 16) return fail(ctx, MOE_ESHAPE, "cols must be a positive multiple of 16");
+    if (cols < 16 || cols % 16 || cols > kMaxCount)
+        return fail(ctx, MOE_ESHAPE, "cols must be a multiple of 16 in 16..2^24");
     if (ld_x < cols) return fail(ctx, MOE_EINVAL, "ld_x < cols");
     if (rows == 0) return MOE_OK;
     if (!d_x || !d_q || !d_scale) return fail(ctx, MOE_EINVAL, "null buffer");
@@ -140,7 +146,7 @@ int moe_i8_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, c
     if (x_type != MOE_A_F32 && x_type != MOE_A_BF16 && x_type != MOE_A_I8) return fail(ctx, MOE_EINVAL, "unknown x type");
     if (y_type != MOE_A_F32 && y_type != MOE_A_BF16) return fail(ctx, MOE_EINVAL, "y must be fp32 or bf16");
     if (K < 16 || K % 16 || K > kMaxKI8) return fail(ctx, MOE_ESHAPE, "K must be a multiple of 16 in 16..131056");
-    if (N < 1) return fail(ctx, MOE_ESHAPE, "N < 1");
+    if (N < 1 || N > kMaxCount || T > kMaxCount) return fail(ctx, MOE_ESHAPE, "N in 1..2^24, T up to 2^24");
     const bool codes = x_type == MOE_A_I8;
     if (ld_x < K || (codes && ld_x != K)) return fail(ctx, MOE_EINVAL, "ld_x: at least K, and K itself for codes");
     if (ld_y < N) return fail(ctx, MOE_EINVAL, "ld_y < N");

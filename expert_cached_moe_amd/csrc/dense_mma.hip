@@ -722,6 +722,7 @@ hipError_t launch(const Product& p, int splits, hipStream_t s) {
     if (mt * nt * splits > 0x7FFFFFF0 / kXcds) return hipErrorInvalidValue;
     if (splits > 1 && p.M * part_ld(p) * splits * 4 > p.part_bytes) return hipErrorInvalidValue;
     const unsigned grid = unsigned((mt * nt * splits + kXcds - 1) / kXcds * kXcds);
+    if (int64_t(grid) * C::kThreads > 0xFFFFFFFF) return hipErrorInvalidValue;      // threads of a launch: 32 bits
     if constexpr (std::is_same<C, Turns>::value) {
         const auto kernel = &k_mma_turns<TYPE, LAYOUT, EPI>;
         static std::atomic<uint64_t> allowed{0};

@@ -336,16 +336,22 @@ int64_t moe_noalloc_scratch_bytes(void);
  * 0 and codes 0; a row that holds an infinity or a NaN has scale NaN and codes 0, so every
  * product with it is NaN.
  *
+ * Here and in the dense block below: no output may overlap an input or another output; the
+ * stream belongs to the current device; calls that share a workspace (or a save buffer) must
+ * not overlap in time, replays of captured graphs included: order them, or give each its own.
+ *
  * Scratch bytes of moe_i8_matmul for up to max_T tokens of K numbers, or a negative status. */
 int64_t moe_i8_workspace_bytes(int32_t max_T, int32_t K);
 /* Quantise `rows` rows of `cols` numbers (async on s).  d_x: MOE_A_F32 or MOE_A_BF16, rows
  * ld_x >= cols elements apart, any alignment of the element; d_q [rows][cols] codes (rows back
- * to back, 16-byte aligned, cols a multiple of 16); d_scale [rows].  rows == 0 is a no-op.
+ * to back, 16-byte aligned, cols a multiple of 16 up to 2^24); d_scale [rows].  rows == 0 is a
+ * no-op.
  * Errors: MOE_EINVAL (null, type, ld_x < cols, alignment), MOE_ESHAPE (cols). */
 int moe_i8_quantize(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, int32_t rows, int32_t cols,
                     int8_t* d_q, float* d_scale, hipStream_t s);
 /* y[t][n] = x_scale[t] * w_scale[n] * sum_k x_code[t][k] * w_code[n][k] (async on s), the sum
- * exact in 32-bit integers, the result rounded once to y_type.
+ * exact in 32-bit integers; it and its products with the scales are fp32 numbers (three
+ * roundings of 2^-24), for bf16 the result is rounded once more.
  *   d_x: MOE_A_I8: codes [T][K] back to back (ld_x = K) with d_x_scale [T]; MOE_A_F32 or
  *     MOE_A_BF16: numbers, rows ld_x >= K elements apart, quantised on the way exactly as
  *     moe_i8_quantize does (d_x_scale must be NULL; callers with several products of one x
@@ -355,8 +361,8 @@ int moe_i8_quantize(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x,
  *   d_y [T][N], rows ld_y >= N elements apart, MOE_A_F32 or MOE_A_BF16; bytes between the rows
  *     are not written;
  *   d_ws: moe_i8_workspace_bytes(max_T >= T, K), 256-byte aligned.
- * K is a multiple of 16 up to 131056 (so no sum leaves 32 bits), N >= 1, code arrays 16-byte
- * aligned.  T == 0 is a no-op.  Errors: MOE_EINVAL, MOE_ESHAPE. */
+ * K is a multiple of 16 up to 131056 (so no sum leaves 32 bits), N and T up to 2^24, N >= 1, code
+ * arrays 16-byte aligned.  T == 0 is a no-op.  Errors: MOE_EINVAL, MOE_ESHAPE. */
 int moe_i8_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, const float* d_x_scale, int32_t T,
                   const int8_t* d_w, const float* d_w_scale, int32_t N, int32_t K, void* d_y, int32_t y_type,
                   int64_t ld_y, void* d_ws, hipStream_t s);
@@ -365,7 +371,7 @@ int moe_i8_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, c
 /* One gated feed-forward block over all tokens, y = Wd (silu(Wg x) * (Wu x)), on a blob of
  * moe_pack_expert's layout (the shared expert, a dense feed-forward layer: a context whose
  * config has that width).  Contexts with fp32 or bf16 weights; H = cfg.hidden, I = cfg.inter
- * (each up to 2^20; up to 131056 for the 8-bit form),
+ * (each up to 2^20; up to 131056 for the 8-bit form), T up to 2^24,
  * activations in the weights' type.  Blob, x, y, dy, dx, save and workspace 16-byte aligned.
  *
  * Scratch bytes for up to max_T tokens of any moe_dense_* or moe_i8_ffn call. */

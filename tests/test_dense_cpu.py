@@ -99,6 +99,17 @@ def test_sizes():
         assert e.value.status == B.MOE_EINVAL
 
 
+def test_workspace_serves_fewer_tokens():
+    """A workspace for max_T tokens is enough for every T below it (calls with fewer tokens split
+    K and add partial sums)."""
+    for K in (16, 64, 4096, 131056):
+        sizes = [B.moe_i8_workspace_bytes(T, K) for T in (0, 1, 17, 64, 1023, 1024, 1025, 2048, 8192, 100000)]
+        assert sizes == sorted(sizes)
+    for cfg in (B.make_config(128, 64, 1, 1, w_dtype=w) for w in (B.MOE_W_BF16, B.MOE_W_F32)):
+        sizes = [B.moe_dense_workspace_bytes(cfg, T) for T in (0, 1, 17, 1024, 1025, 100000)]
+        assert sizes == sorted(sizes)
+
+
 def _refused(ctx, status, f, *args):
     with pytest.raises(B.MoeError) as e:
         f(ctx, *args)
@@ -180,3 +191,13 @@ def test_mxfp4_context_refused():
     _refused(ctx, B.MOE_EUNSUPPORTED, B.moe_i8_ffn, P, 3, P, P, P)
     _refused(ctx, B.MOE_EUNSUPPORTED, B.moe_i8_pack, P, P)
     B.moe_destroy(ctx)
+
+
+def test_counts_past_the_limits(ctx):
+    big = 2 ** 24 + 16
+    _refused(ctx, B.MOE_ESHAPE, B.moe_i8_quantize, P, B.MOE_A_F32, big, 1, big, P, P)
+    for T, N in ((1, big), (big, 1)):
+        _refused(ctx, B.MOE_ESHAPE, B.moe_i8_matmul, P, B.MOE_A_BF16, 64, None, T, P, P, N, 64, P, B.MOE_A_F32, N, P)
+    _refused(ctx, B.MOE_ESHAPE, B.moe_dense_ffn, P, big, P, None, P, P)
+    _refused(ctx, B.MOE_ESHAPE, B.moe_dense_ffn_backward, P, P, big, P, P, P, P, P)
+    _refused(ctx, B.MOE_ESHAPE, B.moe_i8_ffn, P, big, P, P, P)
