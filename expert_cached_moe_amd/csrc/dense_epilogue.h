@@ -143,9 +143,16 @@ struct ColumnScales {
 // row's stores (a wait for a load waits for every older store).
 template <int TYPE, int EPI, int W>
 struct RowInputs {
-    float rs, g[EPI == kDGate ? W : 1], u[EPI == kDGate ? W : 1];
+    // first * last is the row's scale.  One above 2^60 is applied last: times a sum (below 2^31) it
+    // could overflow although the column's scale brings the result back into range.
+    float first, last, g[EPI == kDGate ? W : 1], u[EPI == kDGate ? W : 1];
+    __device__ __forceinline__ void set_scale(float s) {
+        const bool big = s > 1.1529215e18f;
+        first = big ? 1.0f : s;
+        last = big ? s : 1.0f;
+    }
     __device__ __forceinline__ void load(const Product& p, int64_t m, int n) {
-        if constexpr (kScaled<EPI>) rs = p.row_scale[m];
+        if constexpr (kScaled<EPI>) set_scale(p.row_scale[m]);
         if constexpr (EPI == kDGate) {
             typedef typename Elem<TYPE>::T E;
             const int64_t i = m * 2 * p.N + n / 16 * 32 + n % 16;
@@ -170,7 +177,7 @@ __device__ __forceinline__ void finish(const Product& p, int64_t m, int n, const
         typedef typename std::conditional<EPI == kScale32, float, uint16_t>::type O;
         float f[W];
 #pragma unroll
-        for (int j = 0; j < W; ++j) f[j] = float(v[j]) * in.rs * cs.s[j];
+        for (int j = 0; j < W; ++j) f[j] = float(v[j]) * in.first * cs.s[j] * in.last;
         O* o = static_cast<O*>(p.out) + m * p.ldo + n;
         if (p.vec_out && n + W <= p.N) {
             store_row<W, STREAM>(o, f);
@@ -194,7 +201,10 @@ __device__ __forceinline__ void finish(const Product& p, int64_t m, int n, const
         // on it)
         float h[W];
 #pragma unroll
-        for (int j = 0; j < W; ++j) h[j] = silu(float(v[j]) * in.rs * cs.s[j]) * (float(u[j]) * in.rs * cs.up[j]);
+        for (int j = 0; j < W; ++j) {
+            const float g = float(v[j]) * in.first * cs.s[j] * in.last, up = float(u[j]) * in.first * cs.up[j] * in.last;
+            h[j] = silu(g) * up;
+        }
         store_row<W, STREAM>(static_cast<float*>(p.out) + m * p.ldo + n / 32 * 16 + n % 16, h);
     } else {
         // v = dh, n an inner index

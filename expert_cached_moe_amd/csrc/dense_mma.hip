@@ -397,7 +397,7 @@ __device__ __forceinline__ void finish_tile(const Product& p, int64_t m0, int n0
             }
         }
         if constexpr (!PARTIAL) {
-            if (kScaled<EPI>) ri[k & 1].rs = __shfl(scales, row_of(k), kWave);
+            if (kScaled<EPI>) ri[k & 1].set_scale(__shfl(scales, row_of(k), kWave));
             if (k + 1 < ALL) load_inputs(k + 1);
         }
         if (m >= p.M || !in) continue;

@@ -193,6 +193,25 @@ def test_i8_matmul_special_rows(B, T):
     assert not got[xs == 0].any()
 
 
+@pytest.mark.parametrize("T", [1, 6, 20, 200, 2100])
+def test_i8_matmul_far_scales(B, T):
+    """Scales of x up to 2.4e36 with scales of W near 1e-31, and small ones with large ones: sum *
+    scale leaves fp32 where sum * scale * scale does not."""
+    rng = np.random.default_rng(T)
+    K, N = 1040, 133
+    for far, near in ((3e38, 1e-31), (1e30, 1e-24), (1e-34, 1e20)):
+        x = normal(rng, (T, K), F32)
+        x *= far / x.abs().amax(1, keepdim=True)
+        wq = rng.integers(-127, 128, (N, K), dtype=np.int8)
+        ws = ((rng.random(N) + 0.5) * near).astype(np.float32)
+        with Ctx(B) as c:
+            got = f64(_matmul(B, c, x, F32, K, None, T, torch.from_numpy(wq).cuda(), torch.from_numpy(ws).cuda(), N, K,
+                              F32, N))
+        xq, xs = D.quantize_rows(f64(x))
+        ref = D.i8_matmul(xq, xs, wq, ws)
+        assert (np.abs(got - ref) <= D.i8_bound(ref, "f32")).all()
+
+
 @pytest.mark.parametrize("T", [1, 40])
 def test_i8_matmul_offsets_past_32_bits(B, T):
     """Weights of 4.6 GB, and rows of x and y more than 2^31 elements apart (T = 2)."""
