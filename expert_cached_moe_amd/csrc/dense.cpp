@@ -282,30 +282,28 @@ int moe_dense_ffn_backward(moe_ctx* ctx, const void* d_dy, const void* d_x, int3
     p.gu_low = const_cast<uint8_t*>(save) + save_low_offset(c, T);
     if ((e = launch_product(type, kNN, kDGate, p, s)) != hipSuccess) return hip_fail(ctx, e, "moe_dense_ffn_backward launch");
     if (dblob) {
-        Product w{};                                   // dWd = dy^T h
+        Product w{};                                   // dWgu = (dg, du)^T x
         w.part = p.part;
         w.part_bytes = p.part_bytes;
-        w.a = d_dy;
-        w.lda = H;
-        w.b = save + save_h_offset(c, T);
-        w.ldb = I;
-        w.M = H;
-        w.N = int32_t(I);
-        w.K = T;
-        w.out = dblob + ctx->lay.d;
-        w.ldo = I;
-        if ((e = launch_product(type, kTN, kStore, w, s)) != hipSuccess)
-            return hip_fail(ctx, e, "moe_dense_ffn_backward launch");
-        w.a = d_ws;                                    // dWgu = (dg, du)^T x
+        w.a = d_ws;
         w.lda = 2 * I;
         w.b = d_x;
         w.ldb = H;
         w.M = 2 * I;
         w.N = int32_t(H);
+        w.K = T;
         w.out = dblob + ctx->lay.gu;
         w.ldo = H;
-        if ((e = launch_product(type, kTN, kStore, w, s)) != hipSuccess)
-            return hip_fail(ctx, e, "moe_dense_ffn_backward launch");
+        Product v = w;                                 // dWd = dy^T h
+        v.a = d_dy;
+        v.lda = H;
+        v.b = save + save_h_offset(c, T);
+        v.ldb = I;
+        v.M = H;
+        v.N = int32_t(I);
+        v.out = dblob + ctx->lay.d;
+        v.ldo = I;
+        if ((e = launch_gradients(type, w, v, s)) != hipSuccess) return hip_fail(ctx, e, "moe_dense_ffn_backward launch");
     }
     if (d_dx) {
         Product q{};

@@ -50,8 +50,10 @@ constexpr int64_t kPartBytes = int64_t(32) << 20;
 // Compute units of the current device.
 int compute_units();
 
-// One product on stream s: type kF32 / kBF16 / kI8, layout kNT / kNN / kTN, epilogue as above.
+// One product on stream s: type kF32 / kBF16 / kI8, layout kNT / kNN, epilogue as above.
 hipError_t launch_product(int type, int layout, int epi, const Product& p, hipStream_t s);
+// Two products kTN, kStore of the same K > 0 in one launch; they share p's scratch.
+hipError_t launch_gradients(int type, const Product& p, const Product& q, hipStream_t s);
 // few tokens, NT: the weight stream.  It takes up to 16 tokens, and up to 32 while the weights
 // are 32 MiB at most: 100003 x 4096 codes take it 90 us at 16 tokens and 101 at 24, the tiles 106
 // and 93-108; a 4096 x 12288 bf16 block 82 and 110 us against 87 and 88; 8192 x 4096 codes 10.7

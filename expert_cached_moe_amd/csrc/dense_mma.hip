@@ -417,17 +417,15 @@ __host__ __device__ inline int64_t part_ld(const Product& p) { return (int64_t(p
 // its last quarter, so the loads of a slice have a whole slice's time to land and the matrix
 // instructions of the last quarter cover the first reads of the next slice.
 template <int TYPE, int LAYOUT, int EPI, class C>
-__global__ void __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::kWavesPerSimd)))
-k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
+__device__ __forceinline__ void mma_tile(const Product& p, int block, int m_tiles, int n_tiles, int splits, uint8_t* lds) {
     typedef typename Frag<TYPE>::V V;
     typedef typename Frag<TYPE>::Acc Acc;
     constexpr int ES = Frag<TYPE>::ES, KS = kSlice / ES;
     constexpr bool AKC = LAYOUT != kTN, BKC = LAYOUT == kNT;
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     // tile of this workgroup
     const int tiles = m_tiles * n_tiles, total = tiles * splits, per = (total + kXcds - 1) / kXcds;
-    const int lid = int(blockIdx.x % kXcds) * per + int(blockIdx.x / kXcds);
-    if (int(blockIdx.x / kXcds) >= per || lid >= total) return;
+    const int lid = block % kXcds * per + block / kXcds;
+    if (block / kXcds >= per || lid >= total) return;
     const int split = lid / tiles, tile = lid % tiles;
     const int2 mn = tile_origin(tile, m_tiles, n_tiles);
     const int64_t m0 = int64_t(mn.x) * C::BM;
@@ -537,6 +535,28 @@ k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
     else
         finish_tile<TYPE, EPI, C, false>(p, mw, nw, acc, lds, nullptr, 0);
 }
+template <int TYPE, int LAYOUT, int EPI, class C>
+__global__ void __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::kWavesPerSimd)))
+k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    mma_tile<TYPE, LAYOUT, EPI, C>(p, blockIdx.x, m_tiles, n_tiles, splits, lds);
+}
+
+// Two products of one kind and one K in a launch (the gradients of the two weights): the first
+// `blocks` workgroups (a multiple of the XCDs) serve p, the others q.
+struct Pair {
+    Product p, q;
+    int blocks, m_tiles[2], n_tiles[2];
+};
+template <int TYPE, int LAYOUT, int EPI, class C>
+__global__ void __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::kWavesPerSimd)))
+k_mma_pair(const Pair a, int splits) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int b = blockIdx.x;
+    const bool q = b >= a.blocks;
+    const Product p = q ? a.q : a.p;
+    mma_tile<TYPE, LAYOUT, EPI, C>(p, q ? b - a.blocks : b, a.m_tiles[q], a.n_tiles[q], splits, lds);
+}
 
 __device__ __forceinline__ void fence_barrier() {
     __builtin_amdgcn_sched_barrier(0);
@@ -567,17 +587,15 @@ struct Turns {
 };
 
 template <int TYPE, int LAYOUT, int EPI>
-__global__ void __launch_bounds__(Turns::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
-k_mma_turns(const Product p, int m_tiles, int n_tiles) {
+__device__ __forceinline__ void turns_tile(const Product& p, int block, int m_tiles, int n_tiles, uint8_t* lds) {
     typedef Turns C;
     typedef typename Frag<TYPE>::V V;
     typedef typename Frag<TYPE>::Acc Acc;
     constexpr int ES = Frag<TYPE>::ES, KS = kSlice / ES;
     constexpr bool AKC = LAYOUT != kTN, BKC = LAYOUT == kNT;
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int tiles = m_tiles * n_tiles, per = (tiles + kXcds - 1) / kXcds;
-    const int tile = int(blockIdx.x % kXcds) * per + int(blockIdx.x / kXcds);
-    if (int(blockIdx.x / kXcds) >= per || tile >= tiles) return;
+    const int tile = block % kXcds * per + block / kXcds;
+    if (block / kXcds >= per || tile >= tiles) return;
     const int2 mn = tile_origin(tile, m_tiles, n_tiles);
     const int64_t m0 = int64_t(mn.x) * C::BM;
     const int n0 = mn.y * C::BN;
@@ -668,6 +686,21 @@ k_mma_turns(const Product p, int m_tiles, int n_tiles) {
 
     finish_tile<TYPE, EPI, C, false>(p, m0 + wm * C::TM, n0 + wn * C::TN, acc, lds, nullptr, 0);
 }
+template <int TYPE, int LAYOUT, int EPI>
+__global__ void __launch_bounds__(Turns::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
+k_mma_turns(const Product p, int m_tiles, int n_tiles) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    turns_tile<TYPE, LAYOUT, EPI>(p, blockIdx.x, m_tiles, n_tiles, lds);
+}
+template <int TYPE, int LAYOUT, int EPI>
+__global__ void __launch_bounds__(Turns::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
+k_mma_turns_pair(const Pair a) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int b = blockIdx.x;
+    const bool q = b >= a.blocks;
+    const Product p = q ? a.q : a.p;
+    turns_tile<TYPE, LAYOUT, EPI>(p, q ? b - a.blocks : b, a.m_tiles[q], a.n_tiles[q], lds);
+}
 
 // Adds the splits' partial sums, in order, and finishes: 4 columns (or 4 pairs) of a row a thread.
 template <int TYPE, int EPI>
@@ -716,31 +749,73 @@ hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done)
     return e;
 }
 
-template <int TYPE, int LAYOUT, int EPI, class C>
-hipError_t launch(const Product& p, int splits, hipStream_t s) {
+int64_t part_bytes(const Product& p, int splits) { return p.M * part_ld(p) * splits * 4; }
+
+// The tiles of a product, and the workgroups of a launch for them (0: too many).
+struct Tiles {
+    int m, n;
+    unsigned blocks;
+};
+template <class C>
+Tiles tiles_of(const Product& p, int splits) {
     const int64_t mt = (p.M + C::BM - 1) / C::BM, nt = (p.N + C::BN - 1) / C::BN;
-    if (mt * nt * splits > 0x7FFFFFF0 / kXcds) return hipErrorInvalidValue;
-    if (splits > 1 && p.M * part_ld(p) * splits * 4 > p.part_bytes) return hipErrorInvalidValue;
-    const unsigned grid = unsigned((mt * nt * splits + kXcds - 1) / kXcds * kXcds);
-    if (int64_t(grid) * C::kThreads > 0xFFFFFFFF) return hipErrorInvalidValue;      // threads of a launch: 32 bits
-    if constexpr (std::is_same<C, Turns>::value) {
-        const auto kernel = &k_mma_turns<TYPE, LAYOUT, EPI>;
-        static std::atomic<uint64_t> allowed{0};
-        hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), C::kLdsBytes, allowed);
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(kernel, dim3(grid), dim3(C::kThreads), C::kLdsBytes, s, p, int(mt), int(nt));
-        return hipGetLastError();
-    } else {
-        hipLaunchKernelGGL((k_mma<TYPE, LAYOUT, EPI, C>), dim3(grid), dim3(C::kThreads), C::kLdsBytes, s, p, int(mt),
-                           int(nt), splits);
-    }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || splits == 1) return e;
+    const int64_t blocks = (mt * nt * splits + kXcds - 1) / kXcds * kXcds;
+    if (mt * nt > 0x7FFFFFF0 / kXcds || blocks > 0x7FFFFFFF / C::kThreads) return Tiles{0, 0, 0};
+    return Tiles{int(mt), int(nt), unsigned(blocks)};
+}
+
+template <int TYPE, int EPI>
+hipError_t launch_join(const Product& p, int splits, hipStream_t s) {
     // (few results: more workgroups of one wave)
     const int64_t items = p.M * (kPaired<EPI> ? p.N / 8 : part_ld(p) / 4);
     const int threads = items < 256 * 1024 ? 64 : 256;
     hipLaunchKernelGGL((k_join<TYPE, EPI>), dim3(unsigned((items + threads - 1) / threads)), dim3(threads), 0, s, p, splits);
     return hipGetLastError();
+}
+
+template <int TYPE, int LAYOUT, int EPI, class C>
+hipError_t launch(const Product& p, int splits, hipStream_t s) {
+    const Tiles t = tiles_of<C>(p, splits);
+    if (t.blocks == 0) return hipErrorInvalidValue;
+    if (splits > 1 && part_bytes(p, splits) > p.part_bytes) return hipErrorInvalidValue;
+    if constexpr (std::is_same<C, Turns>::value) {
+        const auto kernel = &k_mma_turns<TYPE, LAYOUT, EPI>;
+        static std::atomic<uint64_t> allowed{0};
+        hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), C::kLdsBytes, allowed);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(kernel, dim3(t.blocks), dim3(C::kThreads), C::kLdsBytes, s, p, t.m, t.n);
+        return hipGetLastError();
+    } else {
+        hipLaunchKernelGGL((k_mma<TYPE, LAYOUT, EPI, C>), dim3(t.blocks), dim3(C::kThreads), C::kLdsBytes, s, p, t.m, t.n,
+                           splits);
+    }
+    hipError_t e = hipGetLastError();
+    return e != hipSuccess || splits == 1 ? e : launch_join<TYPE, EPI>(p, splits, s);
+}
+
+template <int TYPE, int LAYOUT, int EPI, class C>
+hipError_t launch_two(const Product& p, const Product& q, int splits, hipStream_t s) {
+    const Tiles t = tiles_of<C>(p, splits), u = tiles_of<C>(q, splits);
+    if (t.blocks == 0 || u.blocks == 0 || int64_t(t.blocks) + u.blocks > 0x7FFFFFFF / C::kThreads) return hipErrorInvalidValue;
+    Pair a{p, q, int(t.blocks), {t.m, u.m}, {t.n, u.n}};
+    const int64_t first = align256(part_bytes(p, splits));
+    if (splits > 1 && first + part_bytes(q, splits) > p.part_bytes) return hipErrorInvalidValue;
+    if (splits > 1) a.q.part = static_cast<uint8_t*>(p.part) + first;
+    if constexpr (std::is_same<C, Turns>::value) {
+        const auto kernel = &k_mma_turns_pair<TYPE, LAYOUT, EPI>;
+        static std::atomic<uint64_t> allowed{0};
+        hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), C::kLdsBytes, allowed);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(kernel, dim3(t.blocks + u.blocks), dim3(C::kThreads), C::kLdsBytes, s, a);
+        return hipGetLastError();
+    } else {
+        hipLaunchKernelGGL((k_mma_pair<TYPE, LAYOUT, EPI, C>), dim3(t.blocks + u.blocks), dim3(C::kThreads), C::kLdsBytes, s,
+                           a, splits);
+    }
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && splits > 1) e = launch_join<TYPE, EPI>(a.p, splits, s);
+    if (e == hipSuccess && splits > 1) e = launch_join<TYPE, EPI>(a.q, splits, s);
+    return e;
 }
 
 // Tile and split of K: the least of the times that a model fitted to measurements gives, in us.
@@ -753,22 +828,26 @@ hipError_t launch(const Product& p, int splits, hipStream_t s) {
 struct Choice {
     int tile, splits;
 };
-Choice plan(const Product& p, int es, int64_t n_cu) {
+Choice plan(const Product& p, const Product* q, int es, int64_t n_cu) {
     struct Kind { int bm, bn, slots; double slice, more, tile; };
     static const Kind half[] = {{256, 256, 1, 1.3, 0.0, 6.0}, {128, 128, 2, 0.68, 0.28, 3.0}, {64, 64, 4, 0.36, 0.13, 1.5}};
     static const Kind fp32[] = {{256, 256, 1, 8.6, 0.0, 6.0}, {128, 128, 2, 2.3, 2.1, 3.0}, {64, 64, 4, 0.65, 0.55, 1.5}};
     const Kind* kinds = es == 4 ? fp32 : half;
     const int64_t nk = (int64_t(p.K) * es + kSlice - 1) / kSlice;
+    static const int splits[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32};
+    const int64_t one = p.M * part_ld(p) + (q ? q->M * part_ld(*q) + 64 : 0);       // numbers of one split's sums
     Choice best{0, 1};
     double best_t = 1e30;
     for (int c = 0; c < 3; ++c) {
         const Kind& k = kinds[c];
-        const int64_t tiles = (p.M + k.bm - 1) / k.bm * ((p.N + k.bn - 1) / k.bn);
-        for (int sp = 1; sp <= 32 && sp * 4 <= (nk > 4 ? nk : 4); sp *= 2) {
-            const int64_t sums = p.M * part_ld(p) * sp, share = (nk + sp - 1) / sp;
+        auto count = [&](const Product& r) { return (r.M + k.bm - 1) / k.bm * ((r.N + k.bn - 1) / k.bn); };
+        const int64_t tiles = count(p) + (q ? count(*q) : 0);
+        for (int sp : splits) {
+            if (sp > 1 && sp * 4 > nk) break;
+            const int64_t sums = one * sp, share = (nk + sp - 1) / sp;
             // (256-tiles that could be split and still fill the chip would need more scratch)
             if (sp > 1 && (sums * 4 > p.part_bytes || c == 0)) break;
-            if (share * (sp - 1) >= nk) break;               // every split has slices
+            if (share * (sp - 1) >= nk) continue;            // every split has slices
             const int64_t groups = tiles * sp, rounds = (groups + n_cu * k.slots - 1) / (n_cu * k.slots);
             const int64_t on_cu = (groups + n_cu - 1) / n_cu < k.slots ? (groups + n_cu - 1) / n_cu : k.slots;
             const double t = rounds * (share * (k.slice + k.more * (on_cu - 1)) + k.tile) + (sp > 1 ? 3.0 + sums * 1.4e-6 : 0.0);
@@ -779,8 +858,16 @@ Choice plan(const Product& p, int es, int64_t n_cu) {
 }
 
 template <int TYPE, int LAYOUT, int EPI>
+hipError_t choose_two(const Product& p, const Product& q, hipStream_t s) {
+    const Choice c = plan(p, &q, Frag<TYPE>::ES, compute_units());
+    if (c.tile == 0) return launch_two<TYPE, LAYOUT, EPI, Turns>(p, q, c.splits, s);
+    if (c.tile == 1) return launch_two<TYPE, LAYOUT, EPI, Mid>(p, q, c.splits, s);
+    return launch_two<TYPE, LAYOUT, EPI, Small>(p, q, c.splits, s);
+}
+
+template <int TYPE, int LAYOUT, int EPI>
 hipError_t choose(const Product& p, hipStream_t s) {
-    const Choice c = plan(p, Frag<TYPE>::ES, compute_units());
+    const Choice c = plan(p, nullptr, Frag<TYPE>::ES, compute_units());
     if (c.tile == 0) return launch<TYPE, LAYOUT, EPI, Turns>(p, c.splits, s);
     if (c.tile == 1) return launch<TYPE, LAYOUT, EPI, Mid>(p, c.splits, s);
     return launch<TYPE, LAYOUT, EPI, Small>(p, c.splits, s);
@@ -802,8 +889,11 @@ hipError_t launch_product(int type, int layout, int epi, const Product& p, hipSt
     if (layout == kNT && epi == kGate) return f32 ? choose<kF32, kNT, kGate>(p, s) : choose<kBF16, kNT, kGate>(p, s);
     if (layout == kNN && epi == kStore) return f32 ? choose<kF32, kNN, kStore>(p, s) : choose<kBF16, kNN, kStore>(p, s);
     if (layout == kNN && epi == kDGate) return f32 ? choose<kF32, kNN, kDGate>(p, s) : choose<kBF16, kNN, kDGate>(p, s);
-    if (layout == kTN && epi == kStore) return f32 ? choose<kF32, kTN, kStore>(p, s) : choose<kBF16, kTN, kStore>(p, s);
     return hipErrorInvalidValue;
+}
+
+hipError_t launch_gradients(int type, const Product& p, const Product& q, hipStream_t s) {
+    return type == kF32 ? choose_two<kF32, kTN, kStore>(p, q, s) : choose_two<kBF16, kTN, kStore>(p, q, s);
 }
 
 }  // namespace dense
