@@ -230,7 +230,6 @@ __device__ __forceinline__ void read_transposed(const uint32_t (&at)[8], s16x4 (
 template <int X, bool KC, int ES>
 struct Reader {
     uint32_t at[2];          // byte offset for the first and second 64 bytes of K
-    int unit, f;             // not KC: first 16-column unit, its permutation
     __device__ __forceinline__ void init(int x0) {
         const int lane = threadIdx.x % kWave, j = lane % 16, g = lane / 16;
         if constexpr (KC) {
@@ -238,18 +237,16 @@ struct Reader {
             at[1] = at[0] ^ 64;
         } else if constexpr (ES == 2) {
             const int k = 8 * g + j / 4;                      // + 4 for the second read
-            at[0] = k * (X * 2) + (j % 4) * 8;
+            at[0] = k * (X * 2) + (j % 4) * 8 + ((x0 / 16 ^ chunk_swz<X, ES>(k) >> 1) << 5);
             at[1] = at[0] + 32 * (X * 2);
-            unit = x0 / 16;
-            f = chunk_swz<X, ES>(k) >> 1;
         } else {
             const int k = 4 * g;                              // + 0 .. 3
-            at[0] = k * (X * 4) + j * 4;
+            at[0] = k * (X * 4) + j * 4 + ((x0 / 16 ^ chunk_swz<X, ES>(k) >> 2) << 6);
             at[1] = at[0] + 16 * (X * 4);
-            unit = x0 / 16;
-            f = chunk_swz<X, ES>(k) >> 2;
         }
     }
+    // (fragment i is unit x0 / 16 + i, permuted: a multiple of the wave's fragments plus i, and rows
+    // are whole periods of the units, so its offset is that of fragment 0 with the bits of i flipped)
     // transposing reads: LDS offsets of fragments first .. first + N - 1, the offset of their
     // second halves, and the halves as one fragment
     static constexpr int kSecond = 4 * X * 2;
@@ -257,7 +254,7 @@ struct Reader {
     __device__ __forceinline__ void offsets(const uint8_t* lds, int half, int first, uint32_t (&from)[N]) const {
         const uint32_t base = uint32_t(reinterpret_cast<uintptr_t>((lds_void*)(lds + at[half])));
 #pragma unroll
-        for (int i = 0; i < N; ++i) from[i] = base + (uint32_t((unit + first + i) ^ f) << 5);
+        for (int i = 0; i < N; ++i) from[i] = base ^ uint32_t(first + i) << 5;
     }
     template <int N, class V>
     static __device__ __forceinline__ void join(const s16x4 (&lo)[N], const s16x4 (&hi)[N], V (&v)[N]) {
@@ -281,7 +278,7 @@ struct Reader {
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float* p = reinterpret_cast<const float*>(lds + at[half] + (((unit + first + i) ^ f) << 6));
+                const float* p = reinterpret_cast<const float*>(lds + (at[half] ^ uint32_t(first + i) << 6));
                 v[i] = V{p[0], p[X], p[2 * X], p[3 * X]};
             }
         }
@@ -538,7 +535,7 @@ __device__ __forceinline__ void mma_tile(const Product& p, int block, int m_tile
 template <int TYPE, int LAYOUT, int EPI, class C>
 __global__ void __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::kWavesPerSimd)))
 k_mma(const Product p, int m_tiles, int n_tiles, int splits) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     mma_tile<TYPE, LAYOUT, EPI, C>(p, blockIdx.x, m_tiles, n_tiles, splits, lds);
 }
 
@@ -551,7 +548,7 @@ struct Pair {
 template <int TYPE, int LAYOUT, int EPI, class C>
 __global__ void __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::kWavesPerSimd)))
 k_mma_pair(const Pair a, int splits) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const int b = blockIdx.x;
     const bool q = b >= a.blocks;
     const Product p = q ? a.q : a.p;
@@ -689,13 +686,13 @@ __device__ __forceinline__ void turns_tile(const Product& p, int block, int m_ti
 template <int TYPE, int LAYOUT, int EPI>
 __global__ void __launch_bounds__(Turns::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 k_mma_turns(const Product p, int m_tiles, int n_tiles) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     turns_tile<TYPE, LAYOUT, EPI>(p, blockIdx.x, m_tiles, n_tiles, lds);
 }
 template <int TYPE, int LAYOUT, int EPI>
 __global__ void __launch_bounds__(Turns::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 k_mma_turns_pair(const Pair a) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const int b = blockIdx.x;
     const bool q = b >= a.blocks;
     const Product p = q ? a.q : a.p;
@@ -751,6 +748,14 @@ hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done)
 
 int64_t part_bytes(const Product& p, int splits) { return p.M * part_ld(p) * splits * 4; }
 
+// LDS of a workgroup.  One slice needs one stage; twice the workgroups on a CU then hide each
+// other's one trip to memory (gradients of the 4096 x 1536 block from 37 tokens 13.6 against 16.6 us).
+template <class C>
+int lds_bytes(const Product& p, int es) {
+    if (int64_t(p.K) * es > kSlice) return C::kLdsBytes;
+    return C::STAGE > C::kFinishBytes ? C::STAGE : C::kFinishBytes;
+}
+
 // The tiles of a product, and the workgroups of a launch for them (0: too many).
 struct Tiles {
     int m, n;
@@ -786,8 +791,8 @@ hipError_t launch(const Product& p, int splits, hipStream_t s) {
         hipLaunchKernelGGL(kernel, dim3(t.blocks), dim3(C::kThreads), C::kLdsBytes, s, p, t.m, t.n);
         return hipGetLastError();
     } else {
-        hipLaunchKernelGGL((k_mma<TYPE, LAYOUT, EPI, C>), dim3(t.blocks), dim3(C::kThreads), C::kLdsBytes, s, p, t.m, t.n,
-                           splits);
+        hipLaunchKernelGGL((k_mma<TYPE, LAYOUT, EPI, C>), dim3(t.blocks), dim3(C::kThreads), lds_bytes<C>(p, Frag<TYPE>::ES), s,
+                           p, t.m, t.n, splits);
     }
     hipError_t e = hipGetLastError();
     return e != hipSuccess || splits == 1 ? e : launch_join<TYPE, EPI>(p, splits, s);
@@ -809,8 +814,8 @@ hipError_t launch_two(const Product& p, const Product& q, int splits, hipStream_
         hipLaunchKernelGGL(kernel, dim3(t.blocks + u.blocks), dim3(C::kThreads), C::kLdsBytes, s, a);
         return hipGetLastError();
     } else {
-        hipLaunchKernelGGL((k_mma_pair<TYPE, LAYOUT, EPI, C>), dim3(t.blocks + u.blocks), dim3(C::kThreads), C::kLdsBytes, s,
-                           a, splits);
+        hipLaunchKernelGGL((k_mma_pair<TYPE, LAYOUT, EPI, C>), dim3(t.blocks + u.blocks), dim3(C::kThreads),
+                           lds_bytes<C>(p, Frag<TYPE>::ES), s, a, splits);
     }
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && splits > 1) e = launch_join<TYPE, EPI>(a.p, splits, s);
