@@ -148,13 +148,19 @@ struct Side {
         return in ? off[q] : kOutside;
     }
     __device__ __forceinline__ void issue(uint8_t* lds, int k_left) {
-        const int wave = threadIdx.x / kWave;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
         const __amdgpu_buffer_rsrc_t r =
             __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, kRange, 0x00027000);
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const uint32_t o = k_left >= KS ? off[q] : tail(q, k_left);
+        auto load = [&](int q, uint32_t o) {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + (wave + NW * q) * 1024), 16, o, 0, 0, 0);
+        };
+        if (k_left >= KS) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) load(q, off[q]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) load(q, tail(q, k_left));
+            asm volatile("");           // (a path of its own: no selects among every slice's loads)
         }
         base += step;
     }
