@@ -98,6 +98,14 @@ __device__ __forceinline__ int chunk_swz(int k) {
 // share the 256 bytes of the banks by two
 __device__ __forceinline__ int row_swz(int r) { return (r >> 1) & 7; }
 
+// A wave's loads of a slice of one operand into LDS (256 rows, 8 waves): four times 1 KiB, 8 KiB
+// apart.
+struct SliceLoads {
+    uint32_t lds;
+    i32x4 rsrc;
+    uint32_t off[4];
+};
+
 // One operand's tile: X rows (tokens or weights) by one slice of K, X * 128 bytes in LDS.
 // KC: contiguous along K.
 template <int X, bool KC, int ES, int NW>
@@ -134,6 +142,21 @@ struct Side {
                 off[q] = uint32_t(k) * ldb + (col < left ? col : 0) * ES;
             }
         }
+    }
+    // the loads of the next slice for an assembly block; their offsets once k_left k are left
+    __device__ __forceinline__ SliceLoads next(uint8_t* lds) {
+        static_assert(Q == 4 && NW == 8, "as SliceLoads has them");
+        const uint64_t b = reinterpret_cast<uint64_t>(base);
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+        SliceLoads l{uint32_t(reinterpret_cast<uintptr_t>((lds_void*)lds)) + wave * 1024,
+                     i32x4{int(b), int(b >> 32) & 0xFFFF, int(kRange), 0x00027000},
+                     {off[0], off[1], off[2], off[3]}};
+        base += step;
+        return l;
+    }
+    __device__ __forceinline__ void end_of_k(int k_left) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) off[q] = k_left > 0 ? tail(q, k_left) : kOutside;
     }
     // offset of load q when only k_left k of the slice exist
     __device__ __forceinline__ uint32_t tail(int q, int k_left) const {
@@ -189,47 +212,60 @@ __device__ __forceinline__ void read_transposed(const uint32_t (&at)[4], s16x4 (
                  : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]), "=&v"(lo[3]), "=&v"(hi[3])
                  : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(OFF) : "memory");
 }
+// Transposing reads of 8 fragments, and of 8 and 4 of two operands, with the loads of a slice issued
+// among them, and the wait for the reads.  All loads before the reads delay those, all after
+// them end late: dx of the 4096 x 12288 block 1267 us before, 1220 after, 1210 among them.
 template <int OFF>
-__device__ __forceinline__ void read_transposed(const uint32_t (&at)[8], s16x4 (&lo)[8], s16x4 (&hi)[8]) {
-    asm volatile("ds_read_b64_tr_b16 %0, %16\n\tds_read_b64_tr_b16 %1, %16 offset:%24\n\t"
+__device__ __forceinline__ void read_transposed_and_load(const uint32_t (&at)[8], s16x4 (&lo)[8], s16x4 (&hi)[8],
+                                                     const SliceLoads& ld) {
+    asm volatile("s_mov_b32 m0, %25\n\tds_read_b64_tr_b16 %0, %16\n\tds_read_b64_tr_b16 %1, %16 offset:%24\n\t"
                  "ds_read_b64_tr_b16 %2, %17\n\tds_read_b64_tr_b16 %3, %17 offset:%24\n\t"
+                 "buffer_load_dwordx4 %27, %26, 0 offen lds\n\ts_add_u32 m0, %25, 0x2000\n\t"
                  "ds_read_b64_tr_b16 %4, %18\n\tds_read_b64_tr_b16 %5, %18 offset:%24\n\t"
                  "ds_read_b64_tr_b16 %6, %19\n\tds_read_b64_tr_b16 %7, %19 offset:%24\n\t"
+                 "buffer_load_dwordx4 %28, %26, 0 offen lds\n\ts_add_u32 m0, %25, 0x4000\n\t"
                  "ds_read_b64_tr_b16 %8, %20\n\tds_read_b64_tr_b16 %9, %20 offset:%24\n\t"
                  "ds_read_b64_tr_b16 %10, %21\n\tds_read_b64_tr_b16 %11, %21 offset:%24\n\t"
+                 "buffer_load_dwordx4 %29, %26, 0 offen lds\n\ts_add_u32 m0, %25, 0x6000\n\t"
                  "ds_read_b64_tr_b16 %12, %22\n\tds_read_b64_tr_b16 %13, %22 offset:%24\n\t"
-                 "ds_read_b64_tr_b16 %14, %23\n\tds_read_b64_tr_b16 %15, %23 offset:%24\n\ts_waitcnt lgkmcnt(0)"
-                 : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]), "=&v"(lo[3]),
-                   "=&v"(hi[3]), "=&v"(lo[4]), "=&v"(hi[4]), "=&v"(lo[5]), "=&v"(hi[5]), "=&v"(lo[6]), "=&v"(hi[6]),
-                   "=&v"(lo[7]), "=&v"(hi[7])
-                 : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]), "v"(at[6]), "v"(at[7]), "n"(OFF)
-                 : "memory");
+                 "ds_read_b64_tr_b16 %14, %23\n\tds_read_b64_tr_b16 %15, %23 offset:%24\n\t"
+                 "buffer_load_dwordx4 %30, %26, 0 offen lds\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]),
+                   "=&v"(lo[3]), "=&v"(hi[3]), "=&v"(lo[4]), "=&v"(hi[4]), "=&v"(lo[5]), "=&v"(hi[5]),
+                   "=&v"(lo[6]), "=&v"(hi[6]), "=&v"(lo[7]), "=&v"(hi[7])
+                 : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]), "v"(at[6]),
+                   "v"(at[7]), "n"(OFF), "s"(ld.lds), "s"(ld.rsrc), "v"(ld.off[0]), "v"(ld.off[1]),
+                   "v"(ld.off[2]), "v"(ld.off[3])
+                 : "memory", "m0", "scc");
 }
-
-// The same of two operands at once: 8 fragments of the one, 4 of the other.
 template <int OFF, int OFF2>
-__device__ __forceinline__ void read_transposed(const uint32_t (&at)[8], s16x4 (&lo)[8], s16x4 (&hi)[8],
-                                                const uint32_t (&at2)[4], s16x4 (&lo2)[4], s16x4 (&hi2)[4]) {
-    asm volatile("ds_read_b64_tr_b16 %0, %24\n\tds_read_b64_tr_b16 %1, %24 offset:%36\n\t"
+__device__ __forceinline__ void read_transposed_and_load(const uint32_t (&at)[8], s16x4 (&lo)[8], s16x4 (&hi)[8],
+                                                     const uint32_t (&at2)[4], s16x4 (&lo2)[4], s16x4 (&hi2)[4],
+                                                     const SliceLoads& ld) {
+    asm volatile("s_mov_b32 m0, %38\n\tds_read_b64_tr_b16 %0, %24\n\tds_read_b64_tr_b16 %1, %24 offset:%36\n\t"
                  "ds_read_b64_tr_b16 %2, %25\n\tds_read_b64_tr_b16 %3, %25 offset:%36\n\t"
                  "ds_read_b64_tr_b16 %4, %26\n\tds_read_b64_tr_b16 %5, %26 offset:%36\n\t"
+                 "buffer_load_dwordx4 %40, %39, 0 offen lds\n\ts_add_u32 m0, %38, 0x2000\n\t"
                  "ds_read_b64_tr_b16 %6, %27\n\tds_read_b64_tr_b16 %7, %27 offset:%36\n\t"
                  "ds_read_b64_tr_b16 %8, %28\n\tds_read_b64_tr_b16 %9, %28 offset:%36\n\t"
                  "ds_read_b64_tr_b16 %10, %29\n\tds_read_b64_tr_b16 %11, %29 offset:%36\n\t"
+                 "buffer_load_dwordx4 %41, %39, 0 offen lds\n\ts_add_u32 m0, %38, 0x4000\n\t"
                  "ds_read_b64_tr_b16 %12, %30\n\tds_read_b64_tr_b16 %13, %30 offset:%36\n\t"
                  "ds_read_b64_tr_b16 %14, %31\n\tds_read_b64_tr_b16 %15, %31 offset:%36\n\t"
                  "ds_read_b64_tr_b16 %16, %32\n\tds_read_b64_tr_b16 %17, %32 offset:%37\n\t"
+                 "buffer_load_dwordx4 %42, %39, 0 offen lds\n\ts_add_u32 m0, %38, 0x6000\n\t"
                  "ds_read_b64_tr_b16 %18, %33\n\tds_read_b64_tr_b16 %19, %33 offset:%37\n\t"
                  "ds_read_b64_tr_b16 %20, %34\n\tds_read_b64_tr_b16 %21, %34 offset:%37\n\t"
                  "ds_read_b64_tr_b16 %22, %35\n\tds_read_b64_tr_b16 %23, %35 offset:%37\n\t"
-                 "s_waitcnt lgkmcnt(0)"
+                 "buffer_load_dwordx4 %43, %39, 0 offen lds\n\ts_waitcnt lgkmcnt(0)"
                  : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]),
                    "=&v"(lo[3]), "=&v"(hi[3]), "=&v"(lo[4]), "=&v"(hi[4]), "=&v"(lo[5]), "=&v"(hi[5]),
                    "=&v"(lo[6]), "=&v"(hi[6]), "=&v"(lo[7]), "=&v"(hi[7]), "=&v"(lo2[0]), "=&v"(hi2[0]),
                    "=&v"(lo2[1]), "=&v"(hi2[1]), "=&v"(lo2[2]), "=&v"(hi2[2]), "=&v"(lo2[3]), "=&v"(hi2[3])
-                 : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]),
-                   "v"(at[6]), "v"(at[7]), "v"(at2[0]), "v"(at2[1]), "v"(at2[2]), "v"(at2[3]), "n"(OFF), "n"(OFF2)
-                 : "memory");
+                 : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]), "v"(at[6]),
+                   "v"(at[7]), "v"(at2[0]), "v"(at2[1]), "v"(at2[2]), "v"(at2[3]), "n"(OFF), "n"(OFF2),
+                   "s"(ld.lds), "s"(ld.rsrc), "v"(ld.off[0]), "v"(ld.off[1]), "v"(ld.off[2]), "v"(ld.off[3])
+                 : "memory", "m0", "scc");
 }
 
 // This lane's fragment reads of one operand: rows x0 + 16 i + lane % 16 of the tile.
@@ -647,40 +683,61 @@ __device__ __forceinline__ void turns_tile(const Product& p, int block, int m_ti
     fence_barrier();
     if (second) fence_barrier();                              // half a period behind
     int u = 0;                                                // B's place, A's is the next
+    constexpr bool kLoadsInside = !BKC && ES == 2;            // loads issued among the transposing reads
+    if constexpr (kLoadsInside) {
+        if (left_a < KS) sa.end_of_k(left_a);
+        if (left_b < KS) sb.end_of_k(left_b);
+    }
     for (int j = 0; j < n; ++j) {
         const uint8_t *pb = place(u), *pa = place(u + 1);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             V fa[C::FM], fb[C::FN];
-            // (reads that the compiler waits for later, loads, then reads with their wait)
-            if (AKC) ra.read(pa, half, 0, fa);
-            if (BKC) rb.read(pb, half, 0, fb);
-            if (half == 0 && j + 1 < n) issue_a(u + 3);
-            if (half == 1 && j + 2 < n) issue_b(u + 4);
-            if constexpr (!AKC && !BKC && ES == 2) {          // one wait for both
-                uint32_t ta[C::FM], tb[C::FN];
-                s16x4 la[C::FM], ha[C::FM], lb[C::FN], hb[C::FN];
-                ra.offsets(pa, half, 0, ta);
+            if constexpr (kLoadsInside) {
+                // (past the last slice the loads are out of range and write zeros to a free place)
+                uint32_t tb[C::FN];
+                s16x4 lb[C::FN], hb[C::FN];
+                if (AKC) ra.read(pa, half, 0, fa);
+                const SliceLoads ld = half == 0 ? sa.next(place(u + 3)) : sb.next(place(u + 4));
                 rb.offsets(pb, half, 0, tb);
-                read_transposed<decltype(rb)::kSecond, decltype(ra)::kSecond>(tb, lb, hb, ta, la, ha);
-                ra.join(la, ha, fa);
+                if constexpr (AKC) {
+                    read_transposed_and_load<decltype(rb)::kSecond>(tb, lb, hb, ld);
+                } else {
+                    uint32_t ta[C::FM];
+                    s16x4 la[C::FM], ha[C::FM];
+                    ra.offsets(pa, half, 0, ta);
+                    read_transposed_and_load<decltype(rb)::kSecond, decltype(ra)::kSecond>(tb, lb, hb, ta, la, ha, ld);
+                    ra.join(la, ha, fa);
+                }
                 rb.join(lb, hb, fb);
             } else {
-                if (!AKC) ra.read(pa, half, 0, fa);
-                if (!BKC) rb.read(pb, half, 0, fb);
+                // (reads that the compiler waits for later, then loads)
+                ra.read(pa, half, 0, fa);
+                rb.read(pb, half, 0, fb);
+                if (half == 0 && j + 1 < n) issue_a(u + 3);
+                if (half == 1 && j + 2 < n) issue_b(u + 4);
             }
             // slice j + 1 has landed at the end of the slice's last turn: a reading turn of the
             // second group, a computing turn of the first
-            if (half == 1 && second) landed(j + 2 < n, AlsoLds{});
+            if (half == 1 && second) landed(j + (kLoadsInside ? 1 : 2) < n, AlsoLds{});
             else __builtin_amdgcn_s_waitcnt(wait_for(63, 0));
             fence_barrier();
+            if constexpr (kLoadsInside) {
+                if (half == 0) {
+                    left_a -= KS;
+                    if (left_a < KS) sa.end_of_k(left_a);
+                } else {
+                    left_b -= KS;
+                    if (left_b < KS) sb.end_of_k(left_b);
+                }
+            }
             __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int i = 0; i < C::FM; ++i)
 #pragma unroll
                 for (int k = 0; k < C::FN; ++k) acc[i][k] = mma(fb[k], fa[i], acc[i][k]);
             __builtin_amdgcn_s_setprio(0);
-            if (half == 1 && !second) landed(j + 2 < n, NotLds{});
+            if (half == 1 && !second) landed(j + (kLoadsInside ? 1 : 2) < n, NotLds{});
             fence_barrier();
         }
         u = u + 2 >= C::kPlaces ? u + 2 - C::kPlaces : u + 2;
