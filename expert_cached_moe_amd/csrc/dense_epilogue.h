@@ -197,8 +197,7 @@ __device__ __forceinline__ void finish(const Product& p, int64_t m, int n, const
         }
         store_row<W>(static_cast<E*>(p.out) + m * p.ldo + n / 32 * 16 + n % 16, h);
     } else if constexpr (EPI == kGate8) {
-        // the same from integer sums, in fp32 with the full-precision silu (h's codes are decided
-        // on it)
+        // the same from integer sums, in fp32 throughout (h's codes are decided on it)
         float h[W];
 #pragma unroll
         for (int j = 0; j < W; ++j) {
