@@ -28,6 +28,10 @@
 // 8192 codes 118 us against 139, 4096 x 12288 11.2 against 12.5; with 32 rows the registers cost
 // more: 8 tokens, 50003 x 8192 87 against 81).
 //
+// Measured: 4096 x 12288 bf16 block at one token, 302 MB in 50.6 us (31.5 and 17.1), 6.0 TB/s;
+// 100003 x 4096 codes at 8 tokens, 410 MB in 70-73 us, 5.7 TB/s; 2048 x 2048 codes at one token
+// 5.1 us, latency.
+//
 // QUANT: x comes as numbers and every workgroup quantises it for itself, into LDS, while its
 // first weights are on the way: T K conversions in each workgroup against a launch and a pass
 // through memory, for T K up to kMaxQuant.

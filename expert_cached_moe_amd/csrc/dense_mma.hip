@@ -9,11 +9,13 @@
 //
 // Two kernels: k_mma_turns on 256 x 256 tiles, k_mma on 128 x 128 and 64 x 64 ones, where larger
 // tiles would leave CUs idle; with few of those, K is split over workgroups and k_join adds the
-// parts.  Measured (8,192 tokens, kernel times): 4096 outputs of 12288 in bf16 551 us, 1.50
-// PFLOP/s, the matrix units busy 80% of the cycles at 1.8 GHz, where power holds the clock;
-// gate and up of the 4096 x 12288 block 1.20 ms, 1.37 PFLOP/s; its gradients 0.69, 1.36 and
-// 1.21 ms (dWd, dWgu, dx), 1.18-1.36 PFLOP/s; 24576 outputs of 4096 in 8 bits 617 us, 2.67
-// POP/s.  A library product of 8192^3 reaches 1.45 PFLOP/s and 2.36 POP/s on the same card.
+// parts.  Measured (8,192 tokens through the 4096 x 12288 block, kernel times at their least, cards
+// differ by up to 7%): bf16 down 0.55 ms, 1.50 PFLOP/s, the matrix units busy 79% of the cycles at
+// 1.8 GHz, where power holds the clock; gate and up 1.20 ms, 1.38 PFLOP/s, 70%; dx 1.12 ms, 1.47
+// PFLOP/s, 76%; both weights' gradients 1.82 ms, 1.36 PFLOP/s, 67%; dg and du 0.73 ms, 1.13
+// PFLOP/s, 56% (1 GB of pre-activations read and results written when all CUs end a tile together).
+// In 8 bits down 280 us, 2.95 POP/s, gate and up 666 us, 2.48 POP/s.  A library product of 8192^3
+// reaches 1.45 PFLOP/s and 2.36 POP/s on the same card.
 //
 // Operands contiguous along K lie in LDS as rows of 128 bytes, 16-byte chunk c of row r at slot
 // c ^ ((r >> 1) & 7): two rows share a 256-byte window of the banks, so the 16 rows of a

