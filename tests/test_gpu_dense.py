@@ -652,6 +652,62 @@ def test_graph_replays(B, T):
                     assert same_bits(a, b), k
 
 
+def test_large_workspace_few_tokens(B):
+    """Calls with fewer tokens than their workspace was sized for (they split K and keep partial
+    sums there) give what an exact workspace gives, and stay inside it."""
+    K, N, H, I = 4096, 264, 1024, 160
+    rng = np.random.default_rng(21)
+    w = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda")
+    ws = torch.rand(N, device="cuda")
+    with Ctx(B, H, I) as c:
+        for T in (20, 64, 300):
+            x = normal(rng, (T, K), BF16)
+            want = _matmul(B, c, x, BF16, K, None, T, w, ws, N, K, F32, N)
+            work = Guarded(B.moe_i8_workspace_bytes(1100, K), torch.uint8)
+            y = torch.empty((T, N), device="cuda")
+            B.moe_i8_matmul(c.p, x, BF16, K, None, T, w, ws, N, K, y, F32, N, work.t)
+            torch.cuda.synchronize()
+            work.check()
+            assert same_bits(y, want.contiguous())
+            bx, bdy, wg, wu, wd = _block_inputs(rng, T, H, I, BF16)
+            blob = _blob(B, c, wg, wu, wd)
+            save = torch.empty(B.moe_dense_save_bytes(c.cfg, T), dtype=torch.uint8, device="cuda")
+            outs = []
+            for n in (T, 1100):
+                work = Guarded(B.moe_dense_workspace_bytes(c.cfg, n), torch.uint8)
+                by, dx, grad = torch.empty_like(bx), torch.empty_like(bx), torch.zeros_like(blob)
+                B.moe_dense_ffn(c.p, bx, T, blob, save, by, work.t)
+                B.moe_dense_ffn_backward(c.p, bdy, bx, T, blob, save, dx, grad, work.t)
+                torch.cuda.synchronize()
+                work.check()
+                outs.append((by, dx, grad))
+            assert all(same_bits(p, q) for p, q in zip(*outs))
+
+
+def test_large_tiles_in_a_graph(B):
+    """Calls of the largest tiles captured before they ever ran eagerly (they set an attribute of
+    their kernels), then replayed."""
+    T, N, K = 4096, 4096 + 32, 320
+    rng = np.random.default_rng(22)
+    x = normal(rng, (T, K), F32)
+    w = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda")
+    ws = torch.rand(N, device="cuda")
+    with Ctx(B) as c:
+        work = torch.empty(B.moe_i8_workspace_bytes(T, K), dtype=torch.uint8, device="cuda")
+        y = torch.zeros((T, N), device="cuda")
+        s = torch.cuda.Stream()
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=s):
+            B.moe_i8_matmul(c.p, x, F32, K, None, T, w, ws, N, K, y, F32, N, work, s)
+        for _ in range(3):
+            x.copy_(normal(rng, (T, K), F32))
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            assert same_bits(y, _matmul(B, c, x, F32, K, None, T, w, ws, N, K, F32, N).contiguous())
+
+
 def test_two_streams_at_once(B):
     """Two calls in flight on two streams, each with a workspace and a context of its own."""
     T, K, N = 300, 1040, 777
