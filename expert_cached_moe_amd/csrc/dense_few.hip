@@ -16,26 +16,32 @@
 // load reads 4.0-5.9 TB/s, as 8 whole lines 6.6 TB/s, as 1 KiB of one row 6.7 TB/s (workgroups
 // of 16 rows, non-temporal; of 32 rows 4.9 TB/s).
 //
-// WALK (more than 8 tokens): a workgroup walks groups of 8 R rows; the next group's first weights
-// are requested before the sums of the current one are added, and where K is one pass (ONE:
-// kDepth slices a wave) x stays in registers for all groups.  That saves reading x for every
-// group, which from 9 tokens on is as much as the weights (100003 x 4096 codes, 16 tokens: 90
-// against 109 us); up to 8 tokens the registers it takes cost more than it saves (8 tokens: 81
-// against 78 us, 1 token 76 against 64).
+// WALK: a workgroup walks groups of 8 R rows; the next group's first weights are requested before
+// the sums of the current one are added, and where K is one pass (ONE: kDepth slices a wave) x
+// stays in registers for all groups.  That saves reading x for every group, which from 9 tokens on
+// is as much as the weights (100003 x 4096 codes, 16 tokens: 90 against 109 us).  Without a walk
+// the last workgroups also end alone: at 8 tokens 73 us, 5.6 TB/s, against 67.
+//
+// A pass is 4 KiB of each row.  Workgroups that all begin with the first pass read every other 4 KiB
+// of rows of 8 KiB, and then the rest: half of the memory channels at a time.  So group g begins
+// with pass g % passes (100003 x 8192 codes at 8 tokens 136 us against 169, 6.0 TB/s; 8192 x 8192
+// bf16 block at one token 74 against 84).
 //
 // AHEAD (K of several passes, up to 16 rows a workgroup): the next pass's weights and activations
 // are requested before the current one's products, in registers of their own (1 token, 100003 x
 // 8192 codes 118 us against 139, 4096 x 12288 11.2 against 12.5; with 32 rows the registers cost
-// more: 8 tokens, 50003 x 8192 87 against 81).
+// more: 8 tokens, 100003 x 8192 147 against 136).
 //
-// Measured: 4096 x 12288 bf16 block at one token, 302 MB in 50.6 us (31.5 and 17.1), 6.0 TB/s;
-// 100003 x 4096 codes at 8 tokens, 410 MB in 70-73 us, 5.7 TB/s; 2048 x 2048 codes at one token
+// Measured: 4096 x 12288 bf16 block at one token, 302 MB in 50.6 us (31.5 and 17.2), 6.0 TB/s;
+// 100003 x 4096 codes at 8 tokens, 410 MB in 65-67 us, 6.2 TB/s; 2048 x 2048 codes at one token
 // 5.1 us, latency.
 //
 // QUANT: x comes as numbers and every workgroup quantises it for itself, into LDS, while its
 // first weights are on the way: T K conversions in each workgroup against a launch and a pass
 // through memory, for T K up to kMaxQuant.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 #include "dense_common.h"
 #include "dense_epilogue.h"
@@ -134,7 +140,15 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
     const __amdgpu_buffer_rsrc_t rx = rsrc(p.a);
 #pragma unroll
     for (int m = 0; m < MT; ++m) xo[m] = uint32_t(min(m * 8 + l8, T - 1)) * (QUANT != kNoQuant ? p.K + kCodePad : uint32_t(p.lda * ES));
-    constexpr uint32_t kStride = kWaves * kSlice;
+    constexpr uint32_t kStride = kWaves * kSlice, kPass = kStride * kDepth;
+    // K goes in passes; group g begins with pass g % passes
+    constexpr bool SINGLE = ONE || (!WALK && !AHEAD);
+    const int passes = SINGLE ? 1 : int((kb + kPass - 1) / kPass);
+    int begin = SINGLE ? 0 : int(blockIdx.x) % passes;
+    auto at = [&](int pass) {
+        const int q = pass + begin;
+        return uint32_t(wave * kSlice) + uint32_t(q >= passes ? q - passes : q) * kPass;
+    };
     dev::u32x4 w[AHEAD ? 2 : 1][kDepth][R];
     auto load_w = [&](dev::u32x4 (&w)[kDepth][R], int g, uint32_t s) {
         const int64_t n0 = first_row(g), left = p.N - 1 - n0;   // rows past N repeat the last one
@@ -167,8 +181,8 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
         }
     };
     int g = blockIdx.x;
-    if constexpr (AHEAD && QUANT == kNoQuant) load_x(x[0], wave * kSlice);
-    load_w(w[0], g, wave * kSlice);
+    if constexpr (AHEAD && QUANT == kNoQuant) load_x(x[0], at(0));
+    load_w(w[0], g, at(0));
     if constexpr (QUANT != kNoQuant) {
         float f[NV][8];
 #pragma unroll
@@ -217,49 +231,41 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
     // LDS: the codes, then two areas of sums, [wave][half][m][r][16]
     constexpr int kSums = 2 * kWaves * MT * R * 16;
     Acc* red0 = reinterpret_cast<Acc*>(lds + (QUANT != kNoQuant ? T * (p.K + kCodePad) : 0));
-    if constexpr (ONE) load_x(x[0], wave * kSlice);
-    for (int turn = 0; g < groups; ++turn) {
-        const int next = g + int(gridDim.x);
-        const int64_t n0 = first_row(g);
-        Acc acc[MT][R];
+    Acc acc[MT][R];
+    auto clear = [&]() {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int r = 0; r < R; ++r) acc[m][r] = Acc{0, 0, 0, 0};
-        auto products = [&](const dev::u32x4 (&w)[kDepth][R], const dev::u32x4 (&x)[kDepth][MT]) {
+    };
+    auto products = [&](const dev::u32x4 (&w)[kDepth][R], const dev::u32x4 (&x)[kDepth][MT]) {
 #pragma unroll
-            for (int d = 0; d < kDepth; ++d)
+        for (int d = 0; d < kDepth; ++d)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        if constexpr (TYPE == kF32) acc[m][r] = mma_f32(w[d][r], x[d][m], acc[m][r]);
-                        else acc[m][r] = mma(w[d][r], x[d][m], acc[m][r]);
-                    }
-        };
-        constexpr uint32_t kPass = kStride * kDepth;
-        if constexpr (AHEAD) {
-            if constexpr (QUANT != kNoQuant) load_x(x[0], wave * kSlice);
-            for (uint32_t s = wave * kSlice;; s += 2 * kPass) {
-                if (s + kPass < kb) load_x(x[1], s + kPass), load_w(w[1], g, s + kPass);
-                products(w[0], x[0]);
-                if (s + kPass >= kb) break;
-                if (s + 2 * kPass < kb) load_x(x[0], s + 2 * kPass), load_w(w[0], g, s + 2 * kPass);
-                products(w[1], x[1]);
-                if (s + 2 * kPass >= kb) break;
-            }
-        } else {
-            for (uint32_t s = wave * kSlice;;) {
-                if constexpr (!ONE) load_x(x[0], s);
-                products(w[0], x[0]);
-                s += kPass;
-                if (ONE || s >= kb) break;
-                load_w(w[0], g, s);
-            }
+                for (int r = 0; r < R; ++r) {
+                    if constexpr (TYPE == kF32) acc[m][r] = mma_f32(w[d][r], x[d][m], acc[m][r]);
+                    else acc[m][r] = mma(w[d][r], x[d][m], acc[m][r]);
+                }
+    };
+    // results: thread `tid` finishes 4 columns of one token.  What that reads is requested before
+    // the next weights (a wait for a load waits for every older one).
+    constexpr int PER = GATE ? 2 : 1, RES = R / PER, ITEMS = MT * RES * 16;    // RES: tiles of results
+    static_assert(ITEMS <= kThreads, "one item a thread");
+    const int ent = tid % 16, rm = tid / 16 / RES, rr = tid / 16 % RES, rt = rm * 8 + ent % 8;
+    ColumnScales<EPI, 4> cs;
+    RowInputs<TYPE, EPI, 4> in;
+    auto column = [&](int g) { return first_row(g) + rr * 8 + 4 * (ent / 8); };
+    auto request = [&](int g) {
+        if (tid < ITEMS && rt < T && column(g) < p.N) {
+            cs.load(p, int(column(g)));
+            in.load(p, rt, int(column(g)));
         }
-        if (WALK && next < groups) load_w(w[0], next, wave * kSlice);
-        // sums of the diagonal blocks: lanes 0-7 and 16-23 (rows 0-7, first halves), 40-47 and
-        // 56-63 (rows 8-15, second halves) as entry lane % 8 + 8 (lane / 16 % 2) of half lane / 32
+    };
+    // Sums of the diagonal blocks: lanes 0-7 and 16-23 (rows 0-7, first halves), 40-47 and
+    // 56-63 (rows 8-15, second halves) as entry lane % 8 + 8 (lane / 16 % 2) of half lane / 32.
+    auto reduce = [&](int g, int turn) {
         Acc* red = red0 + (turn & 1) * kSums;
         if ((lane % 16) / 8 == lane / 32) {
 #pragma unroll
@@ -270,39 +276,57 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
         }
         // (the other area's readers are past it: they met at the barrier before this one)
         lds_barrier();
-        constexpr int PER = GATE ? 2 : 1, RES = R / PER, ITEMS = MT * RES * 16;    // RES: tiles of results
-        for (int it = tid; it < ITEMS; it += kThreads) {
-            const int ent = it % 16, m = it / 16 / RES, r = it / 16 % RES;
-            Acc sum[PER];
+        if (tid >= ITEMS) return;
+        Acc sum[PER];
 #pragma unroll
-            for (int q = 0; q < PER; ++q) {
-                const int tile = m * R + r + q * RES;
-                sum[q] = red[tile * 16 + ent];
+        for (int q = 0; q < PER; ++q) {
+            const int tile = rm * R + rr + q * RES;
+            sum[q] = red[tile * 16 + ent];
 #pragma unroll
-                for (int v = 1; v < 2 * kWaves; ++v) sum[q] += red[(v * MT * R + tile) * 16 + ent];
-            }
-            const int t = m * 8 + ent % 8;
-            const int64_t n = n0 + r * 8 + 4 * (ent / 8);
-            if (t >= T || n >= p.N) continue;
-            typename Elem<TYPE>::Acc v[4], u[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = sum[0][e], u[e] = sum[PER - 1][e];
-            ColumnScales<EPI, 4> cs;
-            cs.load(p, int(n));
-            RowInputs<TYPE, EPI, 4> in;
-            in.load(p, t, int(n));
-            finish<TYPE, EPI, 4, false>(p, t, int(n), v, u, cs, in);
+            for (int v = 1; v < 2 * kWaves; ++v) sum[q] += red[(v * MT * R + tile) * 16 + ent];
         }
+        if (rt >= T || column(g) >= p.N) return;
+        typename Elem<TYPE>::Acc v[4], u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = sum[0][e], u[e] = sum[PER - 1][e];
+        finish<TYPE, EPI, 4, false>(p, rt, int(column(g)), v, u, cs, in);
+    };
+    if constexpr (ONE) load_x(x[0], at(0));
+    for (int turn = 0; g < groups; ++turn) {
+        const int next = g + int(gridDim.x);
+        clear();
+        if constexpr (AHEAD) {
+            if constexpr (QUANT != kNoQuant) load_x(x[0], at(0));
+            for (int pass = 0;; pass += 2) {
+                if (pass + 1 < passes) load_x(x[1], at(pass + 1)), load_w(w[1], g, at(pass + 1));
+                products(w[0], x[0]);
+                if (pass + 1 >= passes) break;
+                if (pass + 2 < passes) load_x(x[0], at(pass + 2)), load_w(w[0], g, at(pass + 2));
+                products(w[1], x[1]);
+                if (pass + 2 >= passes) break;
+            }
+        } else {
+            for (int pass = 0;;) {
+                if constexpr (!ONE) load_x(x[0], at(pass));
+                products(w[0], x[0]);
+                if (++pass >= passes) break;
+                load_w(w[0], g, at(pass));
+            }
+        }
+        if constexpr (!SINGLE && WALK) begin = next % passes;
+        request(g);
+        if (WALK && next < groups) load_w(w[0], next, at(0));
+        reduce(g, turn);
         if (!WALK) break;
         g = next;
     }
 }
 
-template <int TYPE, int EPI, int MT, int R, int QUANT>
+template <int TYPE, int EPI, int MT, int R, int QUANT, bool W = (MT > 1)>
 hipError_t launch_few_as(const Product& p, hipStream_t s) {
     constexpr bool GATE = kPaired<EPI>;
     const int64_t groups = (int64_t(p.N) + 8 * R - 1) / (8 * R);
-    constexpr bool WALK = MT > 1;
+    constexpr bool WALK = W;
     const int lds = (WALK ? 2 : 1) * 2 * kWaves * MT * R * 16 * 16 + (QUANT ? int(p.M) * (p.K + kCodePad) : 0);
     const bool one = p.K * (TYPE == kI8 ? 1 : TYPE == kBF16 ? 2 : 4) <= kWaves * kSlice * kDepth;
     if constexpr (!WALK) {
@@ -314,9 +338,10 @@ hipError_t launch_few_as(const Product& p, hipStream_t s) {
             hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, false, false, AHEAD>), dim3(unsigned(groups)),
                                dim3(kThreads), lds, s, p, int(groups));
     } else {
-        // up to four workgroups a CU, each the same number of groups
-        const int64_t most = int64_t(compute_units()) * 4, turns = (groups + most - 1) / most;
-        const dim3 grid(unsigned((groups + turns - 1) / turns));
+        // up to 8 tokens a workgroup a CU (its registers hold 128 KiB of weights); more tokens: up to
+        // four, each the same number of groups
+        const int64_t most = int64_t(compute_units()) * (MT == 1 ? 1 : 4), turns = (groups + most - 1) / most;
+        const dim3 grid(unsigned(MT == 1 ? std::min(groups, most) : (groups + turns - 1) / turns));
         if (one)
             hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, true, true, false>), grid, dim3(kThreads), lds, s, p, int(groups));
         else
@@ -338,11 +363,12 @@ hipError_t choose_few(const Product& p, int quant, hipStream_t s) {
         if (p.N < 4096 && mt == 1) return launch_few_as<TYPE, EPI, 1, 1, kNoQuant>(p, s);
     }
     if (mt == 1) {
-        // Every workgroup reads all of x: 32 rows a workgroup halve that, which pays from a few
-        // tokens on where the rows still fill the chip (8 tokens: 100003 x 4096 codes 70.5 us
-        // against 78, 8192 x 4096 8.4 against 9.5; 4096 x 4096 7.4 against 6.4; 1 token 66
-        // against 64.5).
-        if (p.M > 2 && p.N >= 8192) return launch_few_as<TYPE, EPI, 1, 4, kNoQuant>(p, s);
+        // A walk of 32 rows at a time, one workgroup a CU, keeps the stream going from group to group
+        // and reads x once: it wins where the rows fill the chip, in one pass of K (100003 x 4096
+        // codes 66 us at 8 tokens and 64 at one, against 70 and 66 without the walk) and, from 3
+        // tokens on, in several (100003 x 8192 136 against 177; at 2 tokens 139 against 118).
+        const bool one = int64_t(p.K) * (TYPE == kI8 ? 1 : TYPE == kBF16 ? 2 : 4) <= kWaves * kSlice * kDepth;
+        if (p.N >= 8192 && (p.M > 2 || one)) return launch_few_as<TYPE, EPI, 1, 4, kNoQuant, true>(p, s);
         return launch_few_as<TYPE, EPI, 1, 2, kNoQuant>(p, s);
     }
     if (mt == 2) return launch_few_as<TYPE, EPI, 2, 2, kNoQuant>(p, s);
