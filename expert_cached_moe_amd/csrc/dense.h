@@ -55,8 +55,8 @@ hipError_t launch_product(int type, int layout, int epi, const Product& p, hipSt
 // Two products kTN, kStore of the same K > 0 in one launch; they share p's scratch.
 hipError_t launch_gradients(int type, const Product& p, const Product& q, hipStream_t s);
 // few tokens, NT: the weight stream.  It takes up to 16 tokens, and up to 32 while the weights
-// are 32 MiB at most: 100003 x 4096 codes take it 90 us at 16 tokens and 101 at 24, the tiles 106
-// and 93-108; a 4096 x 12288 bf16 block 82 and 110 us against 87 and 88; 8192 x 4096 codes 10.7
+// are 32 MiB at most: 100003 x 4096 codes take it 71 us at 16 tokens and 101 at 24, the tiles 106
+// and 93-108; a 4096 x 12288 bf16 block 66 and 110 us against 87 and 88; 8192 x 4096 codes 8.6
 // and 13.7 us against 14.6; 2048 x 2048 codes 5.2 and 6.0 against 7.3.
 constexpr int kFewTokens = 32;
 inline bool few_tokens(const Product& p, int es) {

@@ -19,8 +19,8 @@
 // WALK: a workgroup walks groups of 8 R rows; the next group's first weights are requested before
 // the sums of the current one are added, and where K is one pass (ONE: kDepth slices a wave) x
 // stays in registers for all groups.  That saves reading x for every group, which from 9 tokens on
-// is as much as the weights (100003 x 4096 codes, 16 tokens: 90 against 109 us).  Without a walk
-// the last workgroups also end alone: at 8 tokens 73 us, 5.6 TB/s, against 67.
+// is as much as the weights, and the last workgroups do not end alone (100003 x 4096 codes, kernel
+// times: at 8 tokens 73 us, 5.6 TB/s, without a walk and 67 with it).
 //
 // A pass is 4 KiB of each row.  Workgroups that all begin with the first pass read every other 4 KiB
 // of rows of 8 KiB, and then the rest: half of the memory channels at a time.  So group g begins
@@ -338,10 +338,10 @@ hipError_t launch_few_as(const Product& p, hipStream_t s) {
             hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, false, false, AHEAD>), dim3(unsigned(groups)),
                                dim3(kThreads), lds, s, p, int(groups));
     } else {
-        // up to 8 tokens a workgroup a CU (its registers hold 128 KiB of weights); more tokens: up to
-        // four, each the same number of groups
-        const int64_t most = int64_t(compute_units()) * (MT == 1 ? 1 : 4), turns = (groups + most - 1) / most;
-        const dim3 grid(unsigned(MT == 1 ? std::min(groups, most) : (groups + turns - 1) / turns));
+        // 32 rows: a workgroup a CU (its registers hold 128 KiB of weights); 16: up to four, each the
+        // same number of groups
+        const int64_t most = int64_t(compute_units()) * (R == 4 ? 1 : 4), turns = (groups + most - 1) / most;
+        const dim3 grid(unsigned(R == 4 ? std::min(groups, most) : (groups + turns - 1) / turns));
         if (one)
             hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, true, true, false>), grid, dim3(kThreads), lds, s, p, int(groups));
         else
@@ -362,15 +362,16 @@ hipError_t choose_few(const Product& p, int quant, hipStream_t s) {
         // 16 rows a workgroup leave CUs idle below N = 4096: 8 then
         if (p.N < 4096 && mt == 1) return launch_few_as<TYPE, EPI, 1, 1, kNoQuant>(p, s);
     }
-    if (mt == 1) {
-        // A walk of 32 rows at a time, one workgroup a CU, keeps the stream going from group to group
-        // and reads x once: it wins where the rows fill the chip, in one pass of K (100003 x 4096
-        // codes 66 us at 8 tokens and 64 at one, against 70 and 66 without the walk) and, from 3
-        // tokens on, in several (100003 x 8192 136 against 177; at 2 tokens 139 against 118).
-        const bool one = int64_t(p.K) * (TYPE == kI8 ? 1 : TYPE == kBF16 ? 2 : 4) <= kWaves * kSlice * kDepth;
-        if (p.N >= 8192 && (p.M > 2 || one)) return launch_few_as<TYPE, EPI, 1, 4, kNoQuant, true>(p, s);
-        return launch_few_as<TYPE, EPI, 1, 2, kNoQuant>(p, s);
-    }
+    // A walk of 32 rows at a time, one workgroup a CU, keeps the stream going from group to group and
+    // halves the reading of x: it wins where the rows fill the chip, in one pass of K (100003 x 4096
+    // codes 64 us at one token, 66 at 8 and 71 at 16, against 66, 70 and 86 with 16 rows) and, with
+    // three groups or more for every CU, in several (100003 x 8192 136 and 169 at 8 and 16 tokens
+    // against 177 and 222; 16384 x 16384 63 at 12 tokens against 61; at 2 tokens 139 against 118).
+    const bool one = int64_t(p.K) * (TYPE == kI8 ? 1 : TYPE == kBF16 ? 2 : 4) <= kWaves * kSlice * kDepth;
+    const bool walk = p.N >= 8192 && (one || (p.M > 2 && p.N >= 96 * compute_units()));
+    if (mt == 1 && walk) return launch_few_as<TYPE, EPI, 1, 4, kNoQuant, true>(p, s);
+    if (mt == 1) return launch_few_as<TYPE, EPI, 1, 2, kNoQuant>(p, s);
+    if (mt == 2 && walk) return launch_few_as<TYPE, EPI, 2, 4, kNoQuant>(p, s);
     if (mt == 2) return launch_few_as<TYPE, EPI, 2, 2, kNoQuant>(p, s);
     return launch_few_as<TYPE, EPI, 4, 2, kNoQuant>(p, s);
 }
