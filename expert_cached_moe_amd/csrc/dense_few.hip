@@ -25,7 +25,7 @@
 // A pass is 4 KiB of each row.  Workgroups that all begin with the first pass read every other 4 KiB
 // of rows of 8 KiB, and then the rest: half of the memory channels at a time.  So group g begins
 // with pass g % passes (100003 x 8192 codes at 8 tokens 136 us against 169, 6.0 TB/s; 8192 x 8192
-// bf16 block at one token 74 against 84).
+// bf16 block at one token 74 against 84; rows of other lengths gained little).
 //
 // AHEAD (K of several passes, up to 16 rows a workgroup): the next pass's weights and activations
 // are requested before the current one's products, in registers of their own (1 token, 100003 x
@@ -38,7 +38,7 @@
 //
 // QUANT: x comes as numbers and every workgroup quantises it for itself, into LDS, while its
 // first weights are on the way: T K conversions in each workgroup against a launch and a pass
-// through memory, for T K up to kMaxQuant.
+// through memory, for T K up to kMaxQuant and few outputs.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
