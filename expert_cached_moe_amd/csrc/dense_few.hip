@@ -23,7 +23,7 @@
 // times: at 8 tokens 73 us, 5.6 TB/s, without a walk and 67 with it).
 //
 // A pass is 4 KiB of each row.  Workgroups that all begin with the first pass read every other 4 KiB
-// of rows of 8 KiB, and then the rest: half of the memory channels at a time.  So group g begins
+// of rows of 8 KiB, and then the rest, at the rate of half-used memory channels.  So group g begins
 // with pass g % passes (100003 x 8192 codes at 8 tokens 136 us against 169, 6.0 TB/s; 8192 x 8192
 // bf16 block at one token 74 against 84; rows of other lengths gained little).
 //
