@@ -25,13 +25,16 @@ __device__ __forceinline__ void put(uint16_t* p, float v) { *p = dev::f32_to_bf1
 
 // 1 / (1 + e^-z): e^-z overflows to infinity for z < -88, which gives the limit 0.
 __device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
-// z / (1 + e^-z) within four steps of fp32, from the hardware's exp2 and reciprocal (a step each): the
-// rounding of z log2(e), which grows with z, and log2(e)'s own are carried into the result.  Below
-// -128 e^-z stays infinity, whose reciprocal is 0.  (With expf and a division gate and up of the 4096
-// x 12288 8-bit block take 745 us instead of 711 for 8,192 tokens: nothing else runs meanwhile.)
+// z / (1 + e^-z) within four steps of fp32 for z >= -87, from the hardware's exp2 and reciprocal (a step
+// each): the rounding of z log2(e), which grows with z, and log2(e)'s own are carried into the result.
+// From about -87.3 down, where e^z leaves the normal numbers, the result is -0 (the value's size is
+// below 1.1e-36).  The exponent's argument is held to 128 on both sides: past that the result is z
+// or -0 in any case, and z log2(e) itself overflows from 2.4e38 on.  (With expf and a division gate and
+// up of the 4096 x 12288 8-bit block take 745 us instead of 711 for 8,192 tokens: nothing else runs
+// meanwhile.)
 __device__ __forceinline__ float silu(float z) {
     constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596303e-8f, kLn2 = 0.693147181f;
-    const float n = -fmaxf(z, -128.0f), p = n * kLog2e;
+    const float n = -__builtin_amdgcn_fmed3f(z, -128.0f, 128.0f), p = n * kLog2e;
     const float rest = fmaf(n, kLog2eRest, fmaf(n, kLog2e, -p));
     return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(p) * fmaf(rest, kLn2, 1.0f));
 }

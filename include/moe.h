@@ -409,6 +409,8 @@ int moe_i8_pack(moe_ctx* ctx, const void* d_blob, void* d_blob8, hipStream_t s);
 /* y = block(x) with both products in integers (async on s): x [T][H] bf16 is quantised per
  * token, gate and up are fp32 numbers scale * scale * (integer sum), h = silu(gate) * up in
  * fp32 is quantised per token, and the down product's result is rounded once to bf16 y [T][H].
+ * silu(z) is within four steps of fp32 for z >= -87, up to z itself at the end of the range, and 0
+ * from about -87.3 down (where its size is below 1.1e-36).
  * Alignments and d_ws as moe_dense_ffn.  T == 0 is a no-op. */
 int moe_i8_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob8, void* d_y, void* d_ws, hipStream_t s);
 

@@ -1,0 +1,58 @@
+"""Dense operators on values far out: gates near the end of fp32."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import dense_oracle as D
+from test_gpu_dense import Ctx, Guarded, _blob, _check, f64
+from test_gpu_dense import B  # noqa: F401  (fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def _i8_ffn(B, c, x, b8):
+    T, H = x.shape
+    work = torch.full((B.moe_dense_workspace_bytes(c.cfg, T),), 0xFF, dtype=torch.uint8, device="cuda")
+    y = Guarded(T * H, torch.bfloat16)
+    B.moe_i8_ffn(c.p, x, T, b8, y.t, work)
+    torch.cuda.synchronize()
+    y.check()
+    return y.t.view(T, H)
+
+
+def _pack8(B, c, wg, wu, wd):
+    b8 = torch.empty(B.moe_i8_blob_bytes(c.cfg), dtype=torch.uint8, device="cuda")
+    B.moe_i8_pack(c.p, _blob(B, c, wg, wu, wd), b8)
+    return b8
+
+
+@pytest.mark.parametrize("T,I", [(1, 32), (1, 8192), (7, 96), (12, 64), (40, 160), (300, 256)])
+def test_i8_block_far_gates(B, T, I):
+    """Gates up to 3.3e38 of either sign, with |up| < 1: h = silu(gate) up and y are finite.
+
+    One channel of x is not 0, so gate and up are single products: each of the three roundings of
+    2^-24 once, silu's four steps of 2^-23 and the product's rounding put h within 2^-20, and half
+    of the argument's error times its size for gates that are neither small nor far (|gate| <= 8:
+    3 * 8 * 2^-24); 2^-17 of h covers both.  From there on as for ordinary values."""
+    H = 64
+    rng = np.random.default_rng(T + I)
+    x = np.zeros((T, H))
+    x[:, 5] = 2.0 ** 63 * rng.choice([1.0, 0.75, 2.0 ** -64, 2.0 ** -70], T)
+    x[0, 5] = 2.0 ** 63
+    wg, wu, wd = np.zeros((I, H)), np.zeros((I, H)), rng.standard_normal((H, I)) * 2.0 ** -100
+    # gates over 2^127 (1.7e38): 1.5 and 1.9375 of it; ordinary ones (up to 8); their negatives
+    wg[:, 5] = rng.choice([1.5, 1.9375, 1.0, 2.0 ** -127, 2.0 ** -124, 2.0 ** -60], I) * rng.choice([-1, 1], I) * 2.0 ** 64
+    wg[:4, 5] = np.array([1.5, 1.9375, -1.9375, 2.0 ** -126]) * 2.0 ** 64
+    wu[:, 5] = (rng.random(I) * 0.5 + 0.25) * rng.choice([-1, 1], I) * 2.0 ** -63
+    x, wg, wu, wd = (torch.from_numpy(a.astype(np.float32)).bfloat16().cuda() for a in (x, wg, wu, wd))
+    with Ctx(B, H, I) as c:
+        y = _i8_ffn(B, c, x, _pack8(B, c, wg, wu, wd))
+    q = [v for w in (wg, wu, wd) for v in D.quantize_rows(f64(w))]
+    ref, (h, hs) = D.i8_block(f64(x), *q)
+    assert np.abs(h[0]).max() > 1e37 and np.isfinite(ref).all()
+    step = hs.astype(np.float64)[:, None]
+    quot = h / np.where(step > 0, step, 1)
+    near = (np.abs(quot - np.floor(quot) - 0.5) <= 127 * 2.0 ** -16) * step
+    wdeq = np.abs(q[4].astype(np.float64)) * q[5].astype(np.float64)[:, None]
+    bound = near @ wdeq.T + np.abs(ref) * (2.0 ** -16 + 2.0 ** -8) + 2.0 ** -16 * (step * 0.5 * wdeq.sum(1))
+    _check("y", f64(y), ref, bound)
