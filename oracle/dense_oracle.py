@@ -59,7 +59,10 @@ def deinterleave(gu):
 
 
 def sigmoid(z):
-    return 0.5 * (1.0 + np.tanh(0.5 * z))
+    """1 / (1 + e^-z), through e^-|z|: nothing cancels or overflows at either end."""
+    z = np.asarray(z, np.float64)
+    e = np.exp(-np.abs(z))
+    return np.where(z >= 0, 1.0, e) / (1.0 + e)
 
 
 def block(x, wg, wu, wd):
