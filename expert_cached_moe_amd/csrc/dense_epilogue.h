@@ -212,8 +212,9 @@ __device__ __forceinline__ void finish(const Product& p, int64_t m, int n, const
 #pragma unroll
         for (int j = 0; j < W; ++j) {
             const float s = sigmoid_of<TYPE>(in.g[j]);
-            dg[j] = v[j] * in.u[j] * silu_grad(in.g[j], s);
-            du[j] = v[j] * in.g[j] * s;
+            // (v last: a shut gate's factor is 0, and v g or v u may leave fp32)
+            dg[j] = v[j] * (in.u[j] * silu_grad(in.g[j], s));
+            du[j] = v[j] * (in.g[j] * s);
         }
         store_row<W>(static_cast<E*>(p.out) + o, dg);
         store_row<W>(static_cast<E*>(p.out) + o + 16, du);

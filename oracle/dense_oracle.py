@@ -86,13 +86,16 @@ def _gamma(n):
     return n * F32_HALF * 1.01
 
 
-def block_bounds(dy, x, wg, wu, wd, dtype):
-    """Elementwise bounds of the library's y, dx, dWg, dWu, dWd (dy None: y's only)."""
+def block_bounds(dy, x, wg, wu, wd, dtype, exact=False):
+    """Elementwise bounds of the library's y, dx, dWg, dWu, dWd (dy None: y's only).  exact: every
+    pre-activation is one product that its type holds whole (no error, and kept as it is)."""
     half = HALF[dtype]
     H, I, T = x.shape[1], wg.shape[0], x.shape[0]
     y, (g, u, a, h) = block(x, wg, wu, wd)
     ax, awd = np.abs(x), np.abs(wd)
     eg, eu = _gamma(H) * (ax @ np.abs(wg).T), _gamma(H) * (ax @ np.abs(wu).T)
+    if exact:
+        eg, eu = np.zeros_like(eg), np.zeros_like(eu)
     ag, au, aa, ah = np.abs(g), np.abs(u), np.abs(a), np.abs(h)
     # silu' lies in (-0.1, 1.1)
     eh = (aa * (1 + SIGMOID_REL) + 1.1 * eg) * (au + eu) - aa * au
@@ -106,7 +109,8 @@ def block_bounds(dy, x, wg, wu, wd, dtype):
     sp = s + g * s * (1 - s)
     dh = dy @ wd
     adh, ed = np.abs(dh), _gamma(H) * (ady @ awd)
-    egs, eus = eg + (ag + eg) * KEPT[dtype], eu + (au + eu) * KEPT[dtype]             # as saved
+    kept = 0.0 if exact else KEPT[dtype]
+    egs, eus = eg + (ag + eg) * kept, eu + (au + eu) * kept             # as saved
     asp = np.abs(sp)
     # silu'' lies in (-0.1, 0.5]; silu' is a sum of terms of size s and s |g|
     esp = 0.5 * egs + SIGMOID_REL * (s + (ag + egs) * s)

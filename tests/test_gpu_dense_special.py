@@ -1,10 +1,11 @@
-"""Dense operators on values far out: gates near the end of fp32."""
+"""Dense operators on values far out: gates near the end of fp32, and shut gates with large
+gradients behind them."""
 import numpy as np
 import pytest
 import torch
 
 from oracle import dense_oracle as D
-from test_gpu_dense import Ctx, Guarded, _blob, _check, f64
+from test_gpu_dense import BF16, F32, NAME, TORCH, Ctx, Guarded, _blob, _check, _views, f64
 from test_gpu_dense import B  # noqa: F401  (fixture)
 
 pytestmark = pytest.mark.gpu
@@ -56,3 +57,46 @@ def test_i8_block_far_gates(B, T, I):
     wdeq = np.abs(q[4].astype(np.float64)) * q[5].astype(np.float64)[:, None]
     bound = near @ wdeq.T + np.abs(ref) * (2.0 ** -16 + 2.0 ** -8) + 2.0 ** -16 * (step * 0.5 * wdeq.sum(1))
     _check("y", f64(y), ref, bound)
+
+
+@pytest.mark.parametrize("T", [1, 5, 40, 300])
+@pytest.mark.parametrize("w", [BF16, F32])
+def test_block_backward_shut_gates(B, T, w):
+    """Gates at -2^80 beside ordinary ones, with dh near 2^60: dh g leaves fp32, and so does dh u
+    where u is large, but silu and its derivative are 0 there, so dg and du are.
+
+    One channel of x is not 0 and holds a power of two, so gates and up are exact (bounds with
+    exact pre-activations)."""
+    H, I = 64, 96
+    rng = np.random.default_rng(T)
+    xs = np.zeros((T, H))
+    xs[:, 9] = 2.0 ** 40 * rng.choice([1.0, 0.5, 0.25], T)
+    gate, up = rng.standard_normal((I, H)), rng.standard_normal((I, H))
+    gate[:, 9] *= 2.0 ** -40
+    up[:, 9] *= 2.0 ** -40
+    gate[::3, 9] = -2.0 ** 40 * (1 + rng.random(len(gate[::3])))
+    up[::6, 9] *= 2.0 ** 75
+    x, dy, wg, wu, wd = (torch.from_numpy(a.astype(np.float32)).to(TORCH[w]).cuda()
+                         for a in (xs, rng.standard_normal((T, H)) * 2.0 ** 57, gate, up, rng.standard_normal((H, I))))
+    with Ctx(B, H, I, w) as c:
+        blob = _blob(B, c, wg, wu, wd)
+        work = torch.full((B.moe_dense_workspace_bytes(c.cfg, T),), 0xFF, dtype=torch.uint8, device="cuda")
+        save = torch.full((B.moe_dense_save_bytes(c.cfg, T),), 0xFF, dtype=torch.uint8, device="cuda")
+        y, dx, grad = Guarded(T * H, TORCH[w]), Guarded(T * H, TORCH[w]), Guarded(blob.numel(), torch.uint8)
+        B.moe_dense_ffn(c.p, x, T, blob, save, y.t, work)
+        B.moe_dense_ffn_backward(c.p, dy, x, T, blob, save, dx.t, grad.t, work)
+        torch.cuda.synchronize()
+        for g in (y, dx, grad):
+            g.check()
+        gu, dd = _views(grad.t, H, I, TORCH[w])
+    args = [f64(t) for t in (x, wg, wu, wd)]
+    g64 = args[0] @ args[1].T
+    assert (np.abs(f64(dy) @ args[3])[:, ::3] * np.abs(g64)[:, ::3]).max() > 3.5e38
+    bounds = D.block_bounds(f64(dy), *args, NAME[w], exact=True)
+    ref = D.block_backward(f64(dy), *args)
+    _check("y", f64(y.t).reshape(T, H), D.block(*args)[0], bounds["y"])
+    _check("dx", f64(dx.t).reshape(T, H), ref[0], bounds["dx"])
+    dwg, dwu = D.deinterleave(f64(gu))
+    _check("dwg", dwg, ref[1], bounds["dwg"])
+    _check("dwu", dwu, ref[2], bounds["dwu"])
+    _check("dwd", f64(dd), ref[3], bounds["dwd"])
