@@ -1,7 +1,6 @@
 // Entry points of the dense operators: 8-bit integer products, and the dense gated block with
 // its backward pass and its 8-bit form.  Contracts in include/moe.h; the kernels are in
-// dense_quant.hip, dense_few.hip and
-// dense_mma.hip.
+// dense_quant.hip, dense_few.hip and dense_mma.hip.
 #include <hip/hip_runtime.h>
 
 #include "dense.h"
@@ -72,16 +71,41 @@ Blob8 blob8_layout(const moe_config& c) {
 constexpr int kMaxWidth = 1 << 20;    // H and I: row offsets inside a tile stay below 2 GiB
 constexpr int kMaxCount = 1 << 24;    // tokens, outputs, columns: the threads of a launch fit 32 bits
 
+// The configs that the block's calls take: their sizes and the packing refuse the others too.
+int check_config(const moe_config& c, bool i8, const char** why) {
+    if (i8 && c.w_dtype != MOE_W_BF16) {
+        *why = "the 8-bit block is made from and for bf16 contexts";
+        return MOE_EUNSUPPORTED;
+    }
+    if (c.w_dtype == MOE_W_MXFP4) {
+        *why = "the dense block takes fp32 or bf16 weights";
+        return MOE_EUNSUPPORTED;
+    }
+    if (i8 && (c.inter > kMaxKI8 || c.hidden > kMaxKI8)) {
+        *why = "the 8-bit block takes H and I up to 131056";
+        return MOE_ESHAPE;
+    }
+    if (c.hidden > kMaxWidth || c.inter > kMaxWidth) {
+        *why = "the dense block takes H and I up to 2^20";
+        return MOE_ESHAPE;
+    }
+    return MOE_OK;
+}
+
+int check_size(const moe_config* c, int32_t T, bool i8) {
+    int st = validate_config(c, nullptr);
+    if (st != MOE_OK) return st;
+    if (T < 0) return MOE_EINVAL;
+    const char* why;
+    return check_config(*c, i8, &why);
+}
+
 int check_block(moe_ctx* ctx, int32_t T, bool i8) {
     if (T < 0) return fail(ctx, MOE_EINVAL, "T < 0");
     if (T > kMaxCount) return fail(ctx, MOE_ESHAPE, "T above 2^24");
-    if (ctx->cfg.hidden > kMaxWidth || ctx->cfg.inter > kMaxWidth)
-        return fail(ctx, MOE_ESHAPE, "the dense block takes H and I up to 2^20");
-    if (i8 && ctx->cfg.w_dtype != MOE_W_BF16)
-        return fail(ctx, MOE_EUNSUPPORTED, "the 8-bit block is made from and for bf16 contexts");
-    if (!i8 && ctx->cfg.w_dtype == MOE_W_MXFP4)
-        return fail(ctx, MOE_EUNSUPPORTED, "the dense block takes fp32 or bf16 weights");
-    return MOE_OK;
+    const char* why;
+    const int st = check_config(ctx->cfg, i8, &why);
+    return st == MOE_OK ? st : fail(ctx, st, why);
 }
 
 // Whether the few-token kernel quantises x itself: few enough numbers, rows that can be read
@@ -192,16 +216,14 @@ int moe_i8_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, c
 }
 
 int64_t moe_dense_workspace_bytes(const moe_config* cfg, int32_t max_T) {
-    const int st = validate_config(cfg, nullptr);
+    const int st = check_size(cfg, max_T, false);
     if (st != MOE_OK) return st;
-    if (max_T < 0) return MOE_EINVAL;
     return block_work(*cfg, max_T).bytes;
 }
 
 int64_t moe_dense_save_bytes(const moe_config* cfg, int32_t T) {
-    const int st = validate_config(cfg, nullptr);
+    const int st = check_size(cfg, T, false);
     if (st != MOE_OK) return st;
-    if (T < 0) return MOE_EINVAL;
     return align256(save_h_offset(*cfg, T) + int64_t(T) * cfg->inter * act_bytes(*cfg));
 }
 
@@ -329,7 +351,7 @@ int moe_dense_ffn_backward(moe_ctx* ctx, const void* d_dy, const void* d_x, int3
 }
 
 int64_t moe_i8_blob_bytes(const moe_config* cfg) {
-    const int st = validate_config(cfg, nullptr);
+    const int st = check_size(cfg, 0, true);
     return st != MOE_OK ? st : blob8_layout(*cfg).bytes;
 }
 
@@ -356,7 +378,6 @@ int moe_i8_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob8, vo
     int st = check_block(ctx, T, true);
     if (st != MOE_OK) return st;
     const moe_config& c = ctx->cfg;
-    if (c.inter > kMaxKI8 || c.hidden > kMaxKI8) return fail(ctx, MOE_ESHAPE, "H and I at most 131056");
     if (T == 0) return MOE_OK;
     if (!d_x || !d_blob8 || !d_y || !d_ws) return fail(ctx, MOE_EINVAL, "null buffer");
     if (!aligned(d_x, 16) || !aligned(d_blob8, 256) || !aligned(d_y, 16) || !aligned(d_ws, 16))

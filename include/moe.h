@@ -373,6 +373,7 @@ int moe_i8_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, c
  * config has that width).  Contexts with fp32 or bf16 weights; H = cfg.hidden, I = cfg.inter
  * (each up to 2^20; up to 131056 for the 8-bit form), T up to 2^24,
  * activations in the weights' type.  Blob, x, y, dy, dx, save and workspace 16-byte aligned.
+ * Sizes and packing refuse the configs that the calls refuse, with the same status.
  *
  * Scratch bytes for up to max_T tokens of any moe_dense_* or moe_i8_ffn call. */
 int64_t moe_dense_workspace_bytes(const moe_config* cfg, int32_t max_T);
@@ -384,8 +385,8 @@ int64_t moe_dense_save_bytes(const moe_config* cfg, int32_t T);
 /* Forward pass of T tokens (async on s): d_x [T][H], d_blob, d_y [T][H].  d_save
  * (moe_dense_save_bytes of the same T) is written when not NULL; y does not depend on it.
  * Products accumulate in fp32 and h is rounded once to the activation type before the down
- * projection, as in moe_expert_ffn.  T == 0 is a no-op.  Errors: MOE_EINVAL (null, alignment),
- * MOE_EUNSUPPORTED (MXFP4 weights). */
+ * projection, as in moe_expert_ffn.  T == 0 is a no-op.  Errors: MOE_EINVAL (null, alignment, T < 0),
+ * MOE_ESHAPE (T, H or I past the limits), MOE_EUNSUPPORTED (MXFP4 weights). */
 int moe_dense_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob, void* d_save, void* d_y, void* d_ws,
                   hipStream_t s);
 /* Backward pass (async on s): from d_dy = dL/dy [T][H], the same x and blob as the forward
@@ -404,14 +405,16 @@ int moe_dense_ffn_backward(moe_ctx* ctx, const void* d_dy, const void* d_x, int3
  * scales of the Wgu rows [2I], scales of the Wd rows [H], each part 256-byte aligned. */
 int64_t moe_i8_blob_bytes(const moe_config* cfg);
 /* Quantise a device blob's rows (async on s): d_blob (moe_expert_bytes) to d_blob8
- * (moe_i8_blob_bytes), both 256-byte aligned. */
+ * (moe_i8_blob_bytes), both 256-byte aligned.  Errors: MOE_EINVAL, MOE_ESHAPE (H or I above 131056),
+ * MOE_EUNSUPPORTED (weights other than bf16). */
 int moe_i8_pack(moe_ctx* ctx, const void* d_blob, void* d_blob8, hipStream_t s);
 /* y = block(x) with both products in integers (async on s): x [T][H] bf16 is quantised per
  * token, gate and up are fp32 numbers scale * scale * (integer sum), h = silu(gate) * up in
  * fp32 is quantised per token, and the down product's result is rounded once to bf16 y [T][H].
  * silu(z) is within four steps of fp32 for z >= -87, up to z itself at the end of the range, and 0
  * from about -87.3 down (where its size is below 1.1e-36).
- * Alignments and d_ws as moe_dense_ffn.  T == 0 is a no-op. */
+ * Alignments and d_ws as moe_dense_ffn.  T == 0 is a no-op.  Errors as moe_i8_pack, and MOE_ESHAPE
+ * for T above 2^24. */
 int moe_i8_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob8, void* d_y, void* d_ws, hipStream_t s);
 
 /* ---------------------------------------------------------------- layer streaming (prefill) */
