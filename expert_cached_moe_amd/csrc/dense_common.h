@@ -17,9 +17,6 @@ template <> struct Elem<kF32> { typedef float T; typedef float Acc; };
 template <> struct Elem<kBF16> { typedef uint16_t T; typedef float Acc; };
 template <> struct Elem<kI8> { typedef int8_t T; typedef int Acc; };
 
-__device__ __forceinline__ float value(float v) { return v; }
-__device__ __forceinline__ float value(uint16_t v) { return bf16_f32(v); }
-__device__ __forceinline__ int value(int8_t v) { return v; }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(uint16_t* p, float v) { *p = dev::f32_to_bf16_bits(v); }
 

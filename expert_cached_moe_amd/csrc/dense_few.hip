@@ -330,12 +330,12 @@ hipError_t launch_few_as(const Product& p, hipStream_t s) {
     const int lds = (WALK ? 2 : 1) * 2 * kWaves * MT * R * 16 * 16 + (QUANT ? int(p.M) * (p.K + kCodePad) : 0);
     const bool one = p.K * (TYPE == kI8 ? 1 : TYPE == kBF16 ? 2 : 4) <= kWaves * kSlice * kDepth;
     if constexpr (!WALK) {
-        constexpr bool AHEAD = R <= 2;
-        if (one || !AHEAD)
+        static_assert(R <= 2, "registers for the next pass");
+        if (one)
             hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, false, false, false>), dim3(unsigned(groups)),
                                dim3(kThreads), lds, s, p, int(groups));
         else
-            hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, false, false, AHEAD>), dim3(unsigned(groups)),
+            hipLaunchKernelGGL((k_few<TYPE, EPI, MT, R, QUANT, false, false, true>), dim3(unsigned(groups)),
                                dim3(kThreads), lds, s, p, int(groups));
     } else {
         // 32 rows: a workgroup a CU (its registers hold 128 KiB of weights); 16: up to four, each the
@@ -356,7 +356,9 @@ hipError_t choose_few(const Product& p, int quant, hipStream_t s) {
     const int mt = int((p.M + 7) / 8);
     if constexpr (TYPE == kI8) {
         if (quant == kQuantBF16) return launch_few_as<TYPE, EPI, 1, 2, kQuantBF16>(p, s);
-        if (quant == kQuantF32) return launch_few_as<TYPE, EPI, 1, 2, kQuantF32>(p, s);
+        if constexpr (EPI != kGate8) {           // (gate and up read bf16 activations)
+            if (quant == kQuantF32) return launch_few_as<TYPE, EPI, 1, 2, kQuantF32>(p, s);
+        }
     }
     if constexpr (!GATE) {
         // 16 rows a workgroup leave CUs idle below N = 4096: 8 then
@@ -381,7 +383,7 @@ hipError_t choose_few(const Product& p, int quant, hipStream_t s) {
 hipError_t launch_few(int type, int epi, const Product& p, hipStream_t s, int x_type, bool quant) {
     if (p.M > kFewTokens) return hipErrorInvalidValue;
     const int q = !quant ? kNoQuant : x_type == MOE_A_F32 ? kQuantF32 : kQuantBF16;
-    if (quant && (type != kI8 || p.M > 8 || p.M * p.K > kFewQuant)) return hipErrorInvalidValue;
+    if (quant && (type != kI8 || p.M > 8 || p.M * p.K > kFewQuant || (epi == kGate8 && q == kQuantF32))) return hipErrorInvalidValue;
     if (type == kI8) {
         if (epi == kScale) return choose_few<kI8, kScale>(p, q, s);
         if (epi == kScale32) return choose_few<kI8, kScale32>(p, q, s);
