@@ -14,9 +14,7 @@ std::atomic<int> g_units[64];
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// Workspace of moe_i8_matmul: codes and scales of x, and partial sums of calls with few tokens
-// (more than kSplitTokens fill the chip unsplit).
-constexpr int64_t kSplitTokens = 1024;
+// Workspace of moe_i8_matmul: codes and scales of x, and partial sums of calls with few tokens.
 struct I8Work {
     int64_t codes = 0, scale = 0, part = 0, bytes = 0;
 };
@@ -25,7 +23,7 @@ I8Work i8_work(int64_t T, int64_t K) {
     if (T < 1) T = 1;
     w.scale = align256(T * K);
     w.part = align256(w.scale + T * 4);
-    w.bytes = w.part + (T > kSplitTokens ? 0 : kPartBytes);
+    w.bytes = w.part + i8_part_bytes(T);
     return w;
 }
 
@@ -108,16 +106,9 @@ int check_block(moe_ctx* ctx, int32_t T, bool i8) {
     return st == MOE_OK ? st : fail(ctx, st, why);
 }
 
-// Whether the few-token kernel quantises x itself: few enough numbers, rows that can be read
-// 16 bytes at a time, offsets below its range; and few enough outputs, since every 16 of them
-// convert all numbers again (4096 columns, one token: 8192 outputs 8.5 us against 10.8 in two
-// launches, 24576 20.3 against 21.0, 100003 77 against 67; 4 tokens: 4096 9.3 against 9.7, 6144 12.8
-// against 11.4, 100003 107 against 68; 1024 columns, 8 tokens, 4096 outputs 6.3 against 8.2).
-bool quantise_inside(const void* x, int x_type, int64_t ld, int32_t T, int32_t K, int32_t N) {
-    const int64_t es = x_type == MOE_A_F32 ? 4 : 2;
-    const int64_t results = int64_t(T) * N;
-    return T <= 8 && (results <= 16384 || (N <= 16384 && results * K <= int64_t(1) << 25)) && int64_t(T) * K <= kFewQuant && aligned(x, 16) && ld * es % 16 == 0 &&
-           (T == 1 || ld < (int64_t(1) << 25));
+// Rows of numbers that start on 16 bytes each.
+bool whole_rows(const void* x, int x_type, int64_t ld) {
+    return aligned(x, 16) && ld * (x_type == MOE_A_F32 ? 4 : 2) % 16 == 0;
 }
 
 int type_of(const moe_config& c) { return c.w_dtype == MOE_W_F32 ? kF32 : kBF16; }
@@ -191,7 +182,7 @@ int moe_i8_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, c
     const I8Work w = i8_work(T, K);
     p.part = static_cast<uint8_t*>(d_ws) + w.part;
     p.part_bytes = w.bytes - w.part;
-    const bool on_the_way = !codes && quantise_inside(d_x, x_type, ld_x, T, K, N);
+    const bool on_the_way = !codes && quantise_inside(ld_x, whole_rows(d_x, x_type, ld_x), T, K, N);
     if (!codes && !on_the_way) {
         int8_t* q = static_cast<int8_t*>(d_ws) + w.codes;
         float* sc = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + w.scale);
@@ -391,8 +382,8 @@ int moe_i8_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob8, vo
     float* xs = reinterpret_cast<float*>(ws + w.xs);
     float* hs = reinterpret_cast<float*>(ws + w.hs);
     hipError_t e = hipSuccess;
-    const bool x_inside = quantise_inside(d_x, MOE_A_BF16, c.hidden, T, c.hidden, 2 * c.inter);
-    const bool h_inside = quantise_inside(ws + w.h, MOE_A_F32, c.inter, T, c.inter, c.hidden);
+    const bool x_inside = quantise_inside(c.hidden, true, T, c.hidden, 2 * c.inter);
+    const bool h_inside = quantise_inside(c.inter, true, T, c.inter, c.hidden);
     Product p{};
     p.part = ws + w.part;
     p.part_bytes = kPartBytes;

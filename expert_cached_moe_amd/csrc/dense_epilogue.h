@@ -223,7 +223,7 @@ __device__ __forceinline__ void finish(const Product& p, int64_t m, int n, const
 
 // Columns of one row that take part in W results: the gated epilogues pair two runs of 16.
 template <int EPI>
-constexpr bool kPaired = EPI == kGate || EPI == kGate8;
+constexpr bool kPaired = paired(EPI);
 
 }  // namespace dense
 }  // namespace moe

@@ -55,6 +55,7 @@ using dev::kWave;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 constexpr uint32_t kOutside = 0xFFFFFFF0u, kRange = 0x80000000u;
 constexpr int kSlice = 128, kDepth = 4, kThreads = 512, kWaves = kThreads / kWave;
+static_assert(kWaves * kSlice * kDepth == kFewPass, "a pass of K");
 enum { kNoQuant = 0, kQuantBF16 = 1, kQuantF32 = 2 };
 constexpr int kMaxQuant = kFewQuant, kQuantVec = kMaxQuant / 8 / kThreads;   // vectors of 8 a thread
 constexpr int kCodePad = 16;             // bytes between the code rows: other banks
@@ -322,13 +323,10 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
     }
 }
 
-template <int TYPE, int EPI, int MT, int R, int QUANT, bool W = (MT > 1)>
-hipError_t launch_few_as(const Product& p, hipStream_t s) {
-    constexpr bool GATE = kPaired<EPI>;
+template <int TYPE, int EPI, int MT, int R, int QUANT, bool WALK>
+hipError_t launch_few_as(const Product& p, bool one, hipStream_t s) {
     const int64_t groups = (int64_t(p.N) + 8 * R - 1) / (8 * R);
-    constexpr bool WALK = W;
     const int lds = (WALK ? 2 : 1) * 2 * kWaves * MT * R * 16 * 16 + (QUANT ? int(p.M) * (p.K + kCodePad) : 0);
-    const bool one = p.K * (TYPE == kI8 ? 1 : TYPE == kBF16 ? 2 : 4) <= kWaves * kSlice * kDepth;
     if constexpr (!WALK) {
         static_assert(R <= 2, "registers for the next pass");
         if (one)
@@ -352,30 +350,21 @@ hipError_t launch_few_as(const Product& p, hipStream_t s) {
 
 template <int TYPE, int EPI>
 hipError_t choose_few(const Product& p, int quant, hipStream_t s) {
-    constexpr bool GATE = kPaired<EPI>;
-    const int mt = int((p.M + 7) / 8);
+    const Few f = plan_few(p.sizes(), elem_bytes(TYPE), kPaired<EPI>, quant != kNoQuant, compute_units());
     if constexpr (TYPE == kI8) {
-        if (quant == kQuantBF16) return launch_few_as<TYPE, EPI, 1, 2, kQuantBF16>(p, s);
+        if (quant == kQuantBF16) return launch_few_as<TYPE, EPI, 1, 2, kQuantBF16, false>(p, f.one, s);
         if constexpr (EPI != kGate8) {           // (gate and up read bf16 activations)
-            if (quant == kQuantF32) return launch_few_as<TYPE, EPI, 1, 2, kQuantF32>(p, s);
+            if (quant == kQuantF32) return launch_few_as<TYPE, EPI, 1, 2, kQuantF32, false>(p, f.one, s);
         }
     }
-    if constexpr (!GATE) {
-        // 16 rows a workgroup leave CUs idle below N = 4096: 8 then
-        if (p.N < 4096 && mt == 1) return launch_few_as<TYPE, EPI, 1, 1, kNoQuant>(p, s);
+    if constexpr (!kPaired<EPI>) {
+        if (f.r == 1) return launch_few_as<TYPE, EPI, 1, 1, kNoQuant, false>(p, f.one, s);
     }
-    // A walk of 32 rows at a time, one workgroup a CU, keeps the stream going from group to group and
-    // halves the reading of x: it wins where the rows fill the chip, in one pass of K (100003 x 4096
-    // codes 64 us at one token, 66 at 8 and 71 at 16, against 66, 70 and 86 with 16 rows) and, with
-    // three groups or more for every CU, in several (100003 x 8192 136 and 169 at 8 and 16 tokens
-    // against 177 and 222; 16384 x 16384 63 at 12 tokens against 61; at 2 tokens 139 against 118).
-    const bool one = int64_t(p.K) * (TYPE == kI8 ? 1 : TYPE == kBF16 ? 2 : 4) <= kWaves * kSlice * kDepth;
-    const bool walk = p.N >= 8192 && (one || (p.M > 2 && p.N >= 96 * compute_units()));
-    if (mt == 1 && walk) return launch_few_as<TYPE, EPI, 1, 4, kNoQuant, true>(p, s);
-    if (mt == 1) return launch_few_as<TYPE, EPI, 1, 2, kNoQuant>(p, s);
-    if (mt == 2 && walk) return launch_few_as<TYPE, EPI, 2, 4, kNoQuant>(p, s);
-    if (mt == 2) return launch_few_as<TYPE, EPI, 2, 2, kNoQuant>(p, s);
-    return launch_few_as<TYPE, EPI, 4, 2, kNoQuant>(p, s);
+    if (f.mt == 1 && f.walk) return launch_few_as<TYPE, EPI, 1, 4, kNoQuant, true>(p, f.one, s);
+    if (f.mt == 1) return launch_few_as<TYPE, EPI, 1, 2, kNoQuant, false>(p, f.one, s);
+    if (f.mt == 2 && f.r == 4) return launch_few_as<TYPE, EPI, 2, 4, kNoQuant, true>(p, f.one, s);
+    if (f.mt == 2) return launch_few_as<TYPE, EPI, 2, 2, kNoQuant, true>(p, f.one, s);
+    return launch_few_as<TYPE, EPI, 4, 2, kNoQuant, true>(p, f.one, s);
 }
 
 }  // namespace

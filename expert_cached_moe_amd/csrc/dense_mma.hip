@@ -54,7 +54,7 @@ typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kXcds = 8, kGroupM = 8;
-constexpr int kSlice = 128;                       // bytes of K in a slice
+constexpr int kSlice = kSliceBytes;
 constexpr uint32_t kOutside = 0xFFFFFFF0u;        // a buffer offset past every range
 constexpr uint32_t kRange = 0x80000000u;          // range of the buffer descriptors: 2 GiB
 
@@ -451,9 +451,6 @@ __device__ __forceinline__ void finish_tile(const Product& p, int64_t m0, int n0
     }
 }
 
-// Elements between the rows of a partial sum: a multiple of 8 from N up.
-__host__ __device__ inline int64_t part_ld(const Product& p) { return (int64_t(p.N) + 7) / 8 * 8; }
-
 // 128 x 128 and 64 x 64 tiles: 4 waves, two LDS stages.  The one barrier of a slice stands before
 // its last quarter, so the loads of a slice have a whole slice's time to land and the matrix
 // instructions of the last quarter cover the first reads of the next slice.
@@ -570,9 +567,10 @@ __device__ __forceinline__ void mma_tile(const Product& p, int block, int m_tile
     __syncthreads();                                         // the stages are read
     const int64_t mw = m0 + wm * C::TM;
     const int nw = n0 + wn * C::TN;
+    const int64_t row_ld = part_ld(p.N);
     if (splits > 1)
         finish_tile<TYPE, EPI, C, true>(p, mw, nw, acc, lds,
-                                        static_cast<typename Elem<TYPE>::Acc*>(p.part) + split * p.M * part_ld(p), part_ld(p));
+                                        static_cast<typename Elem<TYPE>::Acc*>(p.part) + split * p.M * row_ld, row_ld);
     else
         finish_tile<TYPE, EPI, C, false>(p, mw, nw, acc, lds, nullptr, 0);
 }
@@ -642,7 +640,7 @@ __device__ __forceinline__ void turns_tile(const Product& p, int block, int m_ti
     const int n0 = mn.y * C::BN;
     const int n = (p.K + KS - 1) / KS;                        // slices
 
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const int wave = threadIdx.x / kWave;
     const int wm = wave / C::WN, wn = wave % C::WN;
     const bool second = __builtin_amdgcn_readfirstlane(wave) >= 4;    // (SIMD i has waves i and i + 4)
     Side<C::BM, AKC, ES, C::NW> sa;
@@ -770,7 +768,7 @@ __global__ void __launch_bounds__(256) k_join(const Product p, int splits) {
     typedef typename Elem<TYPE>::Acc S;
     typedef typename Frag<TYPE>::Acc V4;
     constexpr bool PAIR = kPaired<EPI>;
-    const int64_t ld = part_ld(p), units = PAIR ? p.N / 8 : ld / 4, i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+    const int64_t ld = part_ld(p.N), units = PAIR ? p.N / 8 : ld / 4, i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i >= p.M * units) return;
     const int64_t m = i / units;
     const int k = int(i % units), n = PAIR ? k / 4 * 32 + k % 4 * 4 : k * 4;
@@ -811,7 +809,7 @@ hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done)
     return e;
 }
 
-int64_t part_bytes(const Product& p, int splits) { return p.M * part_ld(p) * splits * 4; }
+int64_t part_bytes(const Product& p, int splits) { return p.M * part_ld(p.N) * splits * 4; }
 
 // LDS of a workgroup.  One slice needs one stage; twice the workgroups on a CU then hide each
 // other's one trip to memory (gradients of the 4096 x 1536 block from 37 tokens 13.6 against 16.6 us).
@@ -837,7 +835,7 @@ Tiles tiles_of(const Product& p, int splits) {
 template <int TYPE, int EPI>
 hipError_t launch_join(const Product& p, int splits, hipStream_t s) {
     // (few results: more workgroups of one wave)
-    const int64_t items = p.M * (kPaired<EPI> ? p.N / 8 : part_ld(p) / 4);
+    const int64_t items = p.M * (kPaired<EPI> ? p.N / 8 : part_ld(p.N) / 4);
     const int threads = items < 256 * 1024 ? 64 : 256;
     hipLaunchKernelGGL((k_join<TYPE, EPI>), dim3(unsigned((items + threads - 1) / threads)), dim3(threads), 0, s, p, splits);
     return hipGetLastError();
@@ -888,58 +886,20 @@ hipError_t launch_two(const Product& p, const Product& q, int splits, hipStream_
     return e;
 }
 
-// Tile and split of K: the least of the times that a model fitted to measurements gives, in us.
-// A slice takes `slice` and `more` for each further workgroup on its CU (up to `slots`), a tile
-// `tile` to start and finish; a split costs a second kernel and its partial sums both ways.
-// Measured (8-bit codes, whole call): 300 x 4096 x 4096: 256-tiles 40 us, 128 20, 64 13, 128
-// split in two 23; 2000 x 4096 x 4096: 44, 34, 50; 1024 x 8192 x 8192: 74, 63, 94; 100 x 8192 x
-// 4096: 64-tiles 19, split in two 16.6, in eight 21.  fp32: eight times the matrix time.  Four
-// stages instead of two on the smaller tiles, and 256 x 128 tiles in turns, gained nothing.
-struct Choice {
-    int tile, splits;
-};
-Choice plan(const Product& p, const Product* q, int es, int64_t n_cu) {
-    struct Kind { int bm, bn, slots; double slice, more, tile; };
-    static const Kind half[] = {{256, 256, 1, 1.3, 0.0, 6.0}, {128, 128, 2, 0.68, 0.28, 3.0}, {64, 64, 4, 0.36, 0.13, 1.5}};
-    static const Kind fp32[] = {{256, 256, 1, 8.6, 0.0, 6.0}, {128, 128, 2, 2.3, 2.1, 3.0}, {64, 64, 4, 0.65, 0.55, 1.5}};
-    const Kind* kinds = es == 4 ? fp32 : half;
-    const int64_t nk = (int64_t(p.K) * es + kSlice - 1) / kSlice;
-    static const int splits[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32};
-    const int64_t one = p.M * part_ld(p) + (q ? q->M * part_ld(*q) + 64 : 0);       // numbers of one split's sums
-    Choice best{0, 1};
-    double best_t = 1e30;
-    for (int c = 0; c < 3; ++c) {
-        const Kind& k = kinds[c];
-        auto count = [&](const Product& r) { return (r.M + k.bm - 1) / k.bm * ((r.N + k.bn - 1) / k.bn); };
-        const int64_t tiles = count(p) + (q ? count(*q) : 0);
-        for (int sp : splits) {
-            if (sp > 1 && sp * 4 > nk) break;
-            const int64_t sums = one * sp, share = (nk + sp - 1) / sp;
-            // (256-tiles that could be split and still fill the chip would need more scratch)
-            if (sp > 1 && (sums * 4 > p.part_bytes || c == 0)) break;
-            if (share * (sp - 1) >= nk) continue;            // every split has slices
-            const int64_t groups = tiles * sp, rounds = (groups + n_cu * k.slots - 1) / (n_cu * k.slots);
-            const int64_t on_cu = (groups + n_cu - 1) / n_cu < k.slots ? (groups + n_cu - 1) / n_cu : k.slots;
-            const double t = rounds * (share * (k.slice + k.more * (on_cu - 1)) + k.tile) + (sp > 1 ? 3.0 + sums * 1.4e-6 : 0.0);
-            if (t < best_t) best_t = t, best = Choice{c, sp};
-        }
-    }
-    return best;
-}
-
 template <int TYPE, int LAYOUT, int EPI>
 hipError_t choose_two(const Product& p, const Product& q, hipStream_t s) {
-    const Choice c = plan(p, &q, Frag<TYPE>::ES, compute_units());
-    if (c.tile == 0) return launch_two<TYPE, LAYOUT, EPI, Turns>(p, q, c.splits, s);
-    if (c.tile == 1) return launch_two<TYPE, LAYOUT, EPI, Mid>(p, q, c.splits, s);
+    const Sizes second = q.sizes();
+    const Tiling c = plan_tiles(p.sizes(), &second, Frag<TYPE>::ES, p.part_bytes, compute_units());
+    if (c.tile == kTile256) return launch_two<TYPE, LAYOUT, EPI, Turns>(p, q, c.splits, s);
+    if (c.tile == kTile128) return launch_two<TYPE, LAYOUT, EPI, Mid>(p, q, c.splits, s);
     return launch_two<TYPE, LAYOUT, EPI, Small>(p, q, c.splits, s);
 }
 
 template <int TYPE, int LAYOUT, int EPI>
 hipError_t choose(const Product& p, hipStream_t s) {
-    const Choice c = plan(p, nullptr, Frag<TYPE>::ES, compute_units());
-    if (c.tile == 0) return launch<TYPE, LAYOUT, EPI, Turns>(p, c.splits, s);
-    if (c.tile == 1) return launch<TYPE, LAYOUT, EPI, Mid>(p, c.splits, s);
+    const Tiling c = plan_tiles(p.sizes(), nullptr, Frag<TYPE>::ES, p.part_bytes, compute_units());
+    if (c.tile == kTile256) return launch<TYPE, LAYOUT, EPI, Turns>(p, c.splits, s);
+    if (c.tile == kTile128) return launch<TYPE, LAYOUT, EPI, Mid>(p, c.splits, s);
     return launch<TYPE, LAYOUT, EPI, Small>(p, c.splits, s);
 }
 
@@ -947,7 +907,7 @@ hipError_t choose(const Product& p, hipStream_t s) {
 
 hipError_t launch_product(int type, int layout, int epi, const Product& p, hipStream_t s) {
     if (p.M <= 0 || p.N <= 0) return hipSuccess;
-    if (layout == kNT && few_tokens(p, type == kI8 ? 1 : type == kBF16 ? 2 : 4)) return launch_few(type, epi, p, s);
+    if (layout == kNT && few_tokens(p.sizes(), elem_bytes(type))) return launch_few(type, epi, p, s);
     if (type == kI8) {
         if (layout == kNT && epi == kScale) return choose<kI8, kNT, kScale>(p, s);
         if (layout == kNT && epi == kScale32) return choose<kI8, kNT, kScale32>(p, s);

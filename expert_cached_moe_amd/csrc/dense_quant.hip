@@ -17,7 +17,7 @@ namespace moe {
 namespace dense {
 namespace {
 
-constexpr int kVec = 8;
+constexpr int kVec = kQuantizeVec;
 
 // 8 numbers of a row from index i (in bounds, since cols is a multiple of 16)
 template <bool BF16, bool VEC>
@@ -127,18 +127,15 @@ void launch_rows(const void* x, int64_t ld, int64_t rows, int cols, int8_t* q, f
     typedef std::integral_constant<int, 1> H1;
     typedef std::integral_constant<int, 2> H2;
     typedef std::integral_constant<int, 4> H4;
-    if (rows <= 512 && cols > 256 * kVec) {
-        if (cols <= 1024 * kVec) go(Many{}, H1{});
-        else if (cols <= 1024 * kVec * 2) go(Many{}, H2{});
-        else go(Many{}, H4{});
-    } else if (cols <= 256 * kVec) {
-        go(Some{}, H1{});
-    } else if (cols <= 256 * kVec * 2) {
-        go(Some{}, H2{});
-    } else if (cols <= 256 * kVec * 4) {
-        go(Some{}, H4{});
+    const RowThreads c = plan_rows(rows, cols);
+    if (c.threads == 256) {
+        if (c.hold == 1) go(Some{}, H1{});
+        else if (c.hold == 2) go(Some{}, H2{});
+        else go(Some{}, H4{});
     } else {
-        go(Many{}, H2{});
+        if (c.hold == 1) go(Many{}, H1{});
+        else if (c.hold == 2) go(Many{}, H2{});
+        else go(Many{}, H4{});
     }
 }
 }  // namespace
