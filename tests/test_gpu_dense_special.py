@@ -1,11 +1,12 @@
-"""Dense operators on values far out: gates near the end of fp32, and shut gates with large
-gradients behind them."""
+"""Dense operators on values far out: gates near the end of fp32, shut gates with large gradients
+behind them, and tokens or weight rows with infinities and NaNs beside ordinary ones."""
 import numpy as np
 import pytest
 import torch
 
 from oracle import dense_oracle as D
-from test_gpu_dense import BF16, F32, NAME, TORCH, Ctx, Guarded, _blob, _check, _views, f64
+from test_gpu_dense import (BF16, F32, NAME, TORCH, Ctx, Guarded, _blob, _block_inputs, _check, _matmul, _views, f64,
+                            normal, same_bits)
 from test_gpu_dense import B  # noqa: F401  (fixture)
 
 pytestmark = pytest.mark.gpu
@@ -100,3 +101,86 @@ def test_block_backward_shut_gates(B, T, w):
     _check("dwg", dwg, ref[1], bounds["dwg"])
     _check("dwu", dwu, ref[2], bounds["dwu"])
     _check("dwd", f64(dd), ref[3], bounds["dwd"])
+
+
+TOKENS = [(3, 64, 64), (12, 320, 96), (40, 192, 544), (300, 576, 160), (2100, 1088, 2080)]
+
+
+def _step(B, c, x, dy, blob, w):
+    T, H = x.shape
+    work = torch.full((B.moe_dense_workspace_bytes(c.cfg, T),), 0xFF, dtype=torch.uint8, device="cuda")
+    save = torch.full((B.moe_dense_save_bytes(c.cfg, T),), 0xFF, dtype=torch.uint8, device="cuda")
+    y, dx, grad = torch.empty_like(x), torch.empty_like(x), torch.zeros_like(blob)
+    B.moe_dense_ffn(c.p, x, T, blob, save, y, work)
+    B.moe_dense_ffn_backward(c.p, dy, x, T, blob, save, dx, grad, work)
+    torch.cuda.synchronize()
+    gu, dd = _views(grad, H, c.cfg.inter, TORCH[w])
+    return y, dx, gu.clone(), dd.clone()
+
+
+@pytest.mark.parametrize("T,H,I", TOKENS)
+@pytest.mark.parametrize("w", [BF16, F32])
+def test_block_keeps_tokens_apart(B, w, T, H, I):
+    """A token with a NaN, an infinity or numbers whose products overflow leaves y and dx of the
+    others as they are, bit for bit; so does one in dy, which reaches one row of dWd."""
+    rng = np.random.default_rng(T)
+    x, dy, wg, wu, wd = _block_inputs(rng, T, H, I, w)
+    at, others = T // 2, [t for t in range(T) if t != T // 2]
+    with Ctx(B, H, I, w) as c:
+        blob = _blob(B, c, wg, wu, wd)
+        y, dx, gu, dd = _step(B, c, x, dy, blob, w)
+        for bad in (float("nan"), float("inf"), 3e38):
+            x2 = x.clone()
+            x2[at, 7 if bad != 3e38 else slice(None)] = bad
+            y2, dx2, _, _ = _step(B, c, x2, dy, blob, w)
+            assert same_bits(y2[others], y[others]) and same_bits(dx2[others], dx[others])
+            if bad != bad:
+                assert torch.isnan(y2[at]).all() and torch.isnan(dx2[at]).all()
+            dy2 = dy.clone()
+            dy2[at, 5] = bad
+            y2, dx2, gu2, dd2 = _step(B, c, x, dy2, blob, w)
+            rest = [h for h in range(H) if h != 5]
+            assert same_bits(y2, y) and same_bits(dx2[others], dx[others]) and same_bits(dd2[rest], dd[rest])
+            if bad != bad:
+                assert torch.isnan(dx2[at]).all() and torch.isnan(dd2[5]).all() and torch.isnan(gu2).all()
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 64, 64)] + TOKENS)
+def test_i8_block_keeps_tokens_apart(B, T, H, I):
+    rng = np.random.default_rng(T)
+    x, _, wg, wu, wd = _block_inputs(rng, T, H, I, BF16)
+    at, others = T // 2, [t for t in range(T) if t != T // 2]
+    with Ctx(B, H, I) as c:
+        b8 = _pack8(B, c, wg, wu, wd)
+        y = _i8_ffn(B, c, x, b8)
+        assert torch.isfinite(y.float()).all()
+        for bad in (float("nan"), float("inf"), -float("inf")):
+            x2 = x.clone()
+            x2[at, 7] = bad
+            y2 = _i8_ffn(B, c, x2, b8)
+            assert torch.isnan(y2[at]).all() and same_bits(y2[others], y[others])
+        x2 = x.clone()
+        x2[at] = 0
+        y2 = _i8_ffn(B, c, x2, b8)
+        assert not y2[at].any() and same_bits(y2[others], y[others])
+
+
+@pytest.mark.parametrize("T", [1, 5, 12, 40, 300, 2100])
+def test_i8_matmul_special_weight_rows(B, T):
+    """Weight rows with a NaN or an infinity make their column NaN, zero rows zeros; the others are
+    unchanged."""
+    K, N = 272, 163
+    rng = np.random.default_rng(T)
+    x, w = normal(rng, (T, K), BF16), normal(rng, (N, K), F32)
+    with Ctx(B) as c:
+        def run(w):
+            q, s = torch.empty((N, K), dtype=torch.int8, device="cuda"), torch.empty(N, device="cuda")
+            B.moe_i8_quantize(c.p, w, F32, K, N, K, q, s)
+            return _matmul(B, c, x, BF16, K, None, T, q, s, N, K, F32, N)
+        y = run(w)
+        w2 = w.clone()
+        w2[3, 9], w2[100, 0], w2[162, 271], w2[64] = float("nan"), float("inf"), -float("inf"), 0
+        y2 = run(w2)
+    others = [n for n in range(N) if n not in (3, 64, 100, 162)]
+    assert torch.isnan(y2[:, [3, 100, 162]]).all() and not y2[:, 64].any()
+    assert same_bits(y2[:, others], y[:, others])
