@@ -20,7 +20,7 @@ template <> struct Elem<kI8> { typedef int8_t T; typedef int Acc; };
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(uint16_t* p, float v) { *p = dev::f32_to_bf16_bits(v); }
 
-// 1 / (1 + e^-z): e^-z overflows to infinity for z < -88, which gives the limit 0.
+// 1 / (1 + e^-z): e^-z overflows to infinity for z < -88.7, which gives the limit 0.
 __device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
 // z / (1 + e^-z) within four steps of fp32 for z >= -87, from the hardware's exp2 and reciprocal (a step
 // each): the rounding of z log2(e), which grows with z, and log2(e)'s own are carried into the result.

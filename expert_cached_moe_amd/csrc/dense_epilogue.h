@@ -59,7 +59,9 @@ __device__ __forceinline__ void load_row(float (&v)[W], const float* p) {
 }
 
 // Pre-activations kept for the backward pass.  fp32: as they are.  bf16 contexts: the upper 24
-// bits of the fp32 sums (16 fraction bits), 16 in one array and 8 in another of the same shape.
+// bits of the fp32 sums (a sign, 8 exponent bits, 15 fraction bits), 16 in one array and 8 in another
+// of the same shape.  They are cut there, not rounded: by less than 2^-15 of the value, 1/128 of the
+// rounding of dg and du that follows.
 // Rounded to bf16 they would be a third rounding of that size in the gradients, after those of
 // dg, du and of the result (relative error of dWg and dx 0.0030 against 0.0023); all 32 bits
 // would cost another third of the bytes.
@@ -108,8 +110,9 @@ __device__ __forceinline__ void kept_row(float (&v)[W], const uint16_t* hi, cons
 }
 
 // The sigmoid of the block's kernels.  fp32: expf and a division.  bf16: hardware exp2 and
-// reciprocal (about one fp32 step each; the results are rounded to bf16, 2^16 times coarser).
-// Either way e^-z overflows to infinity for very negative z, whose reciprocal is 0.
+// reciprocal (about one fp32 step each, and the argument's rounding times its size; the results are
+// rounded to bf16, 2^16 times coarser).  Either way the result is 0 from about z = -88 down, where
+// e^-z overflows to infinity.
 template <int TYPE>
 __device__ __forceinline__ float sigmoid_of(float z) {
     if constexpr (TYPE == kF32) return sigmoid(z);

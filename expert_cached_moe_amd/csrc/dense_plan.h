@@ -39,7 +39,9 @@ struct Sizes {
 constexpr int64_t kPartBytes = int64_t(32) << 20;
 // Elements between the rows of a partial sum: a multiple of 8 from N up.
 constexpr int64_t part_ld(int32_t N) { return (int64_t(N) + 7) / 8 * 8; }
-// Scratch of moe_i8_matmul for partial sums.
+// Scratch of moe_i8_matmul for partial sums.  More than kSplitTokens tokens are never split: wide
+// outputs fill the chip unsplit; narrow ones would gain (2048 x 256 x 8192, by the model of plan_tiles,
+// 24.5 us against 15.3 split), at the price of 32 MiB more for every workspace.
 constexpr int64_t kSplitTokens = 1024;
 inline int64_t i8_part_bytes(int64_t T) { return T > kSplitTokens ? 0 : kPartBytes; }
 
@@ -113,7 +115,8 @@ constexpr int kSliceBytes = 128;      // of K in a slice
 // Measured (8-bit codes, whole call): 300 x 4096 x 4096: 256-tiles 40 us, 128 20, 64 13, 128
 // split in two 23; 2000 x 4096 x 4096: 44, 34, 50; 1024 x 8192 x 8192: 74, 63, 94; 100 x 8192 x
 // 4096: 64-tiles 19, split in two 16.6, in eight 21.  fp32: eight times the matrix time.  Four
-// stages instead of two on the smaller tiles, and 256 x 128 tiles in turns, gained nothing.
+// stages instead of two on the smaller tiles, and 256 x 128 tiles in turns, gained nothing.  It ranks
+// tiles; as a time it can be far off (777 x 2051 x 1552 codes: 7.9 by the model, 11.7 measured).
 struct Tiling {
     int tile, splits;            // tile: kTile256, kTile128, kTile64
 };

@@ -11,7 +11,7 @@ import numpy as np
 
 F32_HALF = 2.0 ** -24
 HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
-KEPT = {"f32": 0.0, "bf16": 2.0 ** -15}          # pre-activations: fp32 cut after 16 fraction bits
+KEPT = {"f32": 0.0, "bf16": 2.0 ** -15}          # pre-activations: fp32 cut after 15 fraction bits
 # exp, the reciprocal and the products of the sigmoid: a few steps each, and the argument's own
 # rounding times its size (|z| <= 88 before the result is 0 or 1)
 SIGMOID_REL = 2.0 ** -17
