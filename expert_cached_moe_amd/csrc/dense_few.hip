@@ -140,7 +140,8 @@ __global__ void __launch_bounds__(kThreads) k_few(const Product p0, int groups) 
     }
     const __amdgpu_buffer_rsrc_t rx = rsrc(p.a);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) xo[m] = uint32_t(min(m * 8 + l8, T - 1)) * (QUANT != kNoQuant ? p.K + kCodePad : uint32_t(p.lda * ES));
+    for (int m = 0; m < MT; ++m)
+        xo[m] = uint32_t(min(m * 8 + l8, T - 1)) * (QUANT != kNoQuant ? p.K + kCodePad : uint32_t(p.lda * ES));
     constexpr uint32_t kStride = kWaves * kSlice, kPass = kStride * kDepth;
     // K goes in passes; group g begins with pass g % passes
     constexpr bool SINGLE = ONE || (!WALK && !AHEAD);
@@ -372,7 +373,8 @@ hipError_t choose_few(const Product& p, int quant, hipStream_t s) {
 hipError_t launch_few(int type, int epi, const Product& p, hipStream_t s, int x_type, bool quant) {
     if (p.M > kFewTokens) return hipErrorInvalidValue;
     const int q = !quant ? kNoQuant : x_type == MOE_A_F32 ? kQuantF32 : kQuantBF16;
-    if (quant && (type != kI8 || p.M > 8 || p.M * p.K > kFewQuant || (epi == kGate8 && q == kQuantF32))) return hipErrorInvalidValue;
+    if (quant && (type != kI8 || p.M > 8 || p.M * p.K > kFewQuant)) return hipErrorInvalidValue;
+    if (epi == kGate8 && q == kQuantF32) return hipErrorInvalidValue;
     if (type == kI8) {
         if (epi == kScale) return choose_few<kI8, kScale>(p, q, s);
         if (epi == kScale32) return choose_few<kI8, kScale32>(p, q, s);

@@ -1,5 +1,6 @@
 // Prints the kernels that calls of the dense operators launch on a GPU of 256 compute units, one line
-// a call, from the rules that the library itself uses (" split": with K split over workgroups).  Calls, one a line, on the standard input:
+// a call, from the rules that the library itself uses (" split": with K split over workgroups).
+// Calls, one a line, on the standard input:
 //   m X LD WHOLE T N K Y   moe_i8_matmul: x and y types (MOE_A_*), elements between x's rows, whether
 //                          those start on 16 bytes
 //   8 T H I                moe_i8_ffn
