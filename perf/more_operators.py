@@ -10,17 +10,17 @@ Four operators of the layer and of the dense parts around it:
   train    the same with its gradient: from the gates' gradients to the logits'
            (``moe_route_scored_backward``);
   linear4  y = x . W^T with W held in 4-bit codes, a scale and a zero point for each group of 32,
-           64 or 128 along K, one scale per output channel (``moe_i4_matmul``; the weights are
-           quantised once by ``moe_i4_quantize``);
+           64 or 128 along K, one power of two per output channel (``moe_i4_matmul``; the weights
+           are quantised once by ``moe_i4_quantize``);
   experts4 the routed experts and the shared one from 4-bit blobs, gate, up and down products, one
            result for each pair of a token and an expert (``moe_i4_expert_ffn`` on blobs of
            ``moe_i4_pack``).
 
 ``own`` chooses between the plain form (elementary torch operations) and the library.
 
-4-bit rows: weight = S * (s * (code - z)) with codes 0..15, the row's scale S (fp32), the group's
-scale s (an e4m3 number up to 448) and zero point z (0..15; 8 where the rows are held without zero
-points).  s * (code - z) has eight significant bits, so it is exact in bf16.
+4-bit rows: weight = S * s * (code - z) with codes 0..15, the row's scale S (a power of two), the
+group's scale s (an e4m3 number up to 448) and zero point z (0..15; 8 where the rows are held without
+zero points).  The product has eight significant bits, so every weight is exact in bf16.
 """
 import torch
 
@@ -109,10 +109,10 @@ def work(case):
     if op == "linear4":
         K, N = case["K"], case["N"]
         xb, yb = (4 if case["x"] == F32 else 2), (4 if case["y"] == F32 else 2)
-        return {"bytes": T * K * xb + N * (K // 2 + 2 * -(-K // G) + 4) + T * N * yb, "flops": 2 * T * N * K}
+        return {"bytes": T * K * xb + N * (K // 2 + 2 * -(-K // G) + 1) + T * N * yb, "flops": 2 * T * N * K}
     H, I, E, k = case["H"], case["I"], case["E"], case["k"]
     used = min(E, T * k) if T == 1 else E * (1 - (1 - k / E) ** T)       # experts that some token uses
-    blob = 2 * I * (H // 2 + 2 * -(-H // G) + 4) + H * (I // 2 + 2 * -(-I // G) + 4)
+    blob = 2 * I * (H // 2 + 2 * -(-H // G) + 1) + H * (I // 2 + 2 * -(-I // G) + 1)
     rows = T * k + T * case["shared"]
     return {"bytes": int((used + case["shared"]) * blob) + 2 * T * H + 2 * rows * H + 4 * T * k,
             "flops": 6 * rows * H * I}
@@ -219,7 +219,7 @@ def prepare(case, seed):
             return st
         N, K = w.shape
         h = st["h"] = _Handle(B)
-        st["codes"], st["scale"] = _bytes(N * K // 2), torch.empty(N, device="cuda")
+        st["codes"], st["scale"] = _bytes(N * K // 2), _bytes(N)
         st["words"] = torch.empty((N, -(-K // G)), dtype=torch.int16, device="cuda")
         B.moe_i4_quantize(h.ctx, w, BF16, K, N, K, G, zero, st["codes"], st["words"], st["scale"], _stream())
         st["y"] = torch.empty((T, N), dtype=TORCH[case["y"]], device="cuda")
@@ -280,9 +280,10 @@ def run(st):
 # ---------------------------------------------------------------- plain form
 
 def _quantise(w, G, zero):
-    """(two codes a byte, group scales, zero points, row scales) of rows: a row's scale makes its widest
-    group's 448; group scales are e4m3 numbers, to nearest even, or up where there are zero points, so that
-    the range fits 15 steps; codes from quotients in 64 bits, half to even."""
+    """(two codes a byte, group scales, zero points, row scales) of rows: a row's scale is the least power
+    of two that leaves its group scales at 448 or less; group scales are e4m3 numbers, to nearest even, or
+    up where there are zero points, so that the range fits 15 steps; codes from quotients in 64 bits, half
+    to even."""
     N, K = w.shape
     Kg = -(-K // G)
     v = torch.zeros((N, Kg * G), dtype=torch.float64, device=w.device)
@@ -293,10 +294,12 @@ def _quantise(w, G, zero):
         span = hi - lo
     else:
         span, steps = v.abs().amax(2), 7.0
-    S = (span.amax(1) / (steps * 448.0)).float()
-    S[S < 2.0 ** -126] = 0
-    d = S.double()[:, None]
-    u = torch.where(d > 0, span / torch.where(d > 0, steps * d, 1.0), 0.0)
+    t = span / steps
+    m, e = torch.frexp(t.amax(1) / 448.0)
+    S = torch.exp2((e - (m == 0.5).int()).double())
+    S = torch.where((m > 0) & (S >= 2.0 ** -100), S, 0.0)
+    d = S[:, None]
+    u = torch.where(d > 0, t / torch.where(d > 0, d, 1.0), 0.0)
     e = torch.frexp(u).exponent.clamp(min=-5)                          # 2^(e - 1) <= u < 2^e, or subnormal
     unit = torch.exp2(e.double() - 4)
     s = ((u / unit).ceil() if zero else (u / unit).round()) * unit
@@ -307,7 +310,7 @@ def _quantise(w, G, zero):
     z = torch.where(d > 0, z, 8.0)
     c = torch.where(d > 0, ((v / safe).round() + z).clamp(0, 15), 8.0)
     c = c.view(N, Kg * G)[:, :K].to(torch.uint8)
-    return c[:, 0::2] | (c[:, 1::2] << 4), s.float(), z[:, :, 0].float(), S
+    return c[:, 0::2] | (c[:, 1::2] << 4), s.float(), z[:, :, 0].float(), S.float()
 
 
 def _weights(q, G):
@@ -412,10 +415,11 @@ def _nearest_weights(w, G, zero):
         width, n = [a - b for a, b in zip(top, low)], 15
     else:
         width, n = [torch.max(a, -b) for a, b in zip(top, low)], 7
-    row = torch.stack(width).max(0).values.div(n * 448).to(torch.float32).to(torch.float64)
-    row = torch.where(row < 2.0 ** -126, 0.0, row)
+    widest = torch.stack(width).max(0).values
+    row = torch.pow(2.0, torch.ceil(torch.log2(widest.div(n) / 448)))
+    row = torch.where((widest > 0) & (row >= 2.0 ** -100), row, 0.0)
     for i, p in enumerate(parts):
-        t = torch.where(row > 0, width[i] / (n * torch.where(row > 0, row, 1.0)), 0.0)
+        t = torch.where(row > 0, width[i] / n / torch.where(row > 0, row, 1.0), 0.0)
         quantum = torch.ldexp(torch.ones_like(t), torch.floor(torch.log2(t.clamp(min=2.0 ** -6))).to(torch.int32) - 3)
         t = (torch.ceil(t / quantum) if zero else torch.round(t / quantum)).mul(quantum).clamp(max=448)
         step = (row * t)[:, None]
