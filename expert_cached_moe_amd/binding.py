@@ -24,6 +24,7 @@ MOE_OK, MOE_EINVAL, MOE_ESHAPE, MOE_ECAPACITY, MOE_EHIP, MOE_EUNSUPPORTED, MOE_E
 MOE_W_F32, MOE_W_BF16, MOE_W_MXFP4 = 0, 1, 2
 MOE_A_F32, MOE_A_BF16, MOE_A_I8 = 0, 1, 2
 MOE_Q_NEAREST, MOE_Q_ARGMIN = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 c_i32p = ctypes.POINTER(ctypes.c_int32)
 c_f32p = ctypes.POINTER(ctypes.c_float)
@@ -40,7 +41,7 @@ EXPORTS = [
     "moe_expert_ffn_merge_noalloc", "moe_noalloc_scratch_bytes",
     "moe_i8_workspace_bytes", "moe_i8_quantize", "moe_i8_matmul", "moe_dense_workspace_bytes",
     "moe_dense_save_bytes", "moe_dense_ffn", "moe_dense_ffn_backward", "moe_i8_blob_bytes", "moe_i8_pack",
-    "moe_i8_ffn",
+    "moe_i8_ffn", "moe_route_scored", "moe_route_scored_backward",
 ]
 
 
@@ -69,6 +70,11 @@ class moe_stats(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("steps", "distinct", "hits", "misses", "fills", "host", "evictions")]
 
 
+class moe_route_rule(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "n_groups", "keep_groups", "group_top", "renormalize")] + [
+        ("scale", ctypes.c_float)]
+
+
 _P = ctypes.POINTER
 _sig = {
     "moe_create": (ctypes.c_int, [_P(moe_config), _P(vp)]),
@@ -82,6 +88,8 @@ _sig = {
     "moe_bind_pools": (ctypes.c_int, [vp, vp, ctypes.c_int32, vp, ctypes.c_int32]),
     "moe_route": (ctypes.c_int, [vp, vp, ctypes.c_int32, vp, vp, vp, vp, vp, vp, vp, vp]),
     "moe_router_logits": (ctypes.c_int, [vp, vp, ctypes.c_int32, vp, vp, vp]),
+    "moe_route_scored": (ctypes.c_int, [vp, vp, vp, ctypes.c_int32, _P(moe_route_rule), vp, vp, vp, vp, vp, vp, vp, vp]),
+    "moe_route_scored_backward": (ctypes.c_int, [vp, vp, ctypes.c_int32, _P(moe_route_rule), vp, vp, vp, vp]),
     "moe_qstar": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_double, ctypes.c_double, ctypes.c_int32]),
     "moe_lru_step": (ctypes.c_int, [vp, ctypes.c_int32, vp, ctypes.c_int32, _P(moe_plan)]),
     "moe_lru_replay": (ctypes.c_int, [vp, ctypes.c_int32, vp, ctypes.c_int32, ctypes.c_int32, vp, _P(moe_stats)]),
@@ -163,6 +171,11 @@ def make_config(hidden, inter, n_experts, top_k, n_shared=0, n_slots=0, n_layers
                       q_round, bp_gbps, bh_gbps)
 
 
+def make_route_rule(score=MOE_SCORE_SOFTMAX, n_groups=1, keep_groups=1, group_top=1, renormalize=1,
+                    scale=1.0) -> moe_route_rule:
+    return moe_route_rule(score, n_groups, keep_groups, group_top, renormalize, scale)
+
+
 # ------------------------------------------------------------------ entry points (C names)
 def moe_create(cfg: moe_config) -> int:
     out = vp()
@@ -223,6 +236,18 @@ def moe_router_logits(ctx, d_x, T, d_wr, d_logits, s=None) -> None:
 def moe_route(ctx, d_logits, T, d_topk_ids, d_topk_w, d_counts, d_offsets, d_perm, d_inv, d_ws, s=None) -> None:
     _check(ctx, _lib.moe_route(ctx, _ptr(d_logits), T, _ptr(d_topk_ids), _ptr(d_topk_w), _ptr(d_counts),
                                _ptr(d_offsets), _ptr(d_perm), _ptr(d_inv), _ptr(d_ws), _stream(s)))
+
+
+def moe_route_scored(ctx, d_logits, d_bias, T, rule, d_topk_ids, d_topk_w, d_counts, d_offsets, d_perm, d_inv, d_ws,
+                     s=None) -> None:
+    _check(ctx, _lib.moe_route_scored(ctx, _ptr(d_logits), _ptr(d_bias), T, ctypes.byref(rule) if rule else None,
+                                      _ptr(d_topk_ids), _ptr(d_topk_w), _ptr(d_counts), _ptr(d_offsets), _ptr(d_perm),
+                                      _ptr(d_inv), _ptr(d_ws), _stream(s)))
+
+
+def moe_route_scored_backward(ctx, d_logits, T, rule, d_topk_ids, d_dw, d_dlogits, s=None) -> None:
+    _check(ctx, _lib.moe_route_scored_backward(ctx, _ptr(d_logits), T, ctypes.byref(rule) if rule else None,
+                                               _ptr(d_topk_ids), _ptr(d_dw), _ptr(d_dlogits), _stream(s)))
 
 
 def moe_qstar(m, bp, bh, rounding=MOE_Q_NEAREST) -> int:

@@ -233,6 +233,47 @@ int moe_route(moe_ctx* ctx, const float* d_logits, int32_t T, int32_t* d_topk_id
     return e == hipSuccess ? MOE_OK : hip_fail(ctx, e, "moe_route launch");
 }
 
+static const char* bad_rule(const moe_config& c, const moe_route_rule* r) {
+    if (!r) return "null rule";
+    if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) return "unknown score";
+    if (r->n_groups < 1 || r->n_groups > 64 || c.n_experts % r->n_groups) return "n_groups must be in 1..64 and divide E";
+    if (r->keep_groups < 1 || r->keep_groups > r->n_groups) return "keep_groups must be in 1..n_groups";
+    if (int64_t(r->keep_groups) * (c.n_experts / r->n_groups) < c.top_k) return "the kept groups hold fewer than k experts";
+    if (r->group_top != 1 && r->group_top != 2) return "group_top must be 1 or 2";
+    if (r->renormalize != 0 && r->renormalize != 1) return "renormalize must be 0 or 1";
+    if (!std::isfinite(r->scale)) return "scale must be finite";
+    return nullptr;
+}
+
+int moe_route_scored(moe_ctx* ctx, const float* d_logits, const float* d_bias, int32_t T, const moe_route_rule* rule,
+                     int32_t* d_topk_ids, float* d_topk_w, int32_t* d_counts, int32_t* d_offsets, int32_t* d_perm,
+                     int32_t* d_inv, void* d_ws, hipStream_t s) {
+    if (!ctx) return MOE_EINVAL;
+    if (T < 0) return fail(ctx, MOE_EINVAL, "T < 0");
+    if (T > (1 << 24)) return fail(ctx, MOE_ESHAPE, "T above 2^24");
+    if (const char* why = bad_rule(ctx->cfg, rule)) return fail(ctx, MOE_EINVAL, why);
+    if (!d_counts || !d_offsets) return fail(ctx, MOE_EINVAL, "null counts/offsets");
+    if (T > 0 && (!d_logits || !d_topk_ids || !d_topk_w || !d_perm || !d_inv))
+        return fail(ctx, MOE_EINVAL, "null route buffer");
+    if (int64_t(T) * ctx->cfg.top_k > kSmallScored && !d_ws)
+        return fail(ctx, MOE_EINVAL, "workspace required for this T");
+    hipError_t e = launch_route_scored(ctx->cfg, *rule, d_logits, d_bias, T, d_topk_ids, d_topk_w, d_counts, d_offsets,
+                                       d_perm, d_inv, d_ws, s);
+    return e == hipSuccess ? MOE_OK : hip_fail(ctx, e, "moe_route_scored launch");
+}
+
+int moe_route_scored_backward(moe_ctx* ctx, const float* d_logits, int32_t T, const moe_route_rule* rule,
+                              const int32_t* d_topk_ids, const float* d_dw, float* d_dlogits, hipStream_t s) {
+    if (!ctx) return MOE_EINVAL;
+    if (T < 0) return fail(ctx, MOE_EINVAL, "T < 0");
+    if (T > (1 << 24)) return fail(ctx, MOE_ESHAPE, "T above 2^24");
+    if (const char* why = bad_rule(ctx->cfg, rule)) return fail(ctx, MOE_EINVAL, why);
+    if (T == 0) return MOE_OK;
+    if (!d_logits || !d_topk_ids || !d_dw || !d_dlogits) return fail(ctx, MOE_EINVAL, "null buffer");
+    hipError_t e = launch_route_scored_backward(ctx->cfg, *rule, d_logits, T, d_topk_ids, d_dw, d_dlogits, s);
+    return e == hipSuccess ? MOE_OK : hip_fail(ctx, e, "moe_route_scored_backward launch");
+}
+
 int moe_fill(moe_ctx* ctx, const moe_plan* plan, hipStream_t side) {
     if (!ctx || !plan) return MOE_EINVAL;
     if (plan->n_fill > 0 && (!ctx->d_slots || !ctx->h_pool))

@@ -21,6 +21,7 @@ constexpr int kDecodeMaxT = 8;         // T <= 8: batched GEMV path; larger T: g
 constexpr int kSharedTag = 1023;       // list entry tag of the shared expert
 constexpr int kPermChunk = 1024;       // pairs per permutation chunk (one workgroup)
 constexpr int kSmallRouteMaxPairs = 4096;  // fused route+permute in one workgroup up to here
+constexpr int kSmallScored = 512;      // the same for the router by scores
 
 inline int64_t align256(int64_t v) { return (v + 255) & ~int64_t(255); }
 
@@ -137,6 +138,16 @@ bool decode_shape_supported(const moe_config& c);
 hipError_t launch_route(const moe_config& c, const float* logits, int32_t T, int32_t* ids, float* w,
                         int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv, void* ws,
                         hipStream_t s);
+
+// Counting sort of the pairs of ids [T][k] by expert, for any T (workspace as moe_route's).
+hipError_t launch_permute(const moe_config& c, int32_t T, const int32_t* ids, int32_t* counts, int32_t* offsets,
+                          int32_t* perm, int32_t* inv, void* ws, hipStream_t s);
+// Router by scores with a bias and groups, and its gradient (route_scored.hip).
+hipError_t launch_route_scored(const moe_config& c, const moe_route_rule& r, const float* logits, const float* bias,
+                               int32_t T, int32_t* ids, float* w, int32_t* counts, int32_t* offsets, int32_t* perm,
+                               int32_t* inv, void* ws, hipStream_t s);
+hipError_t launch_route_scored_backward(const moe_config& c, const moe_route_rule& r, const float* logits, int32_t T,
+                                        const int32_t* ids, const float* dw, float* dlogits, hipStream_t s);
 
 // Returns hipSuccess, or hipErrorInvalidValue when no kernel variant fits the shape.
 hipError_t launch_ffn_gemv(const moe_config& c, const BlobLayout& lay, const void* x, int32_t T,

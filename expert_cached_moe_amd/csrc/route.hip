@@ -16,45 +16,12 @@
 // counts use integer LDS atomics, ranks use wave ballots.
 #include <hip/hip_runtime.h>
 
-
-#include "device_common.h"
-#include "internal.h"
+#include "route_common.h"
 
 namespace moe {
 namespace {
 
-using dev::kWave;
-
-constexpr int kRouteWaves = 16;              // tokens per workgroup in the large-T route kernel
-constexpr int kBlock = kRouteWaves * kWave;  // 1024 threads
-static_assert(kBlock == kPermChunk, "one pair per thread per permutation chunk");
-
-// Order-preserving key of a logit: larger logit -> larger unsigned key; -0 and +0 share a key.
-__device__ __forceinline__ uint32_t order_key(float v) {
-    const uint32_t u = __float_as_uint(v == 0.0f ? 0.0f : v);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-    return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-}
-
-// Wave-wide maximum of an unsigned key, left in every lane: butterflies inside each row of
-// 16 lanes (DPP quad swaps, rotations by 4 and 8), then row pairs and wave halves exchanged
-// with permlane16_swap / permlane32_swap.
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_umax(uint32_t a) {
-    return max(a, uint32_t(__builtin_amdgcn_mov_dpp(int(a), CTRL, 0xF, 0xF, false)));
-}
-__device__ __forceinline__ uint32_t wave_umax(uint32_t a) {
-    a = dpp_umax<0xB1>(a);   // quad_perm [1,0,3,2]
-    a = dpp_umax<0x4E>(a);   // quad_perm [2,3,0,1]
-    a = dpp_umax<0x124>(a);  // row_ror:4
-    a = dpp_umax<0x128>(a);  // row_ror:8
-    const auto h16 = __builtin_amdgcn_permlane16_swap(a, a, false, false);
-    a = max(h16[0], h16[1]);
-    const auto h32 = __builtin_amdgcn_permlane32_swap(a, a, false, false);
-    return max(h32[0], h32[1]);
-}
+using namespace routing;
 
 // Route one token with one wave.  EPL = experts per lane (ceil(E/64)); lane l holds experts
 // l + 64 i.  k rounds: the wave-wide maximum of the logit keys, then the lowest expert id
@@ -146,88 +113,6 @@ __device__ __forceinline__ void route_dispatch(const float* logits, int T, int E
     }
 }
 
-// Lanes of the wave holding the same expert id (10-bit ids), among lanes with valid = 1.
-__device__ __forceinline__ uint64_t match_expert(int e, bool valid) {
-    uint64_t m = __ballot(valid);
-#pragma unroll
-    for (int b = 0; b < 10; ++b) {
-        const bool bit = valid && ((e >> b) & 1);
-        const uint64_t bb = __ballot(bit);
-        m &= bit ? bb : ~bb;
-    }
-    return valid ? m : 0;
-}
-
-// Exclusive prefix sum of cnt[0..E) by wave 0 into off[0..E]; other waves idle.
-__device__ void wave0_scan(const int32_t* __restrict__ cnt, int E, int32_t* __restrict__ off_lds,
-                           int32_t* __restrict__ off_global, int32_t* __restrict__ counts_global) {
-    if (threadIdx.x >= kWave) return;
-    const int lane = threadIdx.x;
-    constexpr int kPer = kMaxExperts / kWave;  // 8 experts per lane
-    int local[kPer];
-    int sum = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = lane * kPer + i;
-        local[i] = e < E ? cnt[e] : 0;
-        sum += local[i];
-    }
-    int incl = sum;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const int o = __shfl_up(incl, d, kWave);
-        if (lane >= d) incl += o;
-    }
-    int run = incl - sum;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = lane * kPer + i;
-        if (e < E) {
-            off_lds[e] = run;
-            if (off_global) off_global[e] = run;
-            if (counts_global) counts_global[e] = local[i];
-        }
-        run += local[i];
-    }
-    if (lane == kWave - 1) {
-        off_lds[E] = run;
-        if (off_global) off_global[E] = run;
-    }
-}
-
-// Stable scatter of one chunk of up to 1024 pairs: pair p = p0 + tid with expert
-// e = ids[tid].  run[e] is the output position of the chunk's first pair of expert
-// e; it is advanced by the chunk's count.  wc: [16][E] per-wave counts (LDS).
-__device__ void scatter_chunk(const int32_t* __restrict__ ids_src, int p0, int n_valid, int E,
-                              int32_t* __restrict__ run, int32_t (*wc)[kMaxExperts],
-                              int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
-    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
-    const bool valid = tid < n_valid;
-    const int e = valid ? ids_src[tid] : 0;
-    const uint64_t m = match_expert(e, valid);
-    const uint64_t lt = (lane == 0) ? 0ull : (~0ull >> (kWave - lane));
-    const int rank = __popcll(m & lt);
-    const int cw = __popcll(m);
-    for (int i = tid; i < kRouteWaves * E; i += kBlock) wc[i / E][i % E] = 0;
-    __syncthreads();
-    if (valid && rank == 0) wc[wave][e] = cw;
-    __syncthreads();
-    if (valid) {
-        int pos = run[e] + rank;
-        for (int w2 = 0; w2 < wave; ++w2) pos += wc[w2][e];
-        perm[pos] = p0 + tid;
-        inv[p0 + tid] = pos;
-    }
-    __syncthreads();
-    for (int ee = tid; ee < E; ee += kBlock) {
-        int s = 0;
-#pragma unroll
-        for (int w2 = 0; w2 < kRouteWaves; ++w2) s += wc[w2][ee];
-        run[ee] += s;
-    }
-    __syncthreads();
-}
-
 // T*k <= 4096: route, count, scan and scatter in one workgroup.
 __global__ __launch_bounds__(kBlock) void k_route_small(const float* __restrict__ logits, int T, int E, int k,
                                                         int renorm, int32_t* __restrict__ ids, float* __restrict__ w,
@@ -237,64 +122,19 @@ __global__ __launch_bounds__(kBlock) void k_route_small(const float* __restrict_
     __shared__ int32_t s_cnt[kMaxExperts];
     __shared__ int32_t s_run[kMaxExperts + 1];
     __shared__ int32_t s_wc[kRouteWaves][kMaxExperts];
-    const int tid = threadIdx.x;
     route_dispatch(logits, T, E, k, renorm, 0, kRouteWaves, ids, w, s_ids);
-    for (int e = tid; e < E; e += kBlock) s_cnt[e] = 0;
-    __syncthreads();
-    const int n = T * k;
-    for (int p = tid; p < n; p += kBlock) atomicAdd(&s_cnt[s_ids[p]], 1);
-    __syncthreads();
-    wave0_scan(s_cnt, E, s_run, offsets, counts);
-    __syncthreads();
-    for (int p0 = 0; p0 < n; p0 += kBlock) scatter_chunk(s_ids + p0, p0, n - p0, E, s_run, s_wc, perm, inv);
+    group_small(s_ids, T * k, E, s_cnt, s_run, s_wc, counts, offsets, perm, inv);
 }
 
-// T*k <= 64 (decode): route, then the whole grouping by wave 0 with ballots.  For the
-// pair of lane p with expert e: eq = lanes with expert e, lt = lanes with a smaller
-// expert (bit-serial compare of the 10-bit ids, most significant bit first), so
-// its position is |lt| + |eq below p|.
+// T*k <= 64 (decode): route, then the grouping by ballots.
 __global__ __launch_bounds__(1024) void k_route_tiny(const float* __restrict__ logits, int T, int E, int k,
                                                      int renorm, int32_t* __restrict__ ids, float* __restrict__ w,
                                                      int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                                                      int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
     __shared__ int32_t s_ids[kWave];
-    const int tid = threadIdx.x;
     route_dispatch(logits, T, E, k, renorm, 0, blockDim.x / kWave, ids, w, s_ids);
     __syncthreads();
-    const int n = T * k;
-    for (int e = tid; e < E; e += blockDim.x) {
-        int c = 0, lt = 0;
-        for (int p = 0; p < n; ++p) {
-            const int v = s_ids[p];
-            c += v == e;
-            lt += v < e;
-        }
-        counts[e] = c;
-        offsets[e] = lt;
-    }
-    if (tid == 0) offsets[E] = n;
-    if (tid < kWave) {
-        const bool valid = tid < n;
-        const int e = valid ? s_ids[tid] : 0;
-        uint64_t eq = __ballot(valid), lt = 0;
-#pragma unroll
-        for (int b = 9; b >= 0; --b) {
-            const bool bit = (e >> b) & 1;
-            const uint64_t b1 = __ballot(valid && bit);
-            if (bit) {
-                lt |= eq & ~b1;
-                eq &= b1;
-            } else {
-                eq &= ~b1;
-            }
-        }
-        const uint64_t below = tid == 0 ? 0ull : (~0ull >> (kWave - tid));
-        if (valid) {
-            const int pos = __popcll(lt) + __popcll(eq & below);
-            perm[pos] = tid;
-            inv[tid] = pos;
-        }
-    }
+    group_tiny(s_ids, T * k, E, counts, offsets, perm, inv);
 }
 
 // Large T: one wave per token.
@@ -402,12 +242,19 @@ hipError_t launch_route(const moe_config& c, const float* logits, int32_t T, int
                            counts, offsets, perm, inv);
         return hipGetLastError();
     }
+    hipLaunchKernelGGL(k_route, dim3((T + kRouteWaves - 1) / kRouteWaves), dim3(kBlock), 0, s, logits, T, E, k,
+                       c.renormalize, ids, w);
+    return launch_permute(c, T, ids, counts, offsets, perm, inv, ws, s);
+}
+
+hipError_t launch_permute(const moe_config& c, int32_t T, const int32_t* ids, int32_t* counts, int32_t* offsets,
+                          int32_t* perm, int32_t* inv, void* ws, hipStream_t s) {
+    const int E = c.n_experts;
+    const int64_t n = int64_t(T) * c.top_k;
     const WsLayout L = ws_layout(c, T);
     int32_t* hist = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + L.hist);
     int32_t* base = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + L.base);
     const int nchunks = int((n + kPermChunk - 1) / kPermChunk);
-    hipLaunchKernelGGL(k_route, dim3((T + kRouteWaves - 1) / kRouteWaves), dim3(kBlock), 0, s, logits, T, E, k,
-                       c.renormalize, ids, w);
     hipLaunchKernelGGL(k_perm_hist, dim3(nchunks), dim3(kBlock), 0, s, ids, int(n), E, hist);
     hipLaunchKernelGGL(k_perm_scan, dim3(1), dim3(kBlock), 0, s, hist, nchunks, E, base, counts, offsets);
     hipLaunchKernelGGL(k_perm_scatter, dim3(nchunks), dim3(kBlock), 0, s, ids, int(n), E, base, perm, inv);

@@ -62,6 +62,10 @@ extern "C" {
 #define MOE_A_BF16 1
 #define MOE_A_I8 2   /* 8-bit integer codes with one fp32 scale per row */
 
+/* scores of moe_route_scored */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+
 /* integer readings of q* ~= m*B_P/B_H ([B] "The q* Policy") */
 #define MOE_Q_NEAREST 0  /* floor((m*B_P)/B_H + 1/2) in IEEE double, clamped to [0, m] */
 #define MOE_Q_ARGMIN 1   /* smallest q minimising max(q/B_P, (m-q)/(B_H-B_P)) */
@@ -124,6 +128,16 @@ typedef struct moe_resize {
     int32_t* move_dst;  /* [cap] free slot below the new size it moves to */
     int32_t* evicted;   /* [cap] cache keys (layer*E + expert) dropped, in slot order */
 } moe_resize;
+
+/* How moe_route_scored scores and chooses (k and E are the config's). */
+typedef struct moe_route_rule {
+    int32_t score;         /* MOE_SCORE_SOFTMAX | MOE_SCORE_SIGMOID */
+    int32_t n_groups;      /* groups of E / n_groups consecutive experts; 1..64, divides E */
+    int32_t keep_groups;   /* groups whose experts may be chosen, 1..n_groups; they hold >= k experts */
+    int32_t group_top;     /* a group counts as the sum of its 1 or 2 largest values */
+    int32_t renormalize;   /* 1: gates are divided by the sum of the chosen scores */
+    float scale;           /* factor of every gate (finite) */
+} moe_route_rule;
 
 typedef struct moe_ctx moe_ctx;
 
@@ -193,6 +207,37 @@ int moe_router_logits(moe_ctx* ctx, const void* d_x, int32_t T, const float* d_w
 int moe_route(moe_ctx* ctx, const float* d_logits, int32_t T, int32_t* d_topk_ids, float* d_topk_w,
               int32_t* d_counts, int32_t* d_offsets, int32_t* d_perm, int32_t* d_inv, void* d_ws,
               hipStream_t s);
+
+/* Router by scores with a balance bias and groups of experts (async on s), and the same
+ * permutation as moe_route; its outputs feed the same calls.  For each token
+ *   s_e = softmax(logits)_e or 1 / (1 + e^-logit_e),   c_e = s_e + bias_e (s_e without a bias);
+ *   with n_groups > 1 a group's value is the sum of its group_top largest c_e, and the experts of
+ *   the keep_groups best groups stay (lower group first on equal values);
+ *   the k experts with the largest c_e are chosen, lower id first on equal values (without a bias:
+ *   with the largest logits, the same order without rounding);
+ *   gate_e = scale * s_e (the bias has no part in it), divided by the chosen scores' sum with
+ *   rule->renormalize (where that sum is 0 the gates are 0).
+ * s, c and the groups' values are 64-bit numbers, so that the choice does not depend on fp32's
+ * rounding of a score; gates are rounded once to fp32.  cfg.renormalize has no part in it.
+ *   d_logits [T][E] fp32; d_bias [E] fp32 or NULL; the rest as moe_route (d_ws: moe_workspace_bytes,
+ *   needed for T*k > 512).  Infinite negative logits and biases are taken (score 0; chosen last).
+ *   NaNs and positive infinities: that token's ids are distinct and in range, their order and its
+ *   gates are not specified; other tokens are as they would be.
+ * T == 0 is a valid no-op (counts and offsets are written).  Errors: MOE_EINVAL (null, T < 0, a rule
+ * outside its bounds), MOE_ESHAPE (T above 2^24). */
+int moe_route_scored(moe_ctx* ctx, const float* d_logits, const float* d_bias, int32_t T, const moe_route_rule* rule,
+                     int32_t* d_topk_ids, float* d_topk_w, int32_t* d_counts, int32_t* d_offsets, int32_t* d_perm,
+                     int32_t* d_inv, void* d_ws, hipStream_t s);
+/* Its gradient (async on s): from d_dw = dL/dgates [T][k], the same logits and rule, and the ids of
+ * the forward call, d_dlogits = dL/dlogits [T][E] (overwritten).  With a_j = s_j / (sum of the chosen s)
+ * for the chosen j and d_j = scale * dw_j:
+ *   ds_j = (d_j - sum_i d_i a_i) / (sum of the chosen s) renormalised, else d_j; 0 for the others;
+ *   sigmoid: dlogit_j = ds_j s_j (1 - s_j), 0 for the others;
+ *   softmax: dlogit_e = s_e (ds_e - sum_j ds_j s_j) (renormalised: 0 for the others).
+ * The choice has no gradient, and none goes to the bias (balancing sets it).  Formed in 64 bits and
+ * rounded once.  An id outside 0..E-1 counts as none chosen.  T == 0 is a no-op.  Errors as above. */
+int moe_route_scored_backward(moe_ctx* ctx, const float* d_logits, int32_t T, const moe_route_rule* rule,
+                              const int32_t* d_topk_ids, const float* d_dw, float* d_dlogits, hipStream_t s);
 
 /* ---------------------------------------------------------------- cache planner (host) */
 /* q* for m misses ([B] "The q* Policy").  Pure; negative m gives 0. */
