@@ -42,6 +42,8 @@ EXPORTS = [
     "moe_i8_workspace_bytes", "moe_i8_quantize", "moe_i8_matmul", "moe_dense_workspace_bytes",
     "moe_dense_save_bytes", "moe_dense_ffn", "moe_dense_ffn_backward", "moe_i8_blob_bytes", "moe_i8_pack",
     "moe_i8_ffn", "moe_route_scored", "moe_route_scored_backward",
+    "moe_i4_quantize", "moe_i4_workspace_bytes", "moe_i4_matmul", "moe_i4_blob_bytes", "moe_i4_pack",
+    "moe_i4_expert_workspace_bytes", "moe_i4_expert_ffn",
 ]
 
 
@@ -125,6 +127,16 @@ _sig = {
     "moe_i8_blob_bytes": (ctypes.c_int64, [_P(moe_config)]),
     "moe_i8_pack": (ctypes.c_int, [vp, vp, vp, vp]),
     "moe_i8_ffn": (ctypes.c_int, [vp, vp, ctypes.c_int32, vp, vp, vp, vp]),
+    "moe_i4_quantize": (ctypes.c_int, [vp, vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                       ctypes.c_int32, ctypes.c_int32, vp, vp, vp, vp]),
+    "moe_i4_workspace_bytes": (ctypes.c_int64, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
+    "moe_i4_matmul": (ctypes.c_int, [vp, vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, vp, vp, vp, ctypes.c_int32,
+                                     ctypes.c_int32, ctypes.c_int32, vp, ctypes.c_int32, ctypes.c_int64, vp, vp]),
+    "moe_i4_blob_bytes": (ctypes.c_int64, [_P(moe_config), ctypes.c_int32]),
+    "moe_i4_pack": (ctypes.c_int, [vp, vp, ctypes.c_int32, ctypes.c_int32, vp, vp]),
+    "moe_i4_expert_workspace_bytes": (ctypes.c_int64, [_P(moe_config), ctypes.c_int32]),
+    "moe_i4_expert_ffn": (ctypes.c_int, [vp, vp, ctypes.c_int32, vp, vp, vp, vp, vp, ctypes.c_int32, vp, ctypes.c_int32,
+                                         ctypes.c_int32, vp, vp, vp]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -443,6 +455,41 @@ def moe_i8_pack(ctx, d_blob, d_blob8, s=None) -> None:
 
 def moe_i8_ffn(ctx, d_x, T, d_blob8, d_y, d_ws, s=None) -> None:
     _check(ctx, _lib.moe_i8_ffn(ctx, _ptr(d_x), T, _ptr(d_blob8), _ptr(d_y), _ptr(d_ws), _stream(s)))
+
+
+def moe_i4_quantize(ctx, d_x, x_type, ld_x, rows, cols, group, zero_points, d_q, d_words, d_exps, s=None) -> None:
+    _check(ctx, _lib.moe_i4_quantize(ctx, _ptr(d_x), x_type, ld_x, rows, cols, group, zero_points, _ptr(d_q),
+                                     _ptr(d_words), _ptr(d_exps), _stream(s)))
+
+
+def moe_i4_workspace_bytes(max_T: int, N: int, K: int) -> int:
+    return _size(_lib.moe_i4_workspace_bytes(max_T, N, K), "moe_i4_workspace_bytes")
+
+
+def moe_i4_matmul(ctx, d_x, x_type, ld_x, T, d_w, d_words, d_exps, N, K, group, d_y, y_type, ld_y, d_ws, s=None) -> None:
+    _check(ctx, _lib.moe_i4_matmul(ctx, _ptr(d_x), x_type, ld_x, T, _ptr(d_w), _ptr(d_words), _ptr(d_exps), N, K, group,
+                                   _ptr(d_y), y_type, ld_y, _ptr(d_ws), _stream(s)))
+
+
+def moe_i4_blob_bytes(cfg: moe_config, group: int) -> int:
+    return _size(_lib.moe_i4_blob_bytes(ctypes.byref(cfg), group), "moe_i4_blob_bytes")
+
+
+def moe_i4_pack(ctx, d_blob, group, zero_points, d_blob4, s=None) -> None:
+    _check(ctx, _lib.moe_i4_pack(ctx, _ptr(d_blob), group, zero_points, _ptr(d_blob4), _stream(s)))
+
+
+def moe_i4_expert_workspace_bytes(cfg: moe_config, max_T: int) -> int:
+    return _size(_lib.moe_i4_expert_workspace_bytes(ctypes.byref(cfg), max_T), "moe_i4_expert_workspace_bytes")
+
+
+def moe_i4_expert_ffn(ctx, d_x, T, d_offsets, d_perm, d_slot_base, h_experts, h_slots, n, d_shared, with_shared, group,
+                      d_o, d_ws, s=None) -> None:
+    he = np.ascontiguousarray(h_experts, dtype=np.int32) if h_experts is not None else None
+    hs = np.ascontiguousarray(h_slots, dtype=np.int32) if h_slots is not None else None
+    _check(ctx, _lib.moe_i4_expert_ffn(ctx, _ptr(d_x), T, _ptr(d_offsets), _ptr(d_perm), _ptr(d_slot_base), _ptr(he),
+                                       _ptr(hs), n, _ptr(d_shared), with_shared, group, _ptr(d_o), _ptr(d_ws),
+                                       _stream(s)))
 
 
 def moe_prefill_stream(ctx, d_layer_bufs, n_buffers, d_logits, d_x, T, d_shared, d_topk_ids, d_topk_w, d_counts,

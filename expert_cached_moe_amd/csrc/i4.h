@@ -1,0 +1,72 @@
+// Products with 4-bit weights (moe_i4_*): the argument block of their kernels and the launchers.
+//
+// A row of K weights: weight k = 2^(exp - 127) * s * (code - z), with the codes two a byte (element
+// 2 i in the low half of byte i), and for each group of 32, 64 or 128 along K one word: the low
+// byte an e4m3 number s, the high byte the zero point z.  s has four significant bits and code - z
+// four, so every weight is exact in bf16: a product on the matrix cores is one with these weights.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "internal.h"
+
+namespace moe {
+namespace i4 {
+
+constexpr int kMaxK = 1 << 20;        // offsets inside a tile of rows stay below 2 GiB
+constexpr int kMaxCount = 1 << 23;    // rows: the threads of a launch fit 32 bits
+
+// Rows of 4-bit weights: those of entry e begin `offset(e)` bytes on in all three arrays.
+struct Rows {
+    const uint8_t* codes;    // [N][K / 2]
+    const uint16_t* words;   // [N][groups]
+    const uint8_t* exps;     // [N]
+    int32_t groups;          // of a row
+    int32_t shift;           // log2 of a group's length
+};
+
+// What a product computes and where its rows come from and go to.
+enum {
+    kOut16 = 0,   // dense: row r of x to row r of out, bf16
+    kOut32 = 1,   // the same in fp32
+    kGateUp = 2,  // an expert's rows: x of the pair's token to h of its place in expert order
+    kDown = 3,    // h of a place to the pair's own row
+};
+
+struct Product {
+    const uint16_t* x;       // bf16 rows, 16-byte aligned, ldx elements apart
+    int64_t ldx;
+    int64_t plane;           // fp32 activations: three bf16 parts, `plane` elements apart
+    int32_t planes;          // 1 or 3
+    int32_t N, K;
+    Rows w;
+    void* out;
+    int64_t ldo;
+    int32_t wide;            // dense: every even column of out lies on 4 bytes
+    int64_t T;
+    // experts: entry i of the list, its places offsets[e] .. offsets[e + 1] - 1 in expert order
+    const int32_t *offsets, *perm;
+    int32_t top_k;
+    int64_t stride, shared;  // bytes from slot to slot; of the shared blob from slot 0
+};
+
+// One record of the tile map: entry, its tile of rows, its first place, its rows.
+struct MapTile {
+    int32_t entry, tile, base, count;
+};
+
+hipError_t launch_i4_quantize(const void* x, int x_type, int64_t ld_x, int64_t rows, int32_t cols, int group, int zero,
+                              uint8_t* q, uint16_t* words, uint8_t* exps, hipStream_t s);
+// Rows of numbers to bf16 rows of K back to back (fp32: three parts, T K elements apart).
+hipError_t launch_i4_activations(const void* x, int x_type, int64_t ld_x, int64_t T, int32_t K, uint16_t* out, hipStream_t s);
+// Records of all row tiles of the list's entries, behind a count: int32 count, 3 of padding, records.
+hipError_t launch_i4_map(const ExpertList& list, const int32_t* offsets, int64_t T, int top_k, int rows, void* map,
+                         hipStream_t s);
+int64_t map_tiles(int n, int64_t rows, int tile);            // the most records that there can be
+hipError_t launch_i4_tiles(int kind, const Product& p, const ExpertList* list, const void* map, int64_t max_tiles,
+                           hipStream_t s);
+
+constexpr int kTileRows = 128;
+
+}  // namespace i4
+}  // namespace moe

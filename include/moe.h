@@ -469,6 +469,75 @@ int moe_i8_pack(moe_ctx* ctx, const void* d_blob, void* d_blob8, hipStream_t s);
  * for T above 2^24. */
 int moe_i8_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob8, void* d_y, void* d_ws, hipStream_t s);
 
+/* ---------------------------------------------------------------- 4-bit weights */
+/* Weights held in 4-bit integers, for dense products and for the experts.  A row of K weights is
+ *   weight[k] = 2^(exp - 127) * s * (code[k] - z)
+ * with codes 0..15 (element 2i in the low half of byte i), one exponent byte per row (255: NaN), and
+ * for each group of 32, 64 or 128 along K (the last one may be shorter) one 16-bit word: the low byte
+ * is s, an e4m3 number (OCP FP8, NaN 0x7F), the high byte the zero point z, 0..15.  The scale s has
+ * four significant bits and code - z four, so each weight is exact in bf16, and the products below are
+ * products with these weights: nothing is rounded before the sums.  Activations stay as they are.
+ *
+ * Quantise `rows` rows of `cols` numbers (async on s).  With lo, hi a group's smallest and largest number
+ * and 0:
+ *   zero_points 0:  t = max(hi, -lo) / 7, s to nearest even, z = 8;
+ *   zero_points 1:  t = (hi - lo) / 15, s upwards, z = -lo / d rounded, d = 2^(exp - 127) s;
+ *   2^(exp - 127) is the least power of two with t <= 448 * 2^(exp - 127) for every group of the row,
+ *   s the e4m3 number of t / 2^(exp - 127) (at most 448), code = x / d rounded, plus z, held to 0..15.
+ * Quotients are 64-bit numbers, rounded to the nearest integer, ties to the even one.  A group with s = 0 has
+ * z = 8 and codes 8 (zeros); a row whose power of two would be below 2^-100 is zeros with exp 0; a row
+ * that holds a NaN or a magnitude of 2^120 or more has exp 255, so every product with it is NaN.
+ *   d_x: MOE_A_F32 or MOE_A_BF16, rows ld_x >= cols elements apart, any alignment of the element;
+ *   d_q [rows][cols / 2] 16-byte aligned, d_words [rows][ceil(cols / group)], d_exps [rows];
+ *   cols a multiple of 32 up to 2^20, rows up to 2^23.  rows == 0 is a no-op.
+ * Errors: MOE_EINVAL (null, type, group, ld_x < cols, alignment), MOE_ESHAPE (cols, rows). */
+int moe_i4_quantize(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, int32_t rows, int32_t cols, int32_t group,
+                    int32_t zero_points, uint8_t* d_q, uint16_t* d_words, uint8_t* d_exps, hipStream_t s);
+/* Scratch bytes of moe_i4_matmul for up to max_T tokens, or a negative status. */
+int64_t moe_i4_workspace_bytes(int32_t max_T, int32_t N, int32_t K);
+/* y[t][n] = sum_k x[t][k] * weight[n][k] (async on s), products exact, sums in fp32, the result
+ * rounded once where y is bf16.
+ *   d_x: MOE_A_F32 or MOE_A_BF16, rows ld_x >= K elements apart, any alignment of the element (bf16 rows
+ *     that start on 16 bytes each are read as they are, others are laid out in the workspace first; fp32
+ *     numbers enter the matrix cores as three bf16 parts that add up to them);
+ *   d_w [N][K / 2] (16-byte aligned), d_words [N][ceil(K / group)], d_exps [N] as moe_i4_quantize makes
+ *     them; any codes and words are taken (a zero point above 15 rounds the weights to bf16);
+ *   d_y [T][N], rows ld_y >= N elements apart, MOE_A_F32 or MOE_A_BF16; bytes between the rows are not
+ *     written;
+ *   d_ws: moe_i4_workspace_bytes(max_T >= T, N, K), 256-byte aligned.
+ * K is a multiple of 32 up to 2^20, N >= 1, N and T up to 2^23, T N up to 2^36.  A token that holds an
+ * infinity or a NaN has results that are infinite or NaN; the others are as they would be.  No output may
+ * overlap an input; the stream belongs to the current device; calls that share a workspace must not
+ * overlap in time, replays of captured graphs included.  T == 0 is a no-op.  Errors: MOE_EINVAL,
+ * MOE_ESHAPE. */
+int moe_i4_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, int32_t T, const uint8_t* d_w,
+                  const uint16_t* d_words, const uint8_t* d_exps, int32_t N, int32_t K, int32_t group, void* d_y,
+                  int32_t y_type, int64_t ld_y, void* d_ws, hipStream_t s);
+/* Experts from 4-bit blobs.  Contexts with bf16 weights; H and I up to 2^20.
+ * Bytes of a 4-bit blob (a multiple of 256): codes, words and exponents of the 2I gate and up rows (interleaved as in
+ * moe_pack_expert's blob), then those of the H down rows, each part 256-byte aligned. */
+int64_t moe_i4_blob_bytes(const moe_config* cfg, int32_t group);
+/* Quantise a device blob's rows (async on s): d_blob (moe_expert_bytes) to d_blob4
+ * (moe_i4_blob_bytes), both 256-byte aligned.  Errors: MOE_EINVAL, MOE_ESHAPE, MOE_EUNSUPPORTED (weights other than
+ * bf16). */
+int moe_i4_pack(moe_ctx* ctx, const void* d_blob, int32_t group, int32_t zero_points, void* d_blob4, hipStream_t s);
+/* Scratch bytes of moe_i4_expert_ffn for up to max_T tokens, or a negative status. */
+int64_t moe_i4_expert_workspace_bytes(const moe_config* cfg, int32_t max_T);
+/* moe_expert_ffn on 4-bit blobs, any T (async on s): o[p] = Wd_e (silu(Wg_e x_t) * (Wu_e x_t)) for every pair
+ * p = t*k + j whose expert is listed, from the blob at d_slot_base + h_slots[i]*moe_i4_blob_bytes, and
+ * with with_shared = 1 o[T*k + t] from the blob d_shared.  Sums in fp32; h is rounded once to bf16 before the
+ * down product, results once to bf16.  Rows of experts that are not listed are not written.
+ *   d_x [T][H] bf16; d_offsets [E+1], d_perm [T*k] from moe_route or moe_route_scored (read on the device: the
+ *   call needs no host copy of the ids; listed experts without tokens cost next to nothing; may be NULL with n = 0);
+ *   h_experts / h_slots: host arrays of n distinct ids and slots, copied by the call;
+ *   d_o [moe_pair_rows][H] bf16, for moe_merge_partial; d_ws: moe_i4_expert_workspace_bytes(max_T >= T).
+ * x and o 16-byte, blobs and workspace 256-byte aligned; overlap, stream and workspace as moe_i4_matmul.
+ * T == 0, or nothing listed, is a no-op.  Errors: MOE_EINVAL, MOE_ESHAPE (T above 2^23, H, I),
+ * MOE_EUNSUPPORTED. */
+int moe_i4_expert_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const int32_t* d_offsets, const int32_t* d_perm,
+                      const void* d_slot_base, const int32_t* h_experts, const int32_t* h_slots, int32_t n,
+                      const void* d_shared, int32_t with_shared, int32_t group, void* d_o, void* d_ws, hipStream_t s);
+
 /* ---------------------------------------------------------------- layer streaming (prefill) */
 /* One T-token prefill chunk through cfg.n_layers MoE layers whose expert pools
  * stream from the bound host pool (n_layers*E blobs, layer-major, pinned) into
