@@ -1,5 +1,6 @@
 // Entry points of the products with 4-bit weights: quantisation, the dense product, and the experts
-// of a layer.  Contracts in include/moe.h; the kernels are in i4_quant.hip and i4_tile.hip.
+// of a layer.  Contracts in include/moe.h; the kernels are in i4_quant.hip, i4_few.hip and
+// i4_tile.hip.
 #include <hip/hip_runtime.h>
 
 #include "i4.h"
@@ -126,7 +127,8 @@ int moe_i4_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, i
     p.out = d_y;
     p.ldo = ld_y;
     p.wide = aligned(d_y, 4) && ld_y % 2 == 0;
-    hipError_t e = launch_i4_tiles(y_type == MOE_A_F32 ? kOut32 : kOut16, p, nullptr, nullptr, 0, s);
+    const int kind = y_type == MOE_A_F32 ? kOut32 : kOut16;
+    hipError_t e = T <= kFewTokens ? launch_i4_few(kind, p, nullptr, s) : launch_i4_tiles(kind, p, nullptr, nullptr, 0, s);
     return e == hipSuccess ? MOE_OK : hip_fail(ctx, e, "moe_i4_matmul launch");
 }
 
@@ -215,7 +217,8 @@ int moe_i4_expert_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const int32_t* d
     p.stride = b.bytes;
     p.shared = with_shared ? static_cast<const uint8_t*>(d_shared) - base : 0;
     const int64_t rows = int64_t(T) * c.top_k + (with_shared ? T : 0), tiles = map_tiles(list.n, rows, kTileRows);
-    hipError_t e = launch_i4_map(list, d_offsets, T, c.top_k, kTileRows, ws, s);
+    const bool few = T <= kFewTokens;
+    hipError_t e = few ? hipSuccess : launch_i4_map(list, d_offsets, T, c.top_k, kTileRows, ws, s);
     if (e != hipSuccess) return hip_fail(ctx, e, "moe_i4_expert_ffn launch");
     p.x = static_cast<const uint16_t*>(d_x);
     p.ldx = c.hidden;
@@ -224,7 +227,7 @@ int moe_i4_expert_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const int32_t* d
     p.w = Rows{base + b.gu, reinterpret_cast<const uint16_t*>(base + b.gu_word), base + b.gu_exp, b.gu_groups, shift_of(group)};
     p.out = ws + w.h;
     p.ldo = c.inter;
-    e = launch_i4_tiles(kGateUp, p, &list, ws, tiles, s);
+    e = few ? launch_i4_few(kGateUp, p, &list, s) : launch_i4_tiles(kGateUp, p, &list, ws, tiles, s);
     if (e != hipSuccess) return hip_fail(ctx, e, "moe_i4_expert_ffn launch");
     p.x = reinterpret_cast<const uint16_t*>(ws + w.h);
     p.ldx = c.inter;
@@ -233,7 +236,7 @@ int moe_i4_expert_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const int32_t* d
     p.w = Rows{base + b.d, reinterpret_cast<const uint16_t*>(base + b.d_word), base + b.d_exp, b.d_groups, shift_of(group)};
     p.out = d_o;
     p.ldo = c.hidden;
-    e = launch_i4_tiles(kDown, p, &list, ws, tiles, s);
+    e = few ? launch_i4_few(kDown, p, &list, s) : launch_i4_tiles(kDown, p, &list, ws, tiles, s);
     return e == hipSuccess ? MOE_OK : hip_fail(ctx, e, "moe_i4_expert_ffn launch");
 }
 

@@ -66,7 +66,11 @@ int64_t map_tiles(int n, int64_t rows, int tile);            // the most records
 hipError_t launch_i4_tiles(int kind, const Product& p, const ExpertList* list, const void* map, int64_t max_tiles,
                            hipStream_t s);
 
+// Up to 16 rows of x, dense or of each entry of the list.
+hipError_t launch_i4_few(int kind, const Product& p, const ExpertList* list, hipStream_t s);
+
 constexpr int kTileRows = 128;
+constexpr int kFewTokens = 16;
 
 }  // namespace i4
 }  // namespace moe

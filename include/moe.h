@@ -501,7 +501,8 @@ int64_t moe_i4_workspace_bytes(int32_t max_T, int32_t N, int32_t K);
  *     that start on 16 bytes each are read as they are, others are laid out in the workspace first; fp32
  *     numbers enter the matrix cores as three bf16 parts that add up to them);
  *   d_w [N][K / 2] (16-byte aligned), d_words [N][ceil(K / group)], d_exps [N] as moe_i4_quantize makes
- *     them; any codes and words are taken (a zero point above 15 rounds the weights to bf16);
+ *     them; any codes and words are taken (a zero point above 15 rounds the weights to bf16, scales
+ *     2^(exp - 127) s from 2^119 on overflow);
  *   d_y [T][N], rows ld_y >= N elements apart, MOE_A_F32 or MOE_A_BF16; bytes between the rows are not
  *     written;
  *   d_ws: moe_i4_workspace_bytes(max_T >= T, N, K), 256-byte aligned.
