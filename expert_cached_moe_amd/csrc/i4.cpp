@@ -1,8 +1,9 @@
 // Entry points of the products with 4-bit weights: quantisation, the dense product, and the experts
-// of a layer.  Contracts in include/moe.h; the kernels are in i4_quant.hip, i4_few.hip and
-// i4_tile.hip.
+// of a layer.  Contracts in include/moe.h; the kernels are in i4_quant.hip, i4_few.hip,
+// i4_mid.hip and i4_turns.hip.
 #include <hip/hip_runtime.h>
 
+#include "dense.h"
 #include "i4.h"
 
 namespace moe {
@@ -33,7 +34,8 @@ Blob4 blob4_layout(const moe_config& c, int32_t group) {
     return b;
 }
 
-// Workspace of moe_i4_expert_ffn: the tile map, and h in expert order.
+// Workspace of moe_i4_expert_ffn: the tile maps of the two products, and h in expert order.
+int64_t map_bytes(int n, int64_t rows) { return align256(16 * (1 + map_tiles(n, rows, 32))); }
 struct ExpertWork {
     int64_t h = 0, bytes = 0;
 };
@@ -41,9 +43,15 @@ ExpertWork expert_work(const moe_config& c, int64_t T) {
     if (T < 1) T = 1;
     const int64_t rows = T * c.top_k + (c.n_shared ? T : 0);
     ExpertWork w;
-    w.h = align256(16 * (1 + map_tiles(c.n_experts + 1, rows, kTileRows)));
+    w.h = align256(2 * map_bytes(c.n_experts + 1, rows));
     w.bytes = align256(w.h + rows * c.inter * 2);
     return w;
+}
+
+hipError_t launch_dense(int what, const Product& p, hipStream_t s) {
+    if (p.T <= kFewTokens) return launch_i4_few(what, p, nullptr, s);
+    const int kind = plan_dense(p.T, p.N, p.K, p.planes, dense::compute_units());
+    return kind == kTurns ? launch_i4_turns(what, p, nullptr, nullptr, 0, s) : launch_i4_mid(what, kind, p, nullptr, nullptr, 0, s);
 }
 
 int check_config(const moe_config& c, const char** why) {
@@ -113,7 +121,8 @@ int moe_i4_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, i
     p.x = static_cast<const uint16_t*>(d_x);
     p.ldx = ld_x;
     p.T = T;
-    if (x_type == MOE_A_F32 || !aligned(d_x, 16) || ld_x % 8) {
+    // (rows that are read as they are start on 16 bytes each, and 128 of them lie within 4 GiB)
+    if (x_type == MOE_A_F32 || !aligned(d_x, 16) || ld_x % 8 || ld_x >= (int64_t(1) << 24)) {
         hipError_t e = launch_i4_activations(d_x, x_type, ld_x, T, K, static_cast<uint16_t*>(d_ws), s);
         if (e != hipSuccess) return hip_fail(ctx, e, "moe_i4_matmul launch");
         p.x = static_cast<const uint16_t*>(d_ws);
@@ -128,7 +137,7 @@ int moe_i4_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, i
     p.ldo = ld_y;
     p.wide = aligned(d_y, 4) && ld_y % 2 == 0;
     const int kind = y_type == MOE_A_F32 ? kOut32 : kOut16;
-    hipError_t e = T <= kFewTokens ? launch_i4_few(kind, p, nullptr, s) : launch_i4_tiles(kind, p, nullptr, nullptr, 0, s);
+    hipError_t e = launch_dense(kind, p, s);
     return e == hipSuccess ? MOE_OK : hip_fail(ctx, e, "moe_i4_matmul launch");
 }
 
@@ -216,10 +225,24 @@ int moe_i4_expert_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const int32_t* d
     p.top_k = c.top_k;
     p.stride = b.bytes;
     p.shared = with_shared ? static_cast<const uint8_t*>(d_shared) - base : 0;
-    const int64_t rows = int64_t(T) * c.top_k + (with_shared ? T : 0), tiles = map_tiles(list.n, rows, kTileRows);
-    const bool few = T <= kFewTokens;
-    hipError_t e = few ? hipSuccess : launch_i4_map(list, d_offsets, T, c.top_k, kTileRows, ws, s);
-    if (e != hipSuccess) return hip_fail(ctx, e, "moe_i4_expert_ffn launch");
+    const int64_t pairs = int64_t(T) * c.top_k, rows = (n > 0 ? pairs : 0) + (with_shared ? T : 0);
+    const int n_cu = dense::compute_units();
+    const bool few = few_experts(n, T, pairs, with_shared);
+    int built = 0;                                            // rows of the tiles that the map in the workspace lists
+    auto product = [&](int what) {
+        if (few) return launch_i4_few(what, p, &list, s);
+        int kind = plan_experts(list.n, rows, p.N, p.K, n_cu);
+        // (offsets of gathered rows have 32 bits on the smaller tiles)
+        if (what == kGateUp && int64_t(T) * p.ldx * 2 > int64_t(0xFFFF0000)) kind = kTurns;
+        uint8_t* map = ws + (what == kDown && built != kKind[kind].rows ? map_bytes(c.n_experts + 1, pairs + (c.n_shared ? T : 0)) : 0);
+        if (built != kKind[kind].rows) {
+            const hipError_t e = launch_i4_map(list, d_offsets, T, c.top_k, kKind[kind].rows, map, s);
+            if (e != hipSuccess) return e;
+            built = kKind[kind].rows;
+        }
+        const int64_t tiles = map_tiles(list.n, rows, kKind[kind].rows);
+        return kind == kTurns ? launch_i4_turns(what, p, &list, map, tiles, s) : launch_i4_mid(what, kind, p, &list, map, tiles, s);
+    };
     p.x = static_cast<const uint16_t*>(d_x);
     p.ldx = c.hidden;
     p.N = 2 * c.inter;
@@ -227,7 +250,7 @@ int moe_i4_expert_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const int32_t* d
     p.w = Rows{base + b.gu, reinterpret_cast<const uint16_t*>(base + b.gu_word), base + b.gu_exp, b.gu_groups, shift_of(group)};
     p.out = ws + w.h;
     p.ldo = c.inter;
-    e = few ? launch_i4_few(kGateUp, p, &list, s) : launch_i4_tiles(kGateUp, p, &list, ws, tiles, s);
+    hipError_t e = product(kGateUp);
     if (e != hipSuccess) return hip_fail(ctx, e, "moe_i4_expert_ffn launch");
     p.x = reinterpret_cast<const uint16_t*>(ws + w.h);
     p.ldx = c.inter;
@@ -236,7 +259,7 @@ int moe_i4_expert_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const int32_t* d
     p.w = Rows{base + b.d, reinterpret_cast<const uint16_t*>(base + b.d_word), base + b.d_exp, b.d_groups, shift_of(group)};
     p.out = d_o;
     p.ldo = c.hidden;
-    e = few ? launch_i4_few(kDown, p, &list, s) : launch_i4_tiles(kDown, p, &list, ws, tiles, s);
+    e = product(kDown);
     return e == hipSuccess ? MOE_OK : hip_fail(ctx, e, "moe_i4_expert_ffn launch");
 }
 

@@ -8,6 +8,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include "i4_plan.h"
 #include "internal.h"
 
 namespace moe {
@@ -62,15 +63,14 @@ hipError_t launch_i4_activations(const void* x, int x_type, int64_t ld_x, int64_
 // Records of all row tiles of the list's entries, behind a count: int32 count, 3 of padding, records.
 hipError_t launch_i4_map(const ExpertList& list, const int32_t* offsets, int64_t T, int top_k, int rows, void* map,
                          hipStream_t s);
-int64_t map_tiles(int n, int64_t rows, int tile);            // the most records that there can be
-hipError_t launch_i4_tiles(int kind, const Product& p, const ExpertList* list, const void* map, int64_t max_tiles,
+inline int64_t map_tiles(int n, int64_t rows, int tile) { return rows / tile + n; }   // the most records that there can be
+// What the product computes (kOut16 ...) on tiles of a kind of i4_plan.h; experts: with the map for its rows.
+hipError_t launch_i4_mid(int what, int kind, const Product& p, const ExpertList* list, const void* map, int64_t max_tiles,
+                         hipStream_t s);
+hipError_t launch_i4_turns(int what, const Product& p, const ExpertList* list, const void* map, int64_t max_tiles,
                            hipStream_t s);
-
-// Up to 16 rows of x, dense or of each entry of the list.
-hipError_t launch_i4_few(int kind, const Product& p, const ExpertList* list, hipStream_t s);
-
-constexpr int kTileRows = 128;
-constexpr int kFewTokens = 16;
+// Up to 8 rows of x, dense; experts: entries of few rows.
+hipError_t launch_i4_few(int what, const Product& p, const ExpertList* list, hipStream_t s);
 
 }  // namespace i4
 }  // namespace moe

@@ -48,10 +48,10 @@ __device__ __forceinline__ Rows rows_at(const Rows& w, int64_t bytes) {
     return r;
 }
 
-// Row of x and row of out of place `at` = base + r of an entry (shared: base = T top_k, perm has no part).
+// Row of x and row of out of place base + r of an entry (the shared expert's places begin at T top_k).
 template <int KIND>
 __device__ __forceinline__ int64_t row_in(const Product& p, bool shared, int base, int r) {
-    if (KIND == kGateUp) return shared ? r : p.perm[base + r] / p.top_k;
+    if (KIND == kGateUp) return shared ? base + r - int64_t(p.T) * p.top_k : p.perm[base + r] / p.top_k;
     if (KIND == kDown) return int64_t(base) + r;
     return r;
 }

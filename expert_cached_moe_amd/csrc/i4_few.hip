@@ -7,16 +7,16 @@
 // group.  Codes become bf16 numbers 0..15 by three masks and shifts and four conversions per eight (bytes
 // 0..15 are e4m3 numbers 2^-9 times themselves), eight instructions of the matrix unit sum x * code over
 // the piece for four tokens, started with -z * (sum of x), which gives sum x * (code - z); four
-// multiply-adds add that, times s and the row's power of two, to the sums.  So a code takes 1.2 operations of a lane for up to 4 tokens
-// and 1.9 for 16, of the 3.3 that there is time for; scaling every weight would take 2.4.
+// multiply-adds add that, times s, to the sums.  So a code takes 1.2 operations of a lane for up to 4 tokens
+// and 1.4 for 8, of the 3.3 that there is time for; scaling every weight would take 2.4.
 //
 // The waves of a workgroup split K (by chunks of 512) and, where K is short, rows too; sums meet once a
 // unit of rows, across the blocks in registers, across the waves in LDS, in a fixed order.  Every tile's
 // registers are loaded again as soon as it is used, with the next chunk or the next unit of rows, so
 // the stream does not stop between units.
 //
-// Experts: each workgroup lists the entries that have rows, from the offsets, and walks their units.  An
-// entry's rows are 4, 8 or 16 at most; which of these decides the code that its units run.
+// Experts: each workgroup lists the entries that have rows, from the offsets, in blocks of 8 rows at most, and walks
+// their units; whether a block has more than 4 rows decides the code that its units run.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -34,6 +34,8 @@ using dev::kWave;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 
 constexpr int kChunk = 512, kMaxWaves = 8, kStream = 2;       // cache policy of a non-temporal load
+// The row's power of two comes last; until then sums are held 2^-32 times as large, in range whatever x is.
+constexpr float kDown32 = 2.3283064365386963e-10f;
 constexpr uint32_t kOutside = 0xFFFFFFF0u, kRange = 0x80000000u;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p) {
@@ -65,11 +67,14 @@ __device__ __forceinline__ s16x4 codes4(uint32_t even, uint32_t odd) {
 template <int MAXMT, int P>
 constexpr int kWavesPerSimd = MAXMT * P == 1 ? 4 : MAXMT * P <= 3 ? 3 : 2;
 
+__device__ __forceinline__ float scaled(float sum, uint32_t e) {
+    return e == 255u ? __uint_as_float(0x7FC00000u) : __builtin_ldexpf(sum, int(e) - 127 + 32);
+}
+
 struct Few {
     int kw, rw;              // waves along K, and along rows
     int strips;              // of an entry: runs of 4 R rows (gated: 2 R gate rows and their up rows)
     int entries;             // dense: runs of 4 MT tokens; experts: entries of the list
-    int limit;               // experts with more rows than this are left out
 };
 
 // What a unit of rows is: an entry's rows of x, and its weights.
@@ -83,7 +88,7 @@ template <int KIND, int MAXMT, int R, int P>
 __global__ void __launch_bounds__(kMaxWaves* kWave) __attribute__((amdgpu_waves_per_eu(kWavesPerSimd<MAXMT, P>)))
 k_i4_few(const Product p, const ExpertList list, const Few f) {
     constexpr bool GATE = KIND == kGateUp, EXPERTS = KIND == kGateUp || KIND == kDown;
-    __shared__ int4 s_entry[EXPERTS ? kMaxExperts + 1 : 1];
+    __shared__ int4 s_entry[EXPERTS ? kFewBlocks : 1];
     __shared__ int s_active;
     extern __shared__ __attribute__((aligned(16))) float red[];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
@@ -106,14 +111,22 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
                 base = e == kSharedTag ? int(p.T) * p.top_k : p.offsets[e];
                 count = e == kSharedTag ? int(p.T) : p.offsets[e + 1] - base;
             }
-            const bool in = count > 0 && count <= f.limit;
-            const uint64_t m = __ballot(in);
+            // an entry of more rows is several of 4 MAXMT
+            const int blocks = (count + 4 * MAXMT - 1) / (4 * MAXMT);
+            int incl = blocks;
+#pragma unroll
+            for (int d = 1; d < kWave; d <<= 1) {
+                const int o = __shfl_up(incl, d, kWave);
+                if (lane >= d) incl += o;
+            }
             // (waves in order: the list is the same in every workgroup)
             for (int w = 0; w < int(blockDim.x) / kWave; ++w) {
                 if (w == wave) {
-                    const int first = s_active, at = first + __popcll(m & ((uint64_t(1) << lane) - 1));
-                    if (in) s_entry[at] = make_int4(ent, base, count, 0);
-                    if (lane == 0) s_active = first + __popcll(m);
+                    const int first = s_active + incl - blocks;
+                    for (int q = 0; q < blocks; ++q)
+                        if (first + q < kFewBlocks)           // (the host has seen to it)
+                            s_entry[first + q] = make_int4(ent, base + q * 4 * MAXMT, min(count - q * 4 * MAXMT, 4 * MAXMT), 0);
+                    if (lane == kWave - 1) s_active += incl;
                 }
                 __syncthreads();
             }
@@ -140,8 +153,8 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
     auto tile_row = [](int r) { return GATE ? r / (R / 2) * 16 + r % (R / 2) * 4 : r * 4; };
 
     dev::u32x4 w[R];
-    uint32_t word[R], expo[R];
-    __amdgpu_buffer_rsrc_t rc = rsrc(p.w.codes), rg = rsrc(p.w.words), re = rsrc(p.w.exps);
+    uint32_t word[R];
+    __amdgpu_buffer_rsrc_t rc = rsrc(p.w.codes), rg = rsrc(p.w.words);
     uint32_t left = 0;                                          // last row of the weights from the strip's first
     auto aim = [&](int u) {
         const Entry e = entry_of(u);
@@ -149,7 +162,6 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
         const Rows rows = rows_at(p.w, e.offset);
         rc = rsrc(rows.codes + int64_t(n0) * (p.K / 2));
         rg = rsrc(rows.words + int64_t(n0) * p.w.groups);
-        re = rsrc(rows.exps + n0);
         left = uint32_t(p.N - 1 - n0);
     };
     auto load = [&](int r, int pass) {
@@ -160,13 +172,14 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
             rc, in ? row * uint32_t(p.K / 2) + uint32_t(piece) * 16 : kOutside, 0, kStream));
         word[r] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(
             rg, in ? (row * uint32_t(p.w.groups) + (uint32_t(piece) * 32 >> p.w.shift)) * 2 : kOutside, 0, 0));
-        if (pass == 0) expo[r] = uint8_t(__builtin_amdgcn_raw_buffer_load_b8(re, row, 0, 0));
     };
 
-    // this workgroup's units: a run of them, so that it changes entries seldom
+    // this workgroup's units.  Experts: a run of them, so that it changes entries seldom; else all workgroups
+    // walk through the weights side by side (100003 x 4096 at one token 53.4 us against 55.1)
     const int share = total / int(gridDim.x), more = total % int(gridDim.x), id = int(blockIdx.x);
-    int u = id * share + (id < more ? id : more);
-    const int end = u + share + (id < more ? 1 : 0);
+    const int step = EXPERTS ? 1 : int(gridDim.x);
+    int u = EXPERTS ? id * share + (id < more ? id : more) : id;
+    const int end = EXPERTS ? u + share + (id < more ? 1 : 0) : total;
     if (u >= end) return;
     aim(u);
 #pragma unroll
@@ -180,7 +193,7 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
     int turn = 0;
     auto run = [&](auto mt_, const Entry& e, int u, bool fresh) {
         constexpr int MT = decltype(mt_)::value, V = R * MT * 4, Q = V / 4;
-        const int next = u + 1;
+        const int next = u + step;
         dev::f32x4 y[MT][R];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -206,10 +219,21 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
             auto place = [&](int v) { return (row / ROWS * f.kw) * (V * 4) + (v / Q * 4 + in % 4) * Q + v % Q; };
             return Item{n, t, place(v), place(v + 2 * R), i < items && t < e.count && strip < f.strips && n < p.N};
         };
-        auto row_to = [&](const Item& i) {
-            return !i.live ? 0 : int32_t(EXPERTS ? row_out<KIND>(p, e.shared, e.base, i.t) : int64_t(e.base) + i.t);
+        // what finishing an item reads: its rows' exponents, and its row of out
+        struct Needs {
+            uint32_t exp, up;
+            int32_t to;
         };
-        int32_t first = 0;
+        auto needs = [&](const Item& i) {
+            Needs n{0, 0, 0};
+            if (!i.live) return n;
+            const uint8_t* exps = p.w.exps + e.offset;
+            n.exp = exps[i.n];
+            if constexpr (GATE) n.up = exps[i.n + 16];
+            n.to = int32_t(EXPERTS ? row_out<KIND>(p, e.shared, e.base, i.t) : int64_t(e.base) + i.t);
+            return n;
+        };
+        Needs first{0, 0, 0};
         for (int pass = 0; pass < passes; ++pass) {
             const int piece = (pass * f.kw + kw) * 16 + block;
             if (fresh || passes > 1) {
@@ -240,13 +264,13 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
             if (last) {
                 // what finishing reads, ahead of the next unit's weights (a wait for a load waits for every older
                 // one; a thread has one item with four waves along K and more)
-                first = row_to(item(0));
+                first = needs(item(0));
                 if (next < end) aim(next);
             }
             const int ahead = last ? 0 : pass + 1;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float s = word_scale(word[r]) * 512.0f * row_scale(expo[r]), z = -word_zero(word[r]);
+                const float s = word_scale(word[r]) * (512.0f * kDown32), z = -word_zero(word[r]);
                 s16x4 b[8];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -296,13 +320,17 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
         for (int q = 0; q * threads < items; ++q) {
             const Item i = item(q);
             if (!i.live) continue;
-            const int64_t to = q == 0 ? first : row_to(i);
+            const Needs n = q == 0 ? first : needs(i);
+            const int64_t to = n.to;
             float sum = 0.0f, up = 0.0f;
+#pragma unroll 8
             for (int k = 0; k < f.kw; ++k) {
                 sum += mine[i.at + k * (V * 4)];
                 if constexpr (GATE) up += mine[i.up + k * (V * 4)];
             }
+            sum = scaled(sum, n.exp);
             if constexpr (GATE) {
+                up = scaled(up, n.up);
                 static_cast<uint16_t*>(p.out)[to * p.ldo + i.n / 32 * 16 + i.n % 16] = dev::f32_to_bf16_bits(gated(sum, up));
             } else if constexpr (KIND == kOut32) {
                 static_cast<float*>(p.out)[to * p.ldo + i.n] = sum;
@@ -312,15 +340,12 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
         }
     };
     int had = -1;
-    for (; u < end; ++u) {
+    for (; u < end; u += step) {
         const Entry e = entry_of(u);
         const bool fresh = u / units != had;
         had = u / units;
-        if constexpr (MAXMT >= 4) {
-            if (e.count > 8) run(std::integral_constant<int, 4>{}, e, u, fresh);
-        }
         if constexpr (MAXMT >= 2) {
-            if (e.count > 4 && e.count <= 8) run(std::integral_constant<int, 2>{}, e, u, fresh);
+            if (e.count > 4) run(std::integral_constant<int, 2>{}, e, u, fresh);
         }
         if (e.count <= 4) run(std::integral_constant<int, 1>{}, e, u, fresh);
     }
@@ -337,9 +362,8 @@ hipError_t launch_as(const Product& p, const ExpertList* list, hipStream_t s) {
     f.rw = 1;
     f.strips = int((int64_t(p.N) + strip_rows - 1) / strip_rows);
     f.entries = list ? list->n : int((p.T + 4 * MAXMT - 1) / (4 * MAXMT));
-    f.limit = 4 * MAXMT;
     const int per_cu = std::max(1, 4 * kWavesPerSimd<MAXMT, P> / (f.kw * f.rw));
-    const int64_t units = int64_t((f.strips + f.rw - 1) / f.rw) * f.entries;
+    const int64_t units = int64_t((f.strips + f.rw - 1) / f.rw) * (list ? std::min<int64_t>(kFewBlocks, list->n + p.T * (p.top_k + 1) / (4 * MAXMT)) : f.entries);
     const int64_t grid = std::min<int64_t>(units, int64_t(n_cu) * per_cu);
     const int lds = 2 * kMaxWaves * R * MAXMT * 16 * 4;
     hipLaunchKernelGGL((k_i4_few<KIND, MAXMT, R, P>), dim3(unsigned(grid)), dim3(f.kw * f.rw * kWave), lds, s, p,
@@ -350,16 +374,14 @@ hipError_t launch_as(const Product& p, const ExpertList* list, hipStream_t s) {
 template <int KIND, int P>
 hipError_t choose(const Product& p, const ExpertList* list, hipStream_t s) {
     if (p.T <= 4) return launch_as<KIND, 1, 4, P>(p, list, s);
-    if (p.T <= 8 || P == 3) return launch_as<KIND, 2, 4, P>(p, list, s);
-    if constexpr (P == 1) return launch_as<KIND, 4, 4, P>(p, list, s);
-    return hipErrorInvalidValue;
+    return launch_as<KIND, 2, 4, P>(p, list, s);
 }
 
 }  // namespace
 
 hipError_t launch_i4_few(int kind, const Product& p, const ExpertList* list, hipStream_t s) {
     if (p.T == 0) return hipSuccess;
-    if (p.T > kFewTokens) return hipErrorInvalidValue;
+    if (!list && p.T > kFewTokens) return hipErrorInvalidValue;
     const bool parts = p.planes == 3;
     switch (kind) {
         case kOut16: return parts ? choose<kOut16, 3>(p, nullptr, s) : choose<kOut16, 1>(p, nullptr, s);

@@ -1,0 +1,357 @@
+// Products of some 17 to 128 rows of x with 4-bit weights, dense and by expert: a stream of codes that feeds
+// 16x16x32 matrix instructions.
+//
+// A wave owns 32 rows of the weights and up to 128 of x.  Waves share the work two ways: WN of them have rows of
+// their own and the same k, WK of them the same rows and slices of 64 k by turns.  With few rows of
+// weights in all, a workgroup has 32 or 64 of them and its waves split K, so that the chip is full; with
+// many, its waves have rows of their own and share x, which is what has to be read again for every run of rows:
+// T K numbers for each 32 WN rows.
+//
+// Everything comes by loads straight into LDS, S slices ahead and counted by the wave itself: x as rows of 128
+// bytes (16-byte chunk c of row r at slot c ^ ((r >> 1) & 7)), the codes as rows of 32 bytes, the groups'
+// words one in four bytes.  A lane turns 16 codes of a weight row, one group, into two fragments of exact bf16
+// weights, once for all rows of x.  Sums of the waves meet in LDS at the end, in a fixed order.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "dense.h"
+#include "i4_common.h"
+
+namespace moe {
+namespace i4 {
+namespace {
+
+using dev::kWave;
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((address_space(3))) void lds_void;
+typedef uint32_t __attribute__((ext_vector_type(4), aligned(4))) words4;
+typedef uint32_t __attribute__((ext_vector_type(2), aligned(4))) words2;
+
+constexpr int kSlice = 128;                  // bytes of a row of x in a slice
+
+__device__ __forceinline__ int row_swz(int r) { return (r >> 1) & 7; }
+constexpr int wait_for(int vm, int lgkm) { return (vm & 15) | (7 << 4) | (lgkm << 8) | ((vm >> 4) << 14); }
+
+__device__ __forceinline__ dev::f32x4 mma(const bf16x8& a, const bf16x8& b, const dev::f32x4& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+constexpr uint32_t kRange = 0xFFFFFFFFu;     // of the buffer descriptors
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, int(kRange), 0x00027000);
+}
+// A lane's 16 bytes to its place of the wave's KiB; its two bytes into four of the wave's 256.  `at`: the lane's offset,
+// `from`: the slice's.
+__device__ __forceinline__ void load16_lds(__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t at, uint32_t from) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 16, at, from, 0, 0);
+}
+__device__ __forceinline__ void load2_lds(__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t at, uint32_t from) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 2, at, from, 0, 0);
+}
+
+template <int MF, int WK, int WN, int S>
+struct Mid {
+    static constexpr int NW = WK * WN, kThreads = NW * kWave, BM = MF * 16, BN = 32 * WN;
+    static constexpr int X = BM * kSlice, W = 32 * 32, WORDS = 256;              // bytes of a slice
+    static constexpr int kStage = WK * X + NW * (W + WORDS);
+    static constexpr int XL = X / 1024 / WN;                                     // a wave's loads of x
+    static constexpr int kRow = 36, kSums = NW * BM * kRow * 4;                  // staged sums: rows of 32, padded
+    static constexpr int kLds = S * kStage > kSums ? S * kStage : kSums;
+    static_assert(XL * WN * 1024 == X && kLds <= 160 * 1024, "LDS of a CU");
+    static constexpr int kWavesPerSimd = NW * (160 * 1024 / kLds) / 4 < 1 ? 1 : NW * (160 * 1024 / kLds) / 4 > 4 ? 4 : NW * (160 * 1024 / kLds) / 4;
+};
+
+template <int KIND, int MF, int WK, int WN, int S>
+__global__ void __launch_bounds__((Mid<MF, WK, WN, S>::kThreads))
+    __attribute__((amdgpu_waves_per_eu((Mid<MF, WK, WN, S>::kWavesPerSimd))))
+k_i4_mid(const Product p, const ExpertList list, const int4* __restrict__ map, int n_tiles, int m_tiles) {
+    typedef Mid<MF, WK, WN, S> C;
+    constexpr bool EXPERTS = KIND == kGateUp || KIND == kDown, GATE = KIND == kGateUp;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    // row tiles fastest: those of one run of weights are neighbours
+    const int id = blockIdx.x;
+    int base = 0, left, n0;
+    int64_t r0;
+    bool shared = false;
+    Rows w = p.w;
+    if constexpr (EXPERTS) {
+        const int tiles = reinterpret_cast<const int*>(map)[0];
+        if (id >= tiles * n_tiles) return;
+        const int4 rec = map[1 + id / n_tiles];
+        n0 = id % n_tiles * C::BN;
+        r0 = int64_t(rec.y) * C::BM;
+        base = rec.z;
+        left = rec.w - int(r0);
+        const int ent = list.ent[rec.x];
+        shared = (ent & 1023) == kSharedTag;
+        w = rows_at(p.w, blob_offset(p, ent));
+    } else {
+        r0 = int64_t(id % m_tiles) * C::BM;
+        n0 = id / m_tiles * C::BN;
+        left = int(min(p.T - r0, int64_t(C::BM)));
+    }
+    const int rows = min(left, C::BM);
+
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
+    const int wn = wave % WN, wk = wave / WN;
+    const int j = lane % 16, kb = lane / 16;
+    const int slices = (p.K + 63) / 64, n = (slices * p.planes + WK - 1) / WK;
+    const bool odd = p.K % 64 != 0;
+    // x: offsets of the lane's 16 bytes in row r of the tile.  Where K ends in the middle of a slice its second half is
+    // the first again, with weights 0 (a token's own numbers: an infinity times 0 does no harm to another).
+    uint32_t xo[C::XL];
+    int64_t x0 = 0;                                           // (dense: offsets from the tile's first row)
+    if (!EXPERTS) x0 = r0;
+    else if (KIND == kDown) x0 = base + r0;
+#pragma unroll
+    for (int q = 0; q < C::XL; ++q) {
+        const int r = (wn + WN * q) * 8 + lane / 8, rr = min(r, rows - 1);
+        const int64_t from = KIND == kGateUp ? row_in<KIND>(p, shared, base, int(r0) + rr) : int64_t(rr);
+        xo[q] = uint32_t(from * p.ldx * 2) + (lane % 8 ^ row_swz(r)) * 16;
+    }
+    const uint16_t* xp = p.x + x0 * p.ldx;
+    const int nb = n0 + wn * 32;                              // the wave's first weight row
+    const int first_row = min(nb, p.N - 1), row_l = min(nb + lane / 2, p.N - 1) - first_row;
+    const uint32_t co = uint32_t(row_l) * uint32_t(p.K / 2) + lane % 2 * 16;
+    const uint32_t wo = (uint32_t(row_l) * uint32_t(w.groups) + (lane % 2 * 32 >> w.shift)) * 2;
+    const __amdgpu_buffer_rsrc_t rc = rsrc(w.codes + int64_t(first_row) * (p.K / 2)),
+                                 rg = rsrc(w.words + int64_t(first_row) * w.groups);
+    float E[2];
+#pragma unroll
+    for (int f = 0; f < 2; ++f) E[f] = row_scale(w.exps[min(nb + f * 16 + j, p.N - 1)]);
+
+    // LDS of a stage: x of the WK slices, then codes and words of each wave
+    auto x_at = [&](int stage) { return lds + stage * C::kStage + wk * C::X; };
+    auto w_at = [&](int stage) { return lds + stage * C::kStage + WK * C::X + wave * (C::W + C::WORDS); };
+    int plane = p.planes - 1, slice = wk;                     // of the next request; smallest parts first
+    auto settle = [&](int& slice, int& plane) {
+        while (slice >= slices && plane > 0) slice -= slices, --plane;
+    };
+    settle(slice, plane);
+    auto issue = [&](int stage) {
+        // (past the end: the last slice again, with weights 0)
+        const int s = min(slice, slices - 1);
+        const __amdgpu_buffer_rsrc_t rx = rsrc(xp + plane * p.plane);
+        uint8_t *dx = x_at(stage) + wn * 1024, *dw = w_at(stage);
+        if (odd && s + 1 == slices) {
+#pragma unroll
+            for (int q = 0; q < C::XL; ++q) {
+                const int c = lane % 8 ^ row_swz((wn + WN * q) * 8 + lane / 8);
+                load16_lds(rx, dx + q * (WN * 1024), xo[q] - (c >= 4 ? 64 : 0), s * 128);
+            }
+            load16_lds(rc, dw, co - lane % 2 * 16, s * 32);
+            load2_lds(rg, dw + C::W, wo - (lane % 2 * 32 >> w.shift) * 2, (s * 64 >> w.shift) * 2);
+        } else {
+#pragma unroll
+            for (int q = 0; q < C::XL; ++q) load16_lds(rx, dx + q * (WN * 1024), xo[q], s * 128);
+            load16_lds(rc, dw, co, s * 32);
+            load2_lds(rg, dw + C::W, wo, (s * 64 >> w.shift) * 2);
+        }
+        slice += WK;
+        settle(slice, plane);
+    };
+    dev::f32x4 acc[MF][2];
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) acc[i][f] = dev::f32x4{0, 0, 0, 0};
+
+    constexpr int kLoads = C::XL + 2;
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) issue(s);
+    int now = wk, now_plane = p.planes - 1, stage = 0, ahead = S - 1;
+    for (int it = 0; it < n; ++it) {
+        // this slice has landed, and every wave is past the one whose place the next request takes
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(wait_for((S - 2) * kLoads, 0));
+        asm volatile("" ::: "memory");
+        if constexpr (WN > 1) __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        const uint8_t *x = x_at(stage), *wl = w_at(stage);
+        uint2 c[2];
+        uint32_t word[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const int r = f * 16 + j;
+            c[f] = *reinterpret_cast<const uint2*>(wl + r * 32 + kb * 8);
+            word[f] = *reinterpret_cast<const uint32_t*>(wl + C::W + (r * 2 + kb / 2) * 4);
+        }
+        // k of instruction q in lane block kb: 16 kb + 8 q on, chunk 2 kb + q
+        auto read_x = [&](int i, int q) {
+            return *reinterpret_cast<const bf16x8*>(x + (i * 16 + j) * kSlice + ((2 * kb + q) ^ row_swz(j)) * 16);
+        };
+        constexpr int EARLY = MF < 4 ? MF : 4;                // fragments read ahead of the decoding
+        bf16x8 fa[EARLY][2];
+#pragma unroll
+        for (int i = 0; i < EARLY; ++i) fa[i][0] = read_x(i, 0), fa[i][1] = read_x(i, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        issue(ahead);
+        settle(now, now_plane);
+        const uint32_t live = now >= slices ? 0u : odd && now + 1 == slices && kb >= 2 ? 0u : ~0u;
+        bf16x8 fb[2][2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const uint32_t wd = word[f] & live;               // (0: scale 0)
+            const float s = word_scale(wd) * E[f], off = -word_zero(wd) * s, s2 = s * 512.0f;
+            fb[f][0] = __builtin_bit_cast(bf16x8, decode8(c[f].x, s2, off));
+            fb[f][1] = __builtin_bit_cast(bf16x8, decode8(c[f].y, s2, off));
+        }
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const bf16x8 a = i < EARLY ? fa[i < EARLY ? i : 0][q] : read_x(i, q);
+#pragma unroll
+                for (int f = 0; f < 2; ++f) acc[i][f] = mma(fb[f][q], a, acc[i][f]);
+            }
+        now += WK;
+        stage = stage + 1 == S ? 0 : stage + 1;
+        ahead = ahead + 1 == S ? 0 : ahead + 1;
+    }
+
+    // sums of the waves: [wave][row of x][32 weight rows]
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+            *reinterpret_cast<dev::f32x4*>(red + (wave * C::BM + i * 16 + j) * C::kRow + f * 16 + kb * 4) = acc[i][f];
+    __syncthreads();
+    constexpr int PER = (GATE ? 4 : 8) * WN;                  // items of 4 results in a row of x
+    for (int i = tid; i < rows * PER; i += C::kThreads) {
+        const int r = i / PER, c = i % PER, cw = c / (PER / WN), col = c % (PER / WN) * 4;
+        auto sum = [&](int at) {
+            dev::f32x4 t = *reinterpret_cast<const dev::f32x4*>(red + (cw * C::BM + r) * C::kRow + at);
+#pragma unroll
+            for (int k = 1; k < WK; ++k)
+                t += *reinterpret_cast<const dev::f32x4*>(red + ((k * WN + cw) * C::BM + r) * C::kRow + at);
+            return t;
+        };
+        dev::f32x4 v = sum(col);
+        const int nn = n0 + cw * 32 + col;
+        if (nn >= p.N) continue;
+        if constexpr (GATE) {
+            const dev::f32x4 up = sum(col + 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = gated(v[e], up[e]);
+        }
+        const int64_t to = EXPERTS ? row_out<KIND>(p, shared, base, int(r0) + r) : r0 + r;
+        if constexpr (KIND == kOut32) {
+            float* o = static_cast<float*>(p.out) + to * p.ldo + nn;
+            if (nn + 4 <= p.N) {
+                *reinterpret_cast<words4*>(o) = __builtin_bit_cast(dev::u32x4, v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (nn + e < p.N) o[e] = v[e];
+            }
+        } else {
+            uint16_t* o = static_cast<uint16_t*>(p.out) + to * p.ldo + (GATE ? nn / 32 * 16 + nn % 16 : nn);
+            if (EXPERTS || (p.wide && nn + 4 <= p.N)) {
+                *reinterpret_cast<words2*>(o) = words2{dev::pack_bf16x2(v[0], v[1]), dev::pack_bf16x2(v[2], v[3])};
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (nn + e < p.N) o[e] = dev::f32_to_bf16_bits(v[e]);
+            }
+        }
+    }
+}
+
+// The tile map: one workgroup, one thread an entry (513 at most).
+__global__ __launch_bounds__(1024) void k_i4_map(const ExpertList list, const int32_t* __restrict__ offsets, int T, int top_k,
+                                                 int tile, int4* __restrict__ map) {
+    __shared__ int s_sum[16];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    int count = 0, base = 0;
+    if (tid < list.n) {
+        const int e = list.ent[tid] & 1023;
+        base = e == kSharedTag ? T * top_k : offsets[e];
+        count = e == kSharedTag ? T : offsets[e + 1] - base;
+    }
+    const int tiles = (count + tile - 1) / tile;
+    int incl = tiles;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int o = __shfl_up(incl, d, kWave);
+        if (lane >= d) incl += o;
+    }
+    if (lane == kWave - 1) s_sum[wave] = incl;
+    __syncthreads();
+    int first = incl - tiles, total = 0;
+    for (int w = 0; w < 16; ++w) {
+        if (w < wave) first += s_sum[w];
+        total += s_sum[w];
+    }
+    for (int i = 0; i < tiles; ++i) map[1 + first + i] = make_int4(tid, i, base, count);
+    if (tid == 0) reinterpret_cast<int*>(map)[0] = total;
+}
+
+hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
+template <int KIND, int MF, int WK, int WN, int S>
+hipError_t launch_as(const Product& p, const ExpertList* list, const void* map, int64_t max_tiles, hipStream_t s) {
+    typedef Mid<MF, WK, WN, S> C;
+    static const ExpertList none{};
+    static std::atomic<uint64_t> allowed{0};
+    const int64_t nt = (p.N + C::BN - 1) / C::BN, mt = list ? max_tiles : (p.T + C::BM - 1) / C::BM, blocks = nt * mt;
+    if (blocks == 0) return hipSuccess;
+    if (blocks > 0x7FFFFFFF / C::kThreads) return hipErrorInvalidValue;
+    const auto kernel = &k_i4_mid<KIND, MF, WK, WN, S>;
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), C::kLds, allowed);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(unsigned(blocks)), dim3(C::kThreads), C::kLds, s, p, list ? *list : none,
+                       static_cast<const int4*>(map), int(nt), int(mt));
+    return hipGetLastError();
+}
+
+template <int KIND>
+hipError_t choose(int kind, const Product& p, const ExpertList* list, const void* map, int64_t max_tiles, hipStream_t s) {
+    switch (kind) {
+        case kMid32x32: return launch_as<KIND, 2, 8, 1, 3>(p, list, map, max_tiles, s);
+        case kMid64x32: return launch_as<KIND, 4, 8, 1, 2>(p, list, map, max_tiles, s);
+        case kMid128x32: return launch_as<KIND, 8, 4, 1, 2>(p, list, map, max_tiles, s);
+        case kMid64x64: return launch_as<KIND, 4, 4, 2, 3>(p, list, map, max_tiles, s);
+        case kMid128x64: return launch_as<KIND, 8, 4, 2, 2>(p, list, map, max_tiles, s);
+        case kMid32x128: return launch_as<KIND, 2, 2, 4, 4>(p, list, map, max_tiles, s);
+        case kMid64x128: return launch_as<KIND, 4, 2, 4, 3>(p, list, map, max_tiles, s);
+        case kMid128x256: return launch_as<KIND, 8, 1, 8, 3>(p, list, map, max_tiles, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_i4_map(const ExpertList& list, const int32_t* offsets, int64_t T, int top_k, int rows, void* map,
+                         hipStream_t s) {
+    hipLaunchKernelGGL(k_i4_map, dim3(1), dim3(1024), 0, s, list, offsets, int(T), top_k, rows, static_cast<int4*>(map));
+    return hipGetLastError();
+}
+
+hipError_t launch_i4_mid(int what, int kind, const Product& p, const ExpertList* list, const void* map, int64_t max_tiles,
+                         hipStream_t s) {
+    if (p.T == 0) return hipSuccess;
+    switch (what) {
+        case kOut16: return choose<kOut16>(kind, p, nullptr, nullptr, 0, s);
+        case kOut32: return choose<kOut32>(kind, p, nullptr, nullptr, 0, s);
+        case kGateUp: return choose<kGateUp>(kind, p, list, map, max_tiles, s);
+        default: return choose<kDown>(kind, p, list, map, max_tiles, s);
+    }
+}
+
+}  // namespace i4
+}  // namespace moe
