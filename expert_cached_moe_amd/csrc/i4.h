@@ -20,7 +20,7 @@ constexpr int kMaxCount = 1 << 23;    // rows: the threads of a launch fit 32 bi
 // Rows of 4-bit weights: those of entry e begin `offset(e)` bytes on in all three arrays.
 struct Rows {
     const uint8_t* codes;    // [N][K / 2]
-    const uint16_t* words;   // [N][groups]
+    const uint16_t* words;   // by 16 rows: see word_at
     const uint8_t* exps;     // [N]
     int32_t groups;          // of a row
     int32_t shift;           // log2 of a group's length
@@ -33,6 +33,21 @@ enum {
     kGateUp = 2,  // an expert's rows: x of the pair's token to h of its place in expert order
     kDown = 3,    // h of a place to the pair's own row
 };
+
+// Where the word of row n, group g lies among N rows: runs of 16 rows lie one behind the other, in each the
+// words of a group side by side (the last run has what rows are left).  So the words of a matrix instruction's rows are one
+// piece of a line, not one of each row: as [N][groups] their loads took 15% of the time of the products of few rows.
+struct WordAt {
+    int64_t first;           // of group 0
+    int32_t step;            // from group to group
+};
+#ifdef __HIP__
+__host__ __device__
+#endif
+inline WordAt word_at(int64_t n, int64_t N, int32_t groups) {
+    const int64_t run = n & ~int64_t(15), left = N - run;
+    return WordAt{run * groups + (n - run), left < 16 ? int32_t(left) : 16};
+}
 
 struct Product {
     const uint16_t* x;       // bf16 rows, 16-byte aligned, ldx elements apart

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kMaxWaves* kWave) __attribute__((amdgpu_waves_
 k_i4_few(const Product p, const ExpertList list, const Few f) {
     constexpr bool GATE = KIND == kGateUp, EXPERTS = KIND == kGateUp || KIND == kDown;
     __shared__ int4 s_entry[EXPERTS ? kFewBlocks : 1];
-    __shared__ int s_active;
+    __shared__ int s_waves[kMaxWaves];
     extern __shared__ __attribute__((aligned(16))) float red[];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
     const int rw = wave / f.kw, kw = wave % f.kw;
@@ -99,9 +99,9 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
 
     int total = f.entries * units;
     if constexpr (EXPERTS) {
-        // entries with rows, in the list's order
-        if (tid == 0) s_active = 0;
-        __syncthreads();
+        // entries with rows, in the list's order (the same list in every workgroup); one of more rows is several
+        // of 4 MAXMT
+        int active = 0;
         for (int i0 = 0; i0 < list.n; i0 += blockDim.x) {
             const int i = i0 + tid;
             int base = 0, count = 0, ent = 0;
@@ -111,27 +111,32 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
                 base = e == kSharedTag ? int(p.T) * p.top_k : p.offsets[e];
                 count = e == kSharedTag ? int(p.T) : p.offsets[e + 1] - base;
             }
-            // an entry of more rows is several of 4 MAXMT
             const int blocks = (count + 4 * MAXMT - 1) / (4 * MAXMT);
             int incl = blocks;
+            if (__any(blocks > 1)) {
 #pragma unroll
-            for (int d = 1; d < kWave; d <<= 1) {
-                const int o = __shfl_up(incl, d, kWave);
-                if (lane >= d) incl += o;
-            }
-            // (waves in order: the list is the same in every workgroup)
-            for (int w = 0; w < int(blockDim.x) / kWave; ++w) {
-                if (w == wave) {
-                    const int first = s_active + incl - blocks;
-                    for (int q = 0; q < blocks; ++q)
-                        if (first + q < kFewBlocks)           // (the host has seen to it)
-                            s_entry[first + q] = make_int4(ent, base + q * 4 * MAXMT, min(count - q * 4 * MAXMT, 4 * MAXMT), 0);
-                    if (lane == kWave - 1) s_active += incl;
+                for (int d = 1; d < kWave; d <<= 1) {
+                    const int o = __shfl_up(incl, d, kWave);
+                    if (lane >= d) incl += o;
                 }
-                __syncthreads();
+            } else {
+                incl = __popcll(__ballot(blocks) << (63 - lane));
             }
+            if (i0) __syncthreads();                          // the last turn's sums are read
+            if (lane == kWave - 1) s_waves[wave] = incl;
+            __syncthreads();
+            int first = active + incl - blocks;
+            for (int w = 0; w < int(blockDim.x) / kWave; ++w) {
+                const int n = s_waves[w];
+                if (w < wave) first += n;
+                active += n;
+            }
+            for (int q = 0; q < blocks; ++q)
+                if (first + q < kFewBlocks)                   // (the host has seen to it)
+                    s_entry[first + q] = make_int4(ent, base + q * 4 * MAXMT, min(count - q * 4 * MAXMT, 4 * MAXMT), 0);
         }
-        total = s_active * units;
+        __syncthreads();
+        total = __builtin_amdgcn_readfirstlane(active) * units;
     }
     auto entry_of = [&](int u) {
         const int a = u / units;
@@ -155,14 +160,20 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
     dev::u32x4 w[R];
     uint32_t word[R];
     __amdgpu_buffer_rsrc_t rc = rsrc(p.w.codes), rg = rsrc(p.w.words);
-    uint32_t left = 0;                                          // last row of the weights from the strip's first
+    uint32_t first = 0, left = 0;                               // first row of the strip, and rows behind it
     auto aim = [&](int u) {
         const Entry e = entry_of(u);
         const int strip = strip_of(u), n0 = first_row(strip < f.strips ? strip : f.strips - 1);
         const Rows rows = rows_at(p.w, e.offset);
         rc = rsrc(rows.codes + int64_t(n0) * (p.K / 2));
-        rg = rsrc(rows.words + int64_t(n0) * p.w.groups);
+        rg = rsrc(rows.words + int64_t(n0 & ~15) * p.w.groups);
+        first = uint32_t(n0);
         left = uint32_t(p.N - 1 - n0);
+    };
+    // (from the first word of the strip's run of 16 rows)
+    auto word_of = [&](uint32_t row, uint32_t group) {
+        const uint32_t n = first + row, run = n & ~15u, rest = uint32_t(p.N) - run;
+        return (run - (first & ~15u)) * uint32_t(p.w.groups) + group * (rest < 16 ? rest : 16u) + (n - run);
     };
     auto load = [&](int r, int pass) {
         const int piece = (pass * f.kw + kw) * 16 + block;
@@ -171,7 +182,7 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
         w[r] = __builtin_bit_cast(dev::u32x4, __builtin_amdgcn_raw_buffer_load_b128(
             rc, in ? row * uint32_t(p.K / 2) + uint32_t(piece) * 16 : kOutside, 0, kStream));
         word[r] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(
-            rg, in ? (row * uint32_t(p.w.groups) + (uint32_t(piece) * 32 >> p.w.shift)) * 2 : kOutside, 0, 0));
+            rg, in ? word_of(row, uint32_t(piece) * 32 >> p.w.shift) * 2 : kOutside, 0, 0));
     };
 
     // this workgroup's units.  Experts: a run of them, so that it changes entries seldom; else all workgroups

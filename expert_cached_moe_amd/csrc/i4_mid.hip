@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "dense.h"
 #include "i4_common.h"
@@ -38,7 +39,7 @@ constexpr int wait_for(int vm, int lgkm) { return (vm & 15) | (7 << 4) | (lgkm <
 __device__ __forceinline__ dev::f32x4 mma(const bf16x8& a, const bf16x8& b, const dev::f32x4& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-constexpr uint32_t kRange = 0xFFFFFFFFu;     // of the buffer descriptors
+constexpr uint32_t kRange = 0xFFFF0000u;     // of the buffer descriptors
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, int(kRange), 0x00027000);
 }
@@ -51,48 +52,130 @@ __device__ __forceinline__ void load2_lds(__amdgpu_buffer_rsrc_t r, uint8_t* to,
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 2, at, from, 0, 0);
 }
 
-template <int MF, int WK, int WN, int S>
+template <int MF_, int WK_, int WN_, int S_>
 struct Mid {
+    static constexpr int MF = MF_, WK = WK_, WN = WN_, S = S_;
     static constexpr int NW = WK * WN, kThreads = NW * kWave, BM = MF * 16, BN = 32 * WN;
     static constexpr int X = BM * kSlice, W = 32 * 32, WORDS = 256;              // bytes of a slice
     static constexpr int kStage = WK * X + NW * (W + WORDS);
     static constexpr int XL = X / 1024 / WN;                                     // a wave's loads of x
-    static constexpr int kRow = 36, kSums = NW * BM * kRow * 4;                  // staged sums: rows of 32, padded
+    static constexpr int kPassRows = WK == 1 && BM > 32 ? 32 : BM, kRow = 36, kSums = NW * kPassRows * kRow * 4;   // staged sums
     static constexpr int kLds = S * kStage > kSums ? S * kStage : kSums;
     static_assert(XL * WN * 1024 == X && kLds <= 160 * 1024, "LDS of a CU");
     static constexpr int kWavesPerSimd = NW * (160 * 1024 / kLds) / 4 < 1 ? 1 : NW * (160 * 1024 / kLds) / 4 > 4 ? 4 : NW * (160 * 1024 / kLds) / 4;
 };
+
+// The tile of a workgroup: row tiles fastest, those of one run of weights are neighbours.
+struct At {
+    int64_t r0;              // first row of x, in the entry
+    int n0, base, left;      // first row of the weights; first place of the entry; rows from r0 on
+    bool shared, any;
+    Rows w;
+};
+template <int KIND, class C>
+__device__ __forceinline__ At tile_at(const Product& p, const ExpertList& list, const int4* map, int n_tiles, int m_tiles) {
+    const int id = blockIdx.x;
+    At at;
+    at.w = p.w;
+    at.base = 0;
+    at.shared = false;
+    at.any = true;
+    if constexpr (KIND == kGateUp || KIND == kDown) {
+        const int tiles = reinterpret_cast<const int*>(map)[0];
+        at.any = id < tiles * n_tiles;
+        if (!at.any) return at;
+        const int4 rec = map[1 + id / n_tiles];
+        at.n0 = id % n_tiles * C::BN;
+        at.r0 = int64_t(rec.y) * C::BM;
+        at.base = rec.z;
+        at.left = rec.w - int(at.r0);
+        const int ent = list.ent[rec.x];
+        at.shared = (ent & 1023) == kSharedTag;
+        at.w = rows_at(p.w, blob_offset(p, ent));
+    } else {
+        at.r0 = int64_t(id % m_tiles) * C::BM;
+        at.n0 = id / m_tiles * C::BN;
+        at.left = int(min(p.T - at.r0, int64_t(C::BM)));
+    }
+    return at;
+}
+
+// Sums of the waves, [wave][row of x][32 weight rows] in LDS, added in the waves' order, and finished.
+template <int KIND, class C>
+__device__ __forceinline__ void finish_sums(const Product& p, const dev::f32x4 (&acc)[C::MF][2], uint8_t* lds, int64_t r0, int n0,
+                                            int base, bool shared, int rows) {
+    constexpr bool EXPERTS = KIND == kGateUp || KIND == kDown, GATE = KIND == kGateUp;
+    constexpr int MF = C::MF, WK = C::WK, WN = C::WN;
+    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave, j = lane % 16, kb = lane / 16;
+    __builtin_amdgcn_s_waitcnt(0);
+    float* red = reinterpret_cast<float*>(lds);
+    // (nothing to add where no waves share rows: then 32 rows at a time, which leaves LDS for a second workgroup)
+    constexpr int PF = C::kPassRows / 16;
+#pragma unroll
+    for (int i0 = 0; i0 < MF; i0 += PF) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < PF; ++i)
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+                *reinterpret_cast<dev::f32x4*>(red + (wave * C::kPassRows + i * 16 + j) * C::kRow + f * 16 + kb * 4) = acc[i0 + i][f];
+        __syncthreads();
+        constexpr int PER = (GATE ? 4 : 8) * WN;                  // items of 4 results in a row of x
+        const int left = min(rows - i0 * 16, C::kPassRows);
+        for (int i = tid; i < left * PER; i += C::kThreads) {
+            const int r = i0 * 16 + i / PER, c = i % PER, cw = c / (PER / WN), col = c % (PER / WN) * 4;
+            auto sum = [&](int at) {
+                const float* from = red + (cw * C::kPassRows + i / PER) * C::kRow + at;
+                dev::f32x4 t = *reinterpret_cast<const dev::f32x4*>(from);
+#pragma unroll
+                for (int k = 1; k < WK; ++k) t += *reinterpret_cast<const dev::f32x4*>(from + k * WN * C::kPassRows * C::kRow);
+                return t;
+            };
+            dev::f32x4 v = sum(col);
+            const int nn = n0 + cw * 32 + col;
+            if (nn >= p.N) continue;
+            if constexpr (GATE) {
+                const dev::f32x4 up = sum(col + 16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = gated(v[e], up[e]);
+            }
+            const int64_t to = EXPERTS ? row_out<KIND>(p, shared, base, int(r0) + r) : r0 + r;
+            if constexpr (KIND == kOut32) {
+                float* o = static_cast<float*>(p.out) + to * p.ldo + nn;
+                if (nn + 4 <= p.N) {
+                    *reinterpret_cast<words4*>(o) = __builtin_bit_cast(dev::u32x4, v);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (nn + e < p.N) o[e] = v[e];
+                }
+            } else {
+                uint16_t* o = static_cast<uint16_t*>(p.out) + to * p.ldo + (GATE ? nn / 32 * 16 + nn % 16 : nn);
+                if (EXPERTS || (p.wide && nn + 4 <= p.N)) {
+                    *reinterpret_cast<words2*>(o) = words2{dev::pack_bf16x2(v[0], v[1]), dev::pack_bf16x2(v[2], v[3])};
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (nn + e < p.N) o[e] = dev::f32_to_bf16_bits(v[e]);
+                }
+            }
+        }
+    }
+}
 
 template <int KIND, int MF, int WK, int WN, int S>
 __global__ void __launch_bounds__((Mid<MF, WK, WN, S>::kThreads))
     __attribute__((amdgpu_waves_per_eu((Mid<MF, WK, WN, S>::kWavesPerSimd))))
 k_i4_mid(const Product p, const ExpertList list, const int4* __restrict__ map, int n_tiles, int m_tiles) {
     typedef Mid<MF, WK, WN, S> C;
-    constexpr bool EXPERTS = KIND == kGateUp || KIND == kDown, GATE = KIND == kGateUp;
+    constexpr bool EXPERTS = KIND == kGateUp || KIND == kDown;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-    // row tiles fastest: those of one run of weights are neighbours
-    const int id = blockIdx.x;
-    int base = 0, left, n0;
-    int64_t r0;
-    bool shared = false;
-    Rows w = p.w;
-    if constexpr (EXPERTS) {
-        const int tiles = reinterpret_cast<const int*>(map)[0];
-        if (id >= tiles * n_tiles) return;
-        const int4 rec = map[1 + id / n_tiles];
-        n0 = id % n_tiles * C::BN;
-        r0 = int64_t(rec.y) * C::BM;
-        base = rec.z;
-        left = rec.w - int(r0);
-        const int ent = list.ent[rec.x];
-        shared = (ent & 1023) == kSharedTag;
-        w = rows_at(p.w, blob_offset(p, ent));
-    } else {
-        r0 = int64_t(id % m_tiles) * C::BM;
-        n0 = id / m_tiles * C::BN;
-        left = int(min(p.T - r0, int64_t(C::BM)));
-    }
-    const int rows = min(left, C::BM);
+    const At at = tile_at<KIND, C>(p, list, map, n_tiles, m_tiles);
+    if (!at.any) return;
+    const Rows& w = at.w;
+    const int64_t r0 = at.r0;
+    const int n0 = at.n0, base = at.base, rows = min(at.left, C::BM);
+    const bool shared = at.shared;
 
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
     const int wn = wave % WN, wk = wave / WN;
@@ -115,9 +198,10 @@ k_i4_mid(const Product p, const ExpertList list, const int4* __restrict__ map, i
     const int nb = n0 + wn * 32;                              // the wave's first weight row
     const int first_row = min(nb, p.N - 1), row_l = min(nb + lane / 2, p.N - 1) - first_row;
     const uint32_t co = uint32_t(row_l) * uint32_t(p.K / 2) + lane % 2 * 16;
-    const uint32_t wo = (uint32_t(row_l) * uint32_t(w.groups) + (lane % 2 * 32 >> w.shift)) * 2;
+    const WordAt wa = word_at(first_row + row_l, p.N, w.groups);
+    const uint32_t wo = uint32_t(wa.first - int64_t(first_row & ~15) * w.groups + (lane % 2 * 32 >> w.shift) * wa.step) * 2;
     const __amdgpu_buffer_rsrc_t rc = rsrc(w.codes + int64_t(first_row) * (p.K / 2)),
-                                 rg = rsrc(w.words + int64_t(first_row) * w.groups);
+                                 rg = rsrc(w.words + int64_t(first_row & ~15) * w.groups);
     float E[2];
 #pragma unroll
     for (int f = 0; f < 2; ++f) E[f] = row_scale(w.exps[min(nb + f * 16 + j, p.N - 1)]);
@@ -142,12 +226,12 @@ k_i4_mid(const Product p, const ExpertList list, const int4* __restrict__ map, i
                 load16_lds(rx, dx + q * (WN * 1024), xo[q] - (c >= 4 ? 64 : 0), s * 128);
             }
             load16_lds(rc, dw, co - lane % 2 * 16, s * 32);
-            load2_lds(rg, dw + C::W, wo - (lane % 2 * 32 >> w.shift) * 2, (s * 64 >> w.shift) * 2);
+            load2_lds(rg, dw + C::W, wo + ((s * 64 >> w.shift) - (lane % 2 * 32 >> w.shift)) * wa.step * 2, 0);
         } else {
 #pragma unroll
             for (int q = 0; q < C::XL; ++q) load16_lds(rx, dx + q * (WN * 1024), xo[q], s * 128);
             load16_lds(rc, dw, co, s * 32);
-            load2_lds(rg, dw + C::W, wo, (s * 64 >> w.shift) * 2);
+            load2_lds(rg, dw + C::W, wo + (s * 64 >> w.shift) * wa.step * 2, 0);
         }
         slice += WK;
         settle(slice, plane);
@@ -212,55 +296,154 @@ k_i4_mid(const Product p, const ExpertList list, const int4* __restrict__ map, i
         ahead = ahead + 1 == S ? 0 : ahead + 1;
     }
 
-    // sums of the waves: [wave][row of x][32 weight rows]
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    float* red = reinterpret_cast<float*>(lds);
+    finish_sums<KIND, C>(p, acc, lds, at.r0, at.n0, at.base, at.shared, rows);
+}
+
+// The same with whole lines of codes in registers: a wave's 32 rows by blocks of 128 k, 16 bytes a lane and 16 rows, so
+// that the 32 codes of a lane share a group, D blocks ahead; x alone goes through LDS, in D + 1 stages.  Half the
+// waits, words and addresses for a code: for products whose time is the decoding, many rows of weights or many experts.
+template <int MF_, int WK_, int WN_, int D_>
+struct Wide {
+    static constexpr int MF = MF_, WK = WK_, WN = WN_, D = D_;
+    static constexpr int NW = WK * WN, kThreads = NW * kWave, BM = MF * 16, BN = 32 * WN;
+    static constexpr int X = BM * 256, kStage = WK * X;
+    static constexpr int XL = X / 1024 / WN;
+    static constexpr int kPassRows = WK == 1 && BM > 32 ? 32 : BM, kRow = 36, kSums = NW * kPassRows * kRow * 4;
+    static constexpr int kLds = (D + 1) * kStage > kSums ? (D + 1) * kStage : kSums;
+    static_assert(XL * WN * 1024 == X && kLds <= 160 * 1024, "LDS of a CU");
+    static constexpr int kPerCu = 160 * 1024 / kLds < 1 ? 1 : 160 * 1024 / kLds;
+    static constexpr int kWavesPerSimd = NW * kPerCu / 4 < 1 ? 1 : NW * kPerCu / 4 > 4 ? 4 : NW * kPerCu / 4;
+};
+constexpr uint32_t kOutside = 0xFFFFFFF0u;   // an offset past kRange: zeros, also into LDS
+
+template <int KIND, int MF, int WK, int WN, int D>
+__global__ void __launch_bounds__((Wide<MF, WK, WN, D>::kThreads))
+    __attribute__((amdgpu_waves_per_eu((Wide<MF, WK, WN, D>::kWavesPerSimd))))
+k_i4_wide(const Product p, const ExpertList list, const int4* __restrict__ map, int n_tiles, int m_tiles) {
+    typedef Wide<MF, WK, WN, D> C;
+    constexpr bool EXPERTS = KIND == kGateUp || KIND == kDown;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const At at = tile_at<KIND, C>(p, list, map, n_tiles, m_tiles);
+    if (!at.any) return;
+    const int rows = min(at.left, C::BM);
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
+    const int wn = wave % WN, wk = wave / WN;
+    const int j = lane % 16, kb = lane / 16;
+    const int blocks = (p.K + 127) / 128, n = (blocks * p.planes + WK - 1) / WK;
+
+    // x: 16 lanes a row of 256 bytes, 4 rows a load; 16-byte chunk c of row r at slot c ^ (r % 16)
+    uint32_t xo[C::XL];
+    int64_t x0 = 0;
+    if (!EXPERTS) x0 = at.r0;
+    else if (KIND == kDown) x0 = at.base + at.r0;
+#pragma unroll
+    for (int q = 0; q < C::XL; ++q) {
+        const int r = (wn + WN * q) * 4 + lane / 16, rr = min(r, rows - 1);
+        const int64_t from = KIND == kGateUp ? row_in<KIND>(p, at.shared, at.base, int(at.r0) + rr) : int64_t(rr);
+        xo[q] = uint32_t(from * p.ldx * 2);
+    }
+    const uint16_t* xp = p.x + x0 * p.ldx;
+    const int nb = at.n0 + wn * 32, first_row = min(nb, p.N - 1);
+    const __amdgpu_buffer_rsrc_t rc = rsrc(at.w.codes + int64_t(first_row) * (p.K / 2)),
+                                 rg = rsrc(at.w.words + int64_t(first_row & ~15) * at.w.groups);
+    uint32_t co[2], wo[2];
+    int step[2];
+    float E[2];
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+        const int row = min(nb + f * 16 + j, p.N - 1);
+        co[f] = uint32_t(row - first_row) * uint32_t(p.K / 2) + kb * 16;
+        const WordAt wa = word_at(row, p.N, at.w.groups);
+        wo[f] = uint32_t(wa.first - int64_t(first_row & ~15) * at.w.groups + (kb * 32 >> at.w.shift) * wa.step) * 2;
+        step[f] = __builtin_amdgcn_readfirstlane(wa.step * 2);      // (one run of 16 rows: one step)
+        E[f] = row_scale(at.w.exps[row]);
+    }
+    int x_plane = p.planes - 1, x_block = wk, w_block = wk, w_plane = p.planes - 1;
+    auto settle = [&](int& block, int& plane) {
+        while (block >= blocks && plane > 0) block -= blocks, --plane;
+    };
+    settle(x_block, x_plane);
+    settle(w_block, w_plane);
+    auto issue_x = [&](int stage) {
+        const __amdgpu_buffer_rsrc_t rx = rsrc(xp + x_plane * p.plane);
+        uint8_t* d = lds + stage * C::kStage + wk * C::X + wn * 1024;
+#pragma unroll
+        for (int q = 0; q < C::XL; ++q) {
+            const int r = (wn + WN * q) * 4 + lane / 16, c = lane % 16 ^ (r % 16);
+            load16_lds(rx, d + q * (WN * 1024), x_block * 128 + c * 8 < p.K ? xo[q] + c * 16 : kOutside, x_block * 256);
+        }
+        x_block += WK;
+        settle(x_block, x_plane);
+    };
+    dev::u32x4 code[D][2];
+    uint16_t word[D][2];
+    auto load_w = [&](dev::u32x4 (&c)[2], uint16_t (&g)[2]) {
+        const bool in = w_block * 128 + kb * 32 < p.K;
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            c[f] = __builtin_bit_cast(dev::u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, in ? co[f] : kOutside, w_block * 64, 2));
+            g[f] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(rg, in ? wo[f] : kOutside, (w_block * 128 >> at.w.shift) * step[f], 0));
+        }
+        w_block += WK;
+        settle(w_block, w_plane);
+    };
+    dev::f32x4 acc[MF][2];
 #pragma unroll
     for (int i = 0; i < MF; ++i)
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
-            *reinterpret_cast<dev::f32x4*>(red + (wave * C::BM + i * 16 + j) * C::kRow + f * 16 + kb * 4) = acc[i][f];
-    __syncthreads();
-    constexpr int PER = (GATE ? 4 : 8) * WN;                  // items of 4 results in a row of x
-    for (int i = tid; i < rows * PER; i += C::kThreads) {
-        const int r = i / PER, c = i % PER, cw = c / (PER / WN), col = c % (PER / WN) * 4;
-        auto sum = [&](int at) {
-            dev::f32x4 t = *reinterpret_cast<const dev::f32x4*>(red + (cw * C::BM + r) * C::kRow + at);
+        for (int f = 0; f < 2; ++f) acc[i][f] = dev::f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int k = 1; k < WK; ++k)
-                t += *reinterpret_cast<const dev::f32x4*>(red + ((k * WN + cw) * C::BM + r) * C::kRow + at);
-            return t;
-        };
-        dev::f32x4 v = sum(col);
-        const int nn = n0 + cw * 32 + col;
-        if (nn >= p.N) continue;
-        if constexpr (GATE) {
-            const dev::f32x4 up = sum(col + 16);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = gated(v[e], up[e]);
-        }
-        const int64_t to = EXPERTS ? row_out<KIND>(p, shared, base, int(r0) + r) : r0 + r;
-        if constexpr (KIND == kOut32) {
-            float* o = static_cast<float*>(p.out) + to * p.ldo + nn;
-            if (nn + 4 <= p.N) {
-                *reinterpret_cast<words4*>(o) = __builtin_bit_cast(dev::u32x4, v);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (nn + e < p.N) o[e] = v[e];
-            }
-        } else {
-            uint16_t* o = static_cast<uint16_t*>(p.out) + to * p.ldo + (GATE ? nn / 32 * 16 + nn % 16 : nn);
-            if (EXPERTS || (p.wide && nn + 4 <= p.N)) {
-                *reinterpret_cast<words2*>(o) = words2{dev::pack_bf16x2(v[0], v[1]), dev::pack_bf16x2(v[2], v[3])};
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (nn + e < p.N) o[e] = dev::f32_to_bf16_bits(v[e]);
-            }
-        }
+    for (int d = 0; d < D; ++d) {
+        issue_x(d);
+        asm volatile("" ::: "memory");
+        load_w(code[d], word[d]);
+        asm volatile("" ::: "memory");
     }
+    int stage = 0, ahead = D;
+    auto block = [&](auto slot_) {
+        constexpr int slot = decltype(slot_)::value;
+        // this block has landed, and every wave is past the one whose place the next request takes
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(wait_for((D - 1) * (C::XL + 4), 0));
+        asm volatile("" ::: "memory");
+        if constexpr (C::WN > 1) __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        issue_x(ahead);
+        const uint8_t* x = lds + stage * C::kStage + wk * C::X;
+        float s2[2], off[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const float s = word_scale(word[slot][f]) * E[f];
+            off[f] = -word_zero(word[slot][f]) * s;
+            s2[f] = s * 512.0f;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            // k of instruction q in lane block kb: 32 kb + 8 q on
+            bf16x8 fa[MF], fb[2];
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+                fa[i] = *reinterpret_cast<const bf16x8*>(x + (i * 16 + j) * 256 + ((4 * kb + q) ^ j) * 16);
+#pragma unroll
+            for (int f = 0; f < 2; ++f) fb[f] = __builtin_bit_cast(bf16x8, decode8(code[slot][f][q], s2[f], off[f]));
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) acc[i][f] = mma(fb[f], fa[i], acc[i][f]);
+        }
+        asm volatile("" ::: "memory");
+        load_w(code[slot], word[slot]);
+        stage = stage == D ? 0 : stage + 1;
+        ahead = ahead == D ? 0 : ahead + 1;
+    };
+    // (past the end blocks are zeros)
+    for (int it = 0; it < n; it += D) {
+        block(std::integral_constant<int, 0>{});
+        if constexpr (D > 1) block(std::integral_constant<int, 1 % D>{});
+        if constexpr (D > 2) block(std::integral_constant<int, 2 % D>{});
+    }
+    finish_sums<KIND, C>(p, acc, lds, at.r0, at.n0, at.base, at.shared, rows);
 }
 
 // The tile map: one workgroup, one thread an entry (513 at most).
@@ -303,33 +486,39 @@ hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done)
     return e;
 }
 
-template <int KIND, int MF, int WK, int WN, int S>
-hipError_t launch_as(const Product& p, const ExpertList* list, const void* map, int64_t max_tiles, hipStream_t s) {
-    typedef Mid<MF, WK, WN, S> C;
+template <int KIND, class C, class F>
+hipError_t launch_as(F kernel, const Product& p, const ExpertList* list, const void* map, int64_t max_tiles, hipStream_t s) {
     static const ExpertList none{};
     static std::atomic<uint64_t> allowed{0};
     const int64_t nt = (p.N + C::BN - 1) / C::BN, mt = list ? max_tiles : (p.T + C::BM - 1) / C::BM, blocks = nt * mt;
     if (blocks == 0) return hipSuccess;
     if (blocks > 0x7FFFFFFF / C::kThreads) return hipErrorInvalidValue;
-    const auto kernel = &k_i4_mid<KIND, MF, WK, WN, S>;
     const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), C::kLds, allowed);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, dim3(unsigned(blocks)), dim3(C::kThreads), C::kLds, s, p, list ? *list : none,
                        static_cast<const int4*>(map), int(nt), int(mt));
     return hipGetLastError();
 }
+template <int KIND, int MF, int WK, int WN, int S>
+hipError_t mid(const Product& p, const ExpertList* list, const void* map, int64_t max_tiles, hipStream_t s) {
+    return launch_as<KIND, Mid<MF, WK, WN, S>>(&k_i4_mid<KIND, MF, WK, WN, S>, p, list, map, max_tiles, s);
+}
+template <int KIND, int MF, int WK, int WN, int D>
+hipError_t wide(const Product& p, const ExpertList* list, const void* map, int64_t max_tiles, hipStream_t s) {
+    return launch_as<KIND, Wide<MF, WK, WN, D>>(&k_i4_wide<KIND, MF, WK, WN, D>, p, list, map, max_tiles, s);
+}
 
 template <int KIND>
 hipError_t choose(int kind, const Product& p, const ExpertList* list, const void* map, int64_t max_tiles, hipStream_t s) {
     switch (kind) {
-        case kMid32x32: return launch_as<KIND, 2, 8, 1, 3>(p, list, map, max_tiles, s);
-        case kMid64x32: return launch_as<KIND, 4, 8, 1, 2>(p, list, map, max_tiles, s);
-        case kMid128x32: return launch_as<KIND, 8, 4, 1, 2>(p, list, map, max_tiles, s);
-        case kMid64x64: return launch_as<KIND, 4, 4, 2, 3>(p, list, map, max_tiles, s);
-        case kMid128x64: return launch_as<KIND, 8, 4, 2, 2>(p, list, map, max_tiles, s);
-        case kMid32x128: return launch_as<KIND, 2, 2, 4, 4>(p, list, map, max_tiles, s);
-        case kMid64x128: return launch_as<KIND, 4, 2, 4, 3>(p, list, map, max_tiles, s);
-        case kMid128x256: return launch_as<KIND, 8, 1, 8, 3>(p, list, map, max_tiles, s);
+        case kMid32x32: return mid<KIND, 2, 8, 1, 3>(p, list, map, max_tiles, s);
+        case kMid64x32: return mid<KIND, 4, 8, 1, 2>(p, list, map, max_tiles, s);
+        case kMid128x32: return mid<KIND, 8, 4, 1, 2>(p, list, map, max_tiles, s);
+        case kMid64x64: return mid<KIND, 4, 4, 2, 3>(p, list, map, max_tiles, s);
+        case kMid128x64: return mid<KIND, 8, 4, 2, 2>(p, list, map, max_tiles, s);
+        case kMid32x128: return wide<KIND, 2, 2, 4, 2>(p, list, map, max_tiles, s);
+        case kMid64x128: return wide<KIND, 4, 1, 4, 2>(p, list, map, max_tiles, s);
+        case kMid128x256: return wide<KIND, 8, 1, 8, 1>(p, list, map, max_tiles, s);
         default: return hipErrorInvalidValue;
     }
 }

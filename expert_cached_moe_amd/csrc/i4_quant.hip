@@ -50,6 +50,7 @@ __global__ __launch_bounds__(kThreads) void k_i4_quantize(const E* __restrict__ 
     const int tid = threadIdx.x, pieces = cols / 32, per = group / 32, groups = (pieces + per - 1) / per;
     const E* xr = x + row * ld;
     const double steps = zero ? 15.0 : 7.0;
+    const WordAt at = word_at(row, gridDim.x, groups);
     bool bad = false;
     auto read = [&](int p, float (&v)[32]) {
 #pragma unroll
@@ -109,7 +110,7 @@ __global__ __launch_bounds__(kThreads) void k_i4_quantize(const E* __restrict__ 
         }
         if (p < pieces) {
             *reinterpret_cast<uint4*>(q + row * (cols / 2) + p * 16) = make_uint4(c[0], c[1], c[2], c[3]);
-            if (p % per == 0) words[row * groups + p / per] = uint16_t(s | uint32_t(z) << 8);
+            if (p % per == 0) words[at.first + int64_t(p / per) * at.step] = uint16_t(s | uint32_t(z) << 8);
         }
     }
 }

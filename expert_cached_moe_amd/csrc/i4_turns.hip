@@ -131,7 +131,8 @@ k_i4_turns(const Product p, const ExpertList list, const int4* __restrict__ map,
     const int half_b = tid % 2, br = tid / 2;
     const int64_t nb = min(n0 + br, p.N - 1);
     const uint8_t* codes = w.codes + nb * (p.K / 2) + half_b * 16;
-    const uint16_t* words = w.words + nb * w.groups;
+    const WordAt wa = word_at(nb, p.N, w.groups);
+    const uint16_t* words = w.words + wa.first;
     const float S = row_scale(w.exps[nb]);
     // (words are widened where they are used, so that their loads stay in flight)
     dev::u32x4 code[2];                                       // of slices of even and odd number
@@ -140,7 +141,7 @@ k_i4_turns(const Product p, const ExpertList list, const int4* __restrict__ map,
     auto load_w = [&](dev::u32x4& code, uint16_t& word) {
         const int k = min(slice_w * 64 + half_b * 32, p.K - 32);       // (past K: any codes; not used)
         code = *reinterpret_cast<const dev::u32x4*>(codes + (k - half_b * 32) / 2);
-        word = words[k >> w.shift];
+        word = words[(k >> w.shift) * wa.step];
         if (++slice_w == slices) slice_w = 0;
     };
     float s2 = 0, off = 0;

@@ -474,7 +474,9 @@ int moe_i8_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob8, vo
  *   weight[k] = 2^(exp - 127) * s * (code[k] - z)
  * with codes 0..15 (element 2i in the low half of byte i), one exponent byte per row (255: NaN), and
  * for each group of 32, 64 or 128 along K (the last one may be shorter) one 16-bit word: the low byte
- * is s, an e4m3 number (OCP FP8, NaN 0x7F), the high byte the zero point z, 0..15.  The scale s has
+ * is s, an e4m3 number (OCP FP8, NaN 0x7F), the high byte the zero point z, 0..15.  The words lie by runs of 16
+ * rows (the last run has the rows that are left): behind the 16 r * groups words of earlier runs those of run r, group by
+ * group, the words of a group's rows side by side; the codes and exponents row by row.  The scale s has
  * four significant bits and code - z four, so each weight is exact in bf16, and the products below are
  * products with these weights: nothing is rounded before the sums.  Activations stay as they are.
  *
@@ -488,7 +490,7 @@ int moe_i8_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob8, vo
  * z = 8 and codes 8 (zeros); a row whose power of two would be below 2^-100 is zeros with exp 0; a row
  * that holds a NaN or a magnitude of 2^120 or more has exp 255, so every product with it is NaN.
  *   d_x: MOE_A_F32 or MOE_A_BF16, rows ld_x >= cols elements apart, any alignment of the element;
- *   d_q [rows][cols / 2] 16-byte aligned, d_words [rows][ceil(cols / group)], d_exps [rows];
+ *   d_q [rows][cols / 2] 16-byte aligned, d_words rows * ceil(cols / group) words, d_exps [rows];
  *   cols a multiple of 32 up to 2^20, rows up to 2^23.  rows == 0 is a no-op.
  * Errors: MOE_EINVAL (null, type, group, ld_x < cols, alignment), MOE_ESHAPE (cols, rows). */
 int moe_i4_quantize(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, int32_t rows, int32_t cols, int32_t group,
@@ -500,7 +502,7 @@ int64_t moe_i4_workspace_bytes(int32_t max_T, int32_t N, int32_t K);
  *   d_x: MOE_A_F32 or MOE_A_BF16, rows ld_x >= K elements apart, any alignment of the element (bf16 rows
  *     that start on 16 bytes each are read as they are, others are laid out in the workspace first; fp32
  *     numbers enter the matrix cores as three bf16 parts that add up to them);
- *   d_w [N][K / 2] (16-byte aligned), d_words [N][ceil(K / group)], d_exps [N] as moe_i4_quantize makes
+ *   d_w [N][K / 2] (16-byte aligned), d_words, d_exps [N] as moe_i4_quantize makes
  *     them; any codes and words are taken (a zero point above 15 rounds the weights to bf16, scales
  *     2^(exp - 127) s from 2^119 on overflow);
  *   d_y [T][N], rows ld_y >= N elements apart, MOE_A_F32 or MOE_A_BF16; bytes between the rows are not

@@ -76,6 +76,15 @@ def unpack(q):
     return np.stack([q & 15, q >> 4], 2).reshape(q.shape[0], -1)
 
 
+def lay_words(words):
+    """Words [N][groups] as the library holds them: by runs of 16 rows, in each group by group."""
+    return np.concatenate([words[r:r + 16].T.ravel() for r in range(0, len(words), 16)])
+
+
+def unlay_words(flat, N, groups):
+    return np.concatenate([flat[r * groups:min(r + 16, N) * groups].reshape(groups, -1).T for r in range(0, N, 16)])
+
+
 def scales(words, exps, group, K):
     """(s * S spread over K, z spread over K)."""
     s = np.where(words & 0x80, -1.0, 1.0) * np.concatenate([E4M3, [np.nan]])[words & 0x7F]

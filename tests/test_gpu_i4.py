@@ -48,7 +48,7 @@ class Weights:
         self.parts = (self.codes, self.words, self.exps)
 
     def upload(self):
-        return u8(Q.pack(self.codes)), u8(self.words.view(np.int16)), u8(self.exps)
+        return u8(Q.pack(self.codes)), u8(Q.lay_words(self.words).view(np.int16)), u8(self.exps)
 
 
 # ------------------------------------------------------------------ quantisation
@@ -62,7 +62,7 @@ def quantize(ctx, x, t, ld, rows, cols, group, zero):
     torch.cuda.synchronize()
     assert (q[rows * cols // 2:] == 0x5A).all() and (w[rows * n:] == 0x5A5A).all() and (e[rows:] == 0x5A).all()
     return (Q.unpack(q[:rows * cols // 2].cpu().numpy().reshape(rows, -1)),
-            w[:rows * n].cpu().numpy().view(np.uint16).reshape(rows, n), e[:rows].cpu().numpy())
+            Q.unlay_words(w[:rows * n].cpu().numpy().view(np.uint16), rows, n), e[:rows].cpu().numpy())
 
 
 def same(a, b):
@@ -258,7 +258,8 @@ def test_offsets_past_2_gib_and_4_gib(ctx):
     w.N, w.K, w.group = N, K, group
     rows = [0, 1, 32767, 32768, 65535, 65536, 65999]
     at = torch.tensor(rows, device="cuda")
-    parts = (Q.unpack(q.view(N, K // 2)[at].cpu().numpy()), words[at].cpu().numpy().view(np.uint16), exps[at].cpu().numpy())
+    words_of = words.view(N // 16, K // group, 16)[at // 16, :, at % 16]
+    parts = (Q.unpack(q.view(N, K // 2)[at].cpu().numpy()), words_of.cpu().numpy().view(np.uint16), exps[at].cpu().numpy())
     for T in (1, 20):
         x, ref = numbers((T, K), 3, BF16)
         got = product(ctx, x, BF16, K, T, w, (q, words, exps), F32)

@@ -145,3 +145,11 @@ def test_every_weight_is_exact_in_bf16_and_near_what_it_stands_for(group, zero):
     # where s is 0 the group is below half the least step
     assert (np.abs(v - x) <= np.where(s > 0, s * (1.0 if zero else 0.5), np.abs(x)) * (1 + 2.0 ** -40)).all()
     assert (Q.unpack(Q.pack(c)) == c).all()
+    assert (Q.unlay_words(Q.lay_words(w), *w.shape) == w).all()
+
+
+def test_words_lie_by_runs_of_16_rows():
+    w = np.arange(37 * 3).reshape(37, 3)
+    flat = Q.lay_words(w)
+    assert flat[:3].tolist() == [0, 3, 6] and flat[16] == 1 and flat[48] == w[16, 0] and flat[96:101].tolist() == w[32:, 0].tolist()
+    assert flat[101] == w[32, 1] and flat[-1] == w[36, 2]
