@@ -518,7 +518,7 @@ hipError_t choose(int kind, const Product& p, const ExpertList* list, const void
         case kMid128x64: return mid<KIND, 8, 4, 2, 2>(p, list, map, max_tiles, s);
         case kMid32x128: return wide<KIND, 2, 2, 4, 2>(p, list, map, max_tiles, s);
         case kMid64x128: return wide<KIND, 4, 1, 4, 2>(p, list, map, max_tiles, s);
-        case kMid128x256: return wide<KIND, 8, 1, 8, 1>(p, list, map, max_tiles, s);
+        case kMid128x128: return wide<KIND, 8, 1, 4, 1>(p, list, map, max_tiles, s);
         default: return hipErrorInvalidValue;
     }
 }

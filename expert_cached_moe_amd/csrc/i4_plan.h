@@ -14,19 +14,20 @@ constexpr int kFewTokens = 8;
 
 // The kernels for more rows: tiles of `rows` of x by `cols` of the weights, K split over `split` groups of waves,
 // `slots` workgroups a CU.  A slice of 64 k takes `one` us with one workgroup on each CU and `full` with all.
-// Measured on bf16 x (dense, whole kernel): 4096 x 4096 at 32 rows 9.3 us on 32 x 32 tiles (the next best 17), at 64 11.7
-// on 64 x 32 (17.9 on 64 x 64), at 128 19 on 128 x 32 (26 on 128 x 64), at 512 39 on 128 x 64 (51 on 64 x 64, 103 on 256 x
-// 256); 4096 x 12288 at 128 rows 50 on 128 x 32 against 82; 100003 x 4096 at 32 rows 93 on 32 x 128 (135 on 32 x 32), at 64
-// 106 on 64 x 128, at 256 243 on 256 x 256 (302 on 128 x 256).  `full` of the largest is that of a chip at its power limit.
+// Measured on bf16 x (dense, whole kernel): 4096 x 4096 at 32 rows 8.6 us on 32 x 32 tiles (17 on 128 x 32 and 64 x 64),
+// at 128 11.1 on 64 x 32 (17.3 on 128 x 32), at 512 28 on 128 x 64 (34 on 128 x 32, 102 on 256 x 256); 4096 x 12288 at 256
+// rows 48 on 128 x 32 (77 on 128 x 64); 16384 x 4096 at 1024 rows 121 on 256 x 256 (180 on 128 x 128); 100003 x 4096 at 32
+// rows 77 on 32 x 128 (98 on 64 x 128, 111 on 32 x 32), at 64 105 on 64 x 128 (140), at 128 161 on 128 x 128 (190), at 256
+// 249 on 256 x 256 (309).  `full` of the largest is that of a chip at its power limit.
 struct Kind {
     int rows, cols, split, slots;
     double one, full;
 };
-enum { kMid32x32, kMid64x32, kMid128x32, kMid64x64, kMid128x64, kMid32x128, kMid64x128, kMid128x256, kTurns, kKinds };
+enum { kMid32x32, kMid64x32, kMid128x32, kMid64x64, kMid128x64, kMid32x128, kMid64x128, kMid128x128, kTurns, kKinds };
 constexpr Kind kKind[kKinds] = {
-    {32, 32, 8, 1, 1.08, 1.08},  {64, 32, 8, 1, 1.55, 1.55},   {128, 32, 4, 1, 0.97, 0.97},
-    {64, 64, 4, 1, 1.15, 1.15},  {128, 64, 4, 1, 1.75, 1.75},  {32, 128, 2, 2, 0.83, 1.45},
-    {64, 128, 2, 2, 0.98, 1.65}, {128, 256, 1, 2, 1.07, 2.30}, {256, 256, 1, 1, 1.50, 1.90},
+    {32, 32, 8, 1, 0.87, 0.87},  {64, 32, 8, 1, 1.10, 1.15},  {128, 32, 4, 1, 0.95, 0.95},
+    {64, 64, 4, 1, 1.00, 1.00},  {128, 64, 4, 1, 1.45, 1.45}, {32, 128, 2, 3, 0.57, 1.80},
+    {64, 128, 1, 3, 0.48, 1.20}, {128, 128, 1, 2, 0.95, 1.27}, {256, 256, 1, 1, 1.48, 1.93},
 };
 // Time of `tiles` row tiles over N weight rows of K, `slices` walks of 64 k each.
 inline double kind_time(int kind, double tiles, int64_t N, int64_t slices, int n_cu) {
