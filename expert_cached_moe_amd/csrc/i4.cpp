@@ -227,7 +227,7 @@ int moe_i4_expert_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const int32_t* d
     p.shared = with_shared ? static_cast<const uint8_t*>(d_shared) - base : 0;
     const int64_t pairs = int64_t(T) * c.top_k, rows = (n > 0 ? pairs : 0) + (with_shared ? T : 0);
     const int n_cu = dense::compute_units();
-    const bool few = few_experts(n, T, pairs, with_shared);
+    const bool few = T <= kFewTokens;
     int built = 0;                                            // rows of the tiles that the map in the workspace lists
     auto product = [&](int what) {
         if (few) return launch_i4_few(what, p, &list, s);

@@ -10,13 +10,14 @@
 // multiply-adds add that, times s, to the sums.  So a code takes 1.2 operations of a lane for up to 4 tokens
 // and 1.4 for 8, of the 3.3 that there is time for; scaling every weight would take 2.4.
 //
-// The waves of a workgroup split K (by chunks of 512) and, where K is short, rows too; sums meet once a
+// The waves of a workgroup split K (by chunks of 512); sums meet once a
 // unit of rows, across the blocks in registers, across the waves in LDS, in a fixed order.  Every tile's
 // registers are loaded again as soon as it is used, with the next chunk or the next unit of rows, so
 // the stream does not stop between units.
 //
-// Experts: each workgroup lists the entries that have rows, from the offsets, in blocks of 8 rows at most, and walks
-// their units; whether a block has more than 4 rows decides the code that its units run.
+// Experts: each workgroup lists the entries that have rows, from the offsets, in blocks of 4 rows at most, and walks their
+// units.  Blocks of 8 cost more registers, so waves, for the few entries that fill them (256 experts of 4096 x 1536 with
+// the shared one, top 6, 8 tokens: 157 us against 118; 128 of 2048 x 768, top 8: 48.5 and 48.9).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -34,6 +35,7 @@ using dev::kWave;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 
 constexpr int kChunk = 512, kMaxWaves = 8, kStream = 2;       // cache policy of a non-temporal load
+constexpr int kFewBlocks = kFewTokens * kMaxTopK + 2;          // of up to 4 rows: a block a pair at most, the shared expert's two
 // The row's power of two comes last; until then sums are held 2^-32 times as large, in range whatever x is.
 constexpr float kDown32 = 2.3283064365386963e-10f;
 constexpr uint32_t kOutside = 0xFFFFFFF0u, kRange = 0x80000000u;
@@ -72,8 +74,8 @@ __device__ __forceinline__ float scaled(float sum, uint32_t e) {
 }
 
 struct Few {
-    int kw, rw;              // waves along K, and along rows
-    int strips;              // of an entry: runs of 4 R rows (gated: 2 R gate rows and their up rows)
+    int kw;                  // waves along K
+    int units;               // of an entry: runs of 4 R rows (gated: 2 R gate rows and their up rows)
     int entries;             // dense: runs of 4 MT tokens; experts: entries of the list
 };
 
@@ -92,9 +94,8 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
     __shared__ int s_waves[kMaxWaves];
     extern __shared__ __attribute__((aligned(16))) float red[];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
-    const int rw = wave / f.kw, kw = wave % f.kw;
     const int j = lane % 4, block = lane / 4;
-    const int units = (f.strips + f.rw - 1) / f.rw, chunks = (p.K + kChunk - 1) / kChunk, passes = (chunks + f.kw - 1) / f.kw;
+    const int units = f.units, chunks = (p.K + kChunk - 1) / kChunk, passes = (chunks + f.kw - 1) / f.kw;
     const int pieces = p.K / 32;
 
     int total = f.entries * units;
@@ -150,33 +151,32 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
             return Entry{0, t0, int(p.T) - t0 < 4 * MAXMT ? int(p.T) - t0 : 4 * MAXMT, false};
         }
     };
-    auto strip_of = [&](int u) { return u % units * f.rw + rw; };
-    // first row of a strip, and row of tile r from there
-    auto first_row = [](int strip) {
-        return GATE ? strip / (8 / R) * 32 + strip % (8 / R) * (2 * R) : strip * (4 * R);
+    // first row of a unit, and row of tile r from there
+    auto first_row = [](int unit) {
+        return GATE ? unit / (8 / R) * 32 + unit % (8 / R) * (2 * R) : unit * (4 * R);
     };
     auto tile_row = [](int r) { return GATE ? r / (R / 2) * 16 + r % (R / 2) * 4 : r * 4; };
 
     dev::u32x4 w[R];
     uint32_t word[R];
     __amdgpu_buffer_rsrc_t rc = rsrc(p.w.codes), rg = rsrc(p.w.words);
-    uint32_t first = 0, left = 0;                               // first row of the strip, and rows behind it
+    uint32_t first = 0, left = 0;                               // first row of the unit, and rows behind it
     auto aim = [&](int u) {
         const Entry e = entry_of(u);
-        const int strip = strip_of(u), n0 = first_row(strip < f.strips ? strip : f.strips - 1);
+        const int n0 = first_row(u % units);
         const Rows rows = rows_at(p.w, e.offset);
         rc = rsrc(rows.codes + int64_t(n0) * (p.K / 2));
         rg = rsrc(rows.words + int64_t(n0 & ~15) * p.w.groups);
         first = uint32_t(n0);
         left = uint32_t(p.N - 1 - n0);
     };
-    // (from the first word of the strip's run of 16 rows)
+    // (from the first word of the unit's run of 16 rows)
     auto word_of = [&](uint32_t row, uint32_t group) {
         const uint32_t n = first + row, run = n & ~15u, rest = uint32_t(p.N) - run;
         return (run - (first & ~15u)) * uint32_t(p.w.groups) + group * (rest < 16 ? rest : 16u) + (n - run);
     };
     auto load = [&](int r, int pass) {
-        const int piece = (pass * f.kw + kw) * 16 + block;
+        const int piece = (pass * f.kw + wave) * 16 + block;
         const uint32_t row = min(uint32_t(tile_row(r) + j), left);
         const bool in = piece < pieces;
         w[r] = __builtin_bit_cast(dev::u32x4, __builtin_amdgcn_raw_buffer_load_b128(
@@ -217,18 +217,17 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
         }
         // results: a thread's items are a row each (gated: a gate row) of one token
         constexpr int ROWS = GATE ? 2 * R : 4 * R, ITEMS = ROWS * MT * 4;
-        const int items = ITEMS * f.rw, threads = blockDim.x;
+        const int threads = blockDim.x;
         struct Item {
             int n, t, at, up;                                   // row of the weights, token, places in the sums
             bool live;
         };
         auto item = [&](int q) {
-            const int i = q * threads + tid, row = i % (ROWS * f.rw), t = i / (ROWS * f.rw);
-            const int strip = u % units * f.rw + row / ROWS, in = row % ROWS, tile = in / 4;
-            const int n = first_row(strip) + tile_row(tile) + in % 4;
+            const int i = q * threads + tid, row = i % ROWS, t = i / ROWS, tile = row / 4;
+            const int n = first_row(u % units) + tile_row(tile) + row % 4;
             const int v = ((t / 4) * R + tile) * 4 + t % 4;     // of tile's value; its up row's: R / 2 tiles on
-            auto place = [&](int v) { return (row / ROWS * f.kw) * (V * 4) + (v / Q * 4 + in % 4) * Q + v % Q; };
-            return Item{n, t, place(v), place(v + 2 * R), i < items && t < e.count && strip < f.strips && n < p.N};
+            auto place = [&](int v) { return (v / Q * 4 + row % 4) * Q + v % Q; };
+            return Item{n, t, place(v), place(v + 2 * R), i < ITEMS && t < e.count && n < p.N};
         };
         // what finishing an item reads: its rows' exponents, and its row of out
         struct Needs {
@@ -246,7 +245,7 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
         };
         Needs first{0, 0, 0};
         for (int pass = 0; pass < passes; ++pass) {
-            const int piece = (pass * f.kw + kw) * 16 + block;
+            const int piece = (pass * f.kw + wave) * 16 + block;
             if (fresh || passes > 1) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
@@ -328,7 +327,7 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
         // (the other area's readers are past it: they met at the barrier before this one)
         lds_barrier();
         ++turn;
-        for (int q = 0; q * threads < items; ++q) {
+        for (int q = 0; q * threads < ITEMS; ++q) {
             const Item i = item(q);
             if (!i.live) continue;
             const Needs n = q == 0 ? first : needs(i);
@@ -366,33 +365,33 @@ template <int KIND, int MAXMT, int R, int P>
 hipError_t launch_as(const Product& p, const ExpertList* list, hipStream_t s) {
     static const ExpertList none{};
     const int n_cu = dense::compute_units();
-    const int chunks = (p.K + kChunk - 1) / kChunk, strip_rows = 4 * R;
+    const int chunks = (p.K + kChunk - 1) / kChunk;
     Few f;
     // waves along K: all of a row in one pass where there are enough
     f.kw = chunks < kMaxWaves ? chunks : kMaxWaves;
-    f.rw = 1;
-    f.strips = int((int64_t(p.N) + strip_rows - 1) / strip_rows);
-    f.entries = list ? list->n : int((p.T + 4 * MAXMT - 1) / (4 * MAXMT));
-    const int per_cu = std::max(1, 4 * kWavesPerSimd<MAXMT, P> / (f.kw * f.rw));
-    const int64_t units = int64_t((f.strips + f.rw - 1) / f.rw) * (list ? std::min<int64_t>(kFewBlocks, list->n + p.T * (p.top_k + 1) / (4 * MAXMT)) : f.entries);
+    f.units = int((int64_t(p.N) + 4 * R - 1) / (4 * R));
+    f.entries = list ? 0 : int((p.T + 4 * MAXMT - 1) / (4 * MAXMT));
+    const int per_cu = std::max(1, 4 * kWavesPerSimd<MAXMT, P> / f.kw);
+    const int64_t units = int64_t(f.units) * (list ? std::min<int64_t>(2 * list->n, p.T * p.top_k + 2) : f.entries);
     const int64_t grid = std::min<int64_t>(units, int64_t(n_cu) * per_cu);
     const int lds = 2 * kMaxWaves * R * MAXMT * 16 * 4;
-    hipLaunchKernelGGL((k_i4_few<KIND, MAXMT, R, P>), dim3(unsigned(grid)), dim3(f.kw * f.rw * kWave), lds, s, p,
+    hipLaunchKernelGGL((k_i4_few<KIND, MAXMT, R, P>), dim3(unsigned(grid)), dim3(f.kw * kWave), lds, s, p,
                        list ? *list : none, f);
     return hipGetLastError();
 }
 
 template <int KIND, int P>
 hipError_t choose(const Product& p, const ExpertList* list, hipStream_t s) {
-    if (p.T <= 4) return launch_as<KIND, 1, 4, P>(p, list, s);
-    return launch_as<KIND, 2, 4, P>(p, list, s);
+    if constexpr (KIND == kOut16 || KIND == kOut32)
+        if (p.T > 4) return launch_as<KIND, 2, 4, P>(p, list, s);
+    return launch_as<KIND, 1, 4, P>(p, list, s);
 }
 
 }  // namespace
 
 hipError_t launch_i4_few(int kind, const Product& p, const ExpertList* list, hipStream_t s) {
     if (p.T == 0) return hipSuccess;
-    if (!list && p.T > kFewTokens) return hipErrorInvalidValue;
+    if (p.T > kFewTokens) return hipErrorInvalidValue;
     const bool parts = p.planes == 3;
     switch (kind) {
         case kOut16: return parts ? choose<kOut16, 3>(p, nullptr, s) : choose<kOut16, 1>(p, nullptr, s);

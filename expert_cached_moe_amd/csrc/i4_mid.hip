@@ -381,7 +381,7 @@ k_i4_wide(const Product p, const ExpertList list, const int4* __restrict__ map, 
         const bool in = w_block * 128 + kb * 32 < p.K;
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-            c[f] = __builtin_bit_cast(dev::u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, in ? co[f] : kOutside, w_block * 64, 2));
+            c[f] = __builtin_bit_cast(dev::u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, in ? co[f] : kOutside, w_block * 64, 0));
             g[f] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(rg, in ? wo[f] : kOutside, (w_block * 128 >> at.w.shift) * step[f], 0));
         }
         w_block += WK;
@@ -516,7 +516,7 @@ hipError_t choose(int kind, const Product& p, const ExpertList* list, const void
         case kMid128x32: return mid<KIND, 8, 4, 1, 2>(p, list, map, max_tiles, s);
         case kMid64x64: return mid<KIND, 4, 4, 2, 3>(p, list, map, max_tiles, s);
         case kMid128x64: return mid<KIND, 8, 4, 2, 2>(p, list, map, max_tiles, s);
-        case kMid32x128: return wide<KIND, 2, 2, 4, 2>(p, list, map, max_tiles, s);
+        case kMid32x128: return wide<KIND, 2, 1, 4, 2>(p, list, map, max_tiles, s);
         case kMid64x128: return wide<KIND, 4, 1, 4, 2>(p, list, map, max_tiles, s);
         case kMid128x128: return wide<KIND, 8, 1, 4, 1>(p, list, map, max_tiles, s);
         default: return hipErrorInvalidValue;
