@@ -79,7 +79,10 @@ WsLayout ws_layout(const moe_config& c, int32_t max_T) {
     const int64_t Td = T < kDecodeMaxT ? T : kDecodeMaxT;
     const int64_t rows_d = Td * c.top_k + (c.n_shared ? Td : 0);
     W.o = align256(W.h + rows * int64_t(c.inter) * act_bytes(c));
-    W.bytes = align256(W.o + rows_d * int64_t(c.hidden) * act_bytes(c));
+    W.scored = align256(W.o + rows_d * int64_t(c.hidden) * act_bytes(c));
+    // 16-bit counts of the router by scores, a row for each workgroup (no more of them for any smaller number of tokens)
+    const int64_t groups = scored_alone(T, c.top_k) ? 0 : T <= 1024 ? (T + 3) / 4 : T <= (int64_t(256) << 15) ? 256 : 512;
+    W.bytes = align256(W.scored + groups * ((c.n_experts + 3) / 4 * 8));
     return W;
 }
 
@@ -255,7 +258,7 @@ int moe_route_scored(moe_ctx* ctx, const float* d_logits, const float* d_bias, i
     if (!d_counts || !d_offsets) return fail(ctx, MOE_EINVAL, "null counts/offsets");
     if (T > 0 && (!d_logits || !d_topk_ids || !d_topk_w || !d_perm || !d_inv))
         return fail(ctx, MOE_EINVAL, "null route buffer");
-    if (int64_t(T) * ctx->cfg.top_k > kSmallScored && !d_ws)
+    if (!scored_alone(T, ctx->cfg.top_k) && !d_ws)
         return fail(ctx, MOE_EINVAL, "workspace required for this T");
     hipError_t e = launch_route_scored(ctx->cfg, *rule, d_logits, d_bias, T, d_topk_ids, d_topk_w, d_counts, d_offsets,
                                        d_perm, d_inv, d_ws, s);

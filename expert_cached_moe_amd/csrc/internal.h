@@ -21,7 +21,6 @@ constexpr int kDecodeMaxT = 8;         // T <= 8: batched GEMV path; larger T: g
 constexpr int kSharedTag = 1023;       // list entry tag of the shared expert
 constexpr int kPermChunk = 1024;       // pairs per permutation chunk (one workgroup)
 constexpr int kSmallRouteMaxPairs = 4096;  // fused route+permute in one workgroup up to here
-constexpr int kSmallScored = 512;      // the same for the router by scores
 
 inline int64_t align256(int64_t v) { return (v + 255) & ~int64_t(255); }
 
@@ -44,10 +43,19 @@ inline int act_bytes(const moe_config& c) { return c.w_dtype == MOE_W_F32 ? 4 : 
 // GEMM's tile list; h: SwiGLU activations; o: decode pair outputs of moe_expert_ffn_merge
 // when its down projection and merge run as separate kernels.
 struct WsLayout {
-    int64_t hist = 0, base = 0, tiles = 0, h = 0, o = 0, bytes = 0;
+    int64_t hist = 0, base = 0, tiles = 0, h = 0, o = 0, scored = 0, bytes = 0;
 };
 int64_t gemm_tile_ints(const moe_config& c, int32_t T);  // tile-list entries of the grouped GEMM
 WsLayout ws_layout(const moe_config& c, int32_t max_T);
+// The router by scores: one workgroup without scratch takes a wave's tokens each (64 tokens, top 1: 16.8 us where several
+// workgroups and the second launch take 10; 9 tokens, top 8: 10.7 and 9.4).
+inline bool scored_alone(int64_t T, int k) { return T <= 16 && T * k <= 64; }
+// Tokens of a workgroup otherwise: 256 workgroups at most, 4 tokens and with more than 256 of them 8 (256 experts, top 8:
+// 128 tokens 10.5 us, 10.8 with 8; 1,024 tokens 15.0 and 13.2, 16.3 with 16), and counts that fit 16 bits.
+inline int32_t scored_each(int32_t T) {
+    const int32_t whole = T <= 256 ? 4 : 8, each = (T / 256 + (T % 256 ? 1 : 0) + whole - 1) / whole * whole;
+    return each < 32768 ? each : 32768;
+}
 
 // A small persistent worker pool for the host FFN.
 class ThreadPool {

@@ -220,7 +220,7 @@ int moe_route(moe_ctx* ctx, const float* d_logits, int32_t T, int32_t* d_topk_id
  * s, c and the groups' values are 64-bit numbers, so that the choice does not depend on fp32's
  * rounding of a score; gates are rounded once to fp32.  cfg.renormalize has no part in it.
  *   d_logits [T][E] fp32; d_bias [E] fp32 or NULL; the rest as moe_route (d_ws: moe_workspace_bytes,
- *   needed for T*k > 512).  Infinite negative logits and biases are taken (score 0; chosen last).
+ *   needed for T > 16 and for T*k > 64).  Infinite negative logits and biases are taken (score 0; chosen last).
  *   NaNs and positive infinities: that token's ids are distinct and in range, their order and its
  *   gates are not specified; other tokens are as they would be.
  * T == 0 is a valid no-op (counts and offsets are written).  Errors: MOE_EINVAL (null, T < 0, a rule

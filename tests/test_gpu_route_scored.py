@@ -82,12 +82,16 @@ def cuda(a):
     return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()
 
 
-# T, E, k, groups, keep, top: every number of experts a lane (1, 2, 4, 8, 16), with and without groups; the three
-# launch forms (up to 64 pairs, up to 512, more); E that fill no wave; whole groups of one expert
+# T, E, k, groups, keep, top: every number of experts a lane, of waves (1, 2, 4, 8, 16), of 16 lanes (4, 8, 12, 16) and of 32
+# (above 2,048 tokens), with and without groups; one workgroup (16 tokens and 64 pairs) and several, of 4, 8 and more
+# than 64 tokens; E that fill no wave; whole groups of one expert
 SHAPES = [(1, 1, 1, 1, 1, 1), (1, 8, 2, 1, 1, 1), (4, 256, 8, 8, 4, 2), (3, 512, 16, 1, 1, 1), (1, 512, 16, 1, 1, 2),
           (64, 64, 1, 64, 33, 2), (5, 495, 12, 33, 20, 2), (30, 500, 10, 5, 2, 2), (63, 141, 6, 3, 1, 1),
           (129, 160, 8, 8, 3, 2), (700, 128, 8, 1, 1, 1), (515, 256, 8, 8, 4, 2), (1021, 141, 6, 1, 1, 1),
-          (333, 510, 7, 17, 9, 1), (200, 65, 3, 13, 13, 2), (97, 12, 4, 2, 1, 2), (640, 7, 7, 7, 7, 1)]
+          (333, 510, 7, 17, 9, 1), (200, 65, 3, 13, 13, 2), (97, 12, 4, 2, 1, 2), (640, 7, 7, 7, 7, 1),
+          (17, 9, 1, 3, 2, 1), (256, 24, 2, 1, 1, 1), (257, 24, 3, 2, 1, 2), (2049, 64, 1, 1, 1, 1), (2051, 128, 8, 1, 1, 1),
+          (2050, 141, 6, 1, 1, 1), (4099, 256, 8, 8, 4, 2), (2100, 300, 5, 1, 1, 1), (2053, 512, 3, 32, 9, 2), (2060, 504, 4, 9, 5, 2),
+          (2070, 48, 16, 16, 16, 2), (20001, 32, 2, 4, 2, 1)]
 
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
@@ -115,7 +119,7 @@ def test_prefill_chunk(kind):
     r.check_gradient(logits, ids, dw)
 
 
-@pytest.mark.parametrize("T", [2, 40, 300])
+@pytest.mark.parametrize("T", [2, 40, 300, 2101])
 @pytest.mark.parametrize("kind,groups", [("softmax", 1), ("sigmoid", 1), ("sigmoid", 4)])
 def test_equal_values_take_the_lower_id(T, kind, groups):
     """All equal; few distinct values; zeros of both signs."""
@@ -129,10 +133,11 @@ def test_equal_values_take_the_lower_id(T, kind, groups):
             r.check(logits, bias)
 
 
-def test_values_that_fp32_does_not_tell_apart():
+@pytest.mark.parametrize("T", [6, 70, 2102])
+def test_values_that_fp32_does_not_tell_apart(T):
     """Equal logits and biases 2^-25 apart around 1/4: the biased scores differ by less than the upper
     32 bits of a 64-bit number show, some by less than fp32's rounding of 3/4."""
-    E, k, T = 64, 8, 70
+    E, k = 64, 8
     rng = np.random.default_rng(1)
     bias = (0.25 + rng.permutation(E) * 2.0 ** -25).astype(np.float32)
     logits = np.zeros((T, E), np.float32)
@@ -145,9 +150,10 @@ def test_values_that_fp32_does_not_tell_apart():
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [0, 1])
 @pytest.mark.parametrize("biased", [0, 1])
-def test_masked_experts_and_rows_without_any(kind, renorm, biased):
+@pytest.mark.parametrize("T", [12, 40, 2103])
+def test_masked_experts_and_rows_without_any(T, kind, renorm, biased):
     """Logits of -infinity score 0 and come last; a row of nothing else has gates 0; large logits saturate."""
-    T, E, k = 40, 32, 4
+    E, k = 32, 4
     logits, bias, dw = draw(T, E, 9, biased, k)
     rng = np.random.default_rng(2)
     logits[rng.random((T, E)) < 0.7] = -np.inf
@@ -175,7 +181,7 @@ def test_masked_by_the_bias():
         r.check(logits, bias)
 
 
-@pytest.mark.parametrize("T", [6, 50, 600])
+@pytest.mark.parametrize("T", [6, 50, 600, 2104])
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 def test_a_token_with_nans_keeps_to_itself(T, kind):
     E, k = 40, 8
@@ -246,7 +252,7 @@ def test_agrees_with_the_softmax_router():
         assert np.abs(g[:n].cpu().numpy().reshape(T, k) / w - 1).max() < 140 * 2.0 ** -24
 
 
-@pytest.mark.parametrize("T", [4, 60, 700])
+@pytest.mark.parametrize("T", [4, 60, 700, 2500])
 def test_on_another_stream_and_in_a_graph(T):
     """Replays on new inputs, with eager calls and other work between them."""
     E, k = 96, 4
