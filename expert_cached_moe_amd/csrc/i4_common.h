@@ -9,6 +9,31 @@ namespace i4 {
 
 typedef __attribute__((ext_vector_type(2))) float f32x2;
 
+// The list of experts that a kernel takes (its 2 KB are copied at each launch): dense kernels have none.
+struct NoList {};
+template <int KIND>
+struct ListType {
+    using Type = NoList;
+};
+template <>
+struct ListType<kGateUp> {
+    using Type = ExpertList;
+};
+template <>
+struct ListType<kDown> {
+    using Type = ExpertList;
+};
+template <int KIND>
+using ListOf = typename ListType<KIND>::Type;
+template <int KIND>
+const ListOf<KIND>& list_of(const ExpertList* list) {
+    static const NoList none{};
+    if constexpr (KIND == kGateUp || KIND == kDown)
+        return *list;
+    else
+        return none;
+}
+
 // A group's word: s, and its zero point.  (Bytes as e4m3 numbers: 0..15 are 2^-9 times themselves,
 // the subnormal numbers and the first binade, so the conversion instructions turn codes into numbers.)
 __device__ __forceinline__ float word_scale(uint32_t w) { return __builtin_amdgcn_cvt_f32_fp8(int(w), 0); }

@@ -88,7 +88,7 @@ struct Entry {
 
 template <int KIND, int MAXMT, int R, int P>
 __global__ void __launch_bounds__(kMaxWaves* kWave) __attribute__((amdgpu_waves_per_eu(kWavesPerSimd<MAXMT, P>)))
-k_i4_few(const Product p, const ExpertList list, const Few f) {
+k_i4_few(const Product p, const ListOf<KIND> list, const Few f) {
     constexpr bool GATE = KIND == kGateUp, EXPERTS = KIND == kGateUp || KIND == kDown;
     __shared__ int4 s_entry[EXPERTS ? kFewBlocks : 1];
     __shared__ int s_waves[kMaxWaves];
@@ -363,7 +363,6 @@ k_i4_few(const Product p, const ExpertList list, const Few f) {
 
 template <int KIND, int MAXMT, int R, int P>
 hipError_t launch_as(const Product& p, const ExpertList* list, hipStream_t s) {
-    static const ExpertList none{};
     const int n_cu = dense::compute_units();
     const int chunks = (p.K + kChunk - 1) / kChunk;
     Few f;
@@ -376,7 +375,7 @@ hipError_t launch_as(const Product& p, const ExpertList* list, hipStream_t s) {
     const int64_t grid = std::min<int64_t>(units, int64_t(n_cu) * per_cu);
     const int lds = 2 * kMaxWaves * R * MAXMT * 16 * 4;
     hipLaunchKernelGGL((k_i4_few<KIND, MAXMT, R, P>), dim3(unsigned(grid)), dim3(f.kw * kWave), lds, s, p,
-                       list ? *list : none, f);
+                       list_of<KIND>(list), f);
     return hipGetLastError();
 }
 

@@ -73,7 +73,7 @@ struct At {
     Rows w;
 };
 template <int KIND, class C>
-__device__ __forceinline__ At tile_at(const Product& p, const ExpertList& list, const int4* map, int n_tiles, int m_tiles) {
+__device__ __forceinline__ At tile_at(const Product& p, const ListOf<KIND>& list, const int4* map, int n_tiles, int m_tiles) {
     const int id = blockIdx.x;
     At at;
     at.w = p.w;
@@ -166,7 +166,7 @@ __device__ __forceinline__ void finish_sums(const Product& p, const dev::f32x4 (
 template <int KIND, int MF, int WK, int WN, int S>
 __global__ void __launch_bounds__((Mid<MF, WK, WN, S>::kThreads))
     __attribute__((amdgpu_waves_per_eu((Mid<MF, WK, WN, S>::kWavesPerSimd))))
-k_i4_mid(const Product p, const ExpertList list, const int4* __restrict__ map, int n_tiles, int m_tiles) {
+k_i4_mid(const Product p, const ListOf<KIND> list, const int4* __restrict__ map, int n_tiles, int m_tiles) {
     typedef Mid<MF, WK, WN, S> C;
     constexpr bool EXPERTS = KIND == kGateUp || KIND == kDown;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
@@ -319,7 +319,7 @@ constexpr uint32_t kOutside = 0xFFFFFFF0u;   // an offset past kRange: zeros, al
 template <int KIND, int MF, int WK, int WN, int D>
 __global__ void __launch_bounds__((Wide<MF, WK, WN, D>::kThreads))
     __attribute__((amdgpu_waves_per_eu((Wide<MF, WK, WN, D>::kWavesPerSimd))))
-k_i4_wide(const Product p, const ExpertList list, const int4* __restrict__ map, int n_tiles, int m_tiles) {
+k_i4_wide(const Product p, const ListOf<KIND> list, const int4* __restrict__ map, int n_tiles, int m_tiles) {
     typedef Wide<MF, WK, WN, D> C;
     constexpr bool EXPERTS = KIND == kGateUp || KIND == kDown;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
@@ -488,14 +488,13 @@ hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done)
 
 template <int KIND, class C, class F>
 hipError_t launch_as(F kernel, const Product& p, const ExpertList* list, const void* map, int64_t max_tiles, hipStream_t s) {
-    static const ExpertList none{};
     static std::atomic<uint64_t> allowed{0};
     const int64_t nt = (p.N + C::BN - 1) / C::BN, mt = list ? max_tiles : (p.T + C::BM - 1) / C::BM, blocks = nt * mt;
     if (blocks == 0) return hipSuccess;
     if (blocks > 0x7FFFFFFF / C::kThreads) return hipErrorInvalidValue;
     const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), C::kLds, allowed);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3(unsigned(blocks)), dim3(C::kThreads), C::kLds, s, p, list ? *list : none,
+    hipLaunchKernelGGL(kernel, dim3(unsigned(blocks)), dim3(C::kThreads), C::kLds, s, p, list_of<KIND>(list),
                        static_cast<const int4*>(map), int(nt), int(mt));
     return hipGetLastError();
 }

@@ -64,7 +64,7 @@ __device__ __forceinline__ void write16(uint8_t* to, const dev::u32x4& v) {
 
 template <int KIND>
 __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
-k_i4_turns(const Product p, const ExpertList list, const int4* __restrict__ map, int n_tiles, int m_tiles) {
+k_i4_turns(const Product p, const ListOf<KIND> list, const int4* __restrict__ map, int n_tiles, int m_tiles) {
     constexpr bool EXPERTS = KIND == kGateUp || KIND == kDown, GATE = KIND == kGateUp;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
 
@@ -299,7 +299,6 @@ hipError_t allow_lds(const void* kernel, std::atomic<uint64_t>& done) {
 
 template <int KIND>
 hipError_t launch_as(const Product& p, const ExpertList* list, const void* map, int64_t max_tiles, hipStream_t s) {
-    static const ExpertList none{};
     static std::atomic<uint64_t> allowed{0};
     const int64_t nt = (p.N + kB - 1) / kB, mt = list ? max_tiles : (p.T + kB - 1) / kB;
     const int64_t blocks = (nt * mt + kXcds - 1) / kXcds * kXcds;
@@ -308,7 +307,7 @@ hipError_t launch_as(const Product& p, const ExpertList* list, const void* map, 
     const auto kernel = &k_i4_turns<KIND>;
     const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), allowed);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3(unsigned(blocks)), dim3(kThreads), kLds, s, p, list ? *list : none,
+    hipLaunchKernelGGL(kernel, dim3(unsigned(blocks)), dim3(kThreads), kLds, s, p, list_of<KIND>(list),
                        static_cast<const int4*>(map), int(nt), int(mt));
     return hipGetLastError();
 }
