@@ -97,6 +97,7 @@ k_i4_turns(const Product p, const ListOf<KIND> list, const int4* __restrict__ ma
 
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
     const int wm = wave / WN, wn = wave % WN;
+    const bool mine = wm * TM < rows;                         // (a wave without rows computes nothing)
     const bool second = wave >= 4;                            // (SIMD i has waves i and i + 4)
 
     // x: a wave's loads of a slice are 4 times 8 rows; chunk c of row r at slot c ^ row_swz(r).  Where K ends in
@@ -204,7 +205,7 @@ k_i4_turns(const Product p, const ListOf<KIND> list, const int4* __restrict__ ma
             if (half == 1 && second) __builtin_amdgcn_s_waitcnt(wait_for(AHEAD ? 2 : 0, 0));
             else __builtin_amdgcn_s_waitcnt(wait_for(63, 0));
             fence_barrier();
-            if (half == 0 || whole) {
+            if (mine && (half == 0 || whole)) {
                 __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
