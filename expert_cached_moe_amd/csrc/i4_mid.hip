@@ -302,34 +302,33 @@ k_i4_mid(const Product p, const ListOf<KIND> list, const int4* __restrict__ map,
 // The same with whole lines of codes in registers: a wave's 32 rows by blocks of 128 k, 16 bytes a lane and 16 rows, so
 // that the 32 codes of a lane share a group, D blocks ahead; x alone goes through LDS, in D + 1 stages.  Half the
 // waits, words and addresses for a code: for products whose time is the decoding, many rows of weights or many experts.
-template <int MF_, int WK_, int WN_, int D_>
+template <int MF_, int D_>
 struct Wide {
-    static constexpr int MF = MF_, WK = WK_, WN = WN_, D = D_;
-    static constexpr int NW = WK * WN, kThreads = NW * kWave, BM = MF * 16, BN = 32 * WN;
-    static constexpr int X = BM * 256, kStage = WK * X;
-    static constexpr int XL = X / 1024 / WN;
-    static constexpr int kPassRows = WK == 1 && BM > 32 ? 32 : BM, kRow = 36, kSums = NW * kPassRows * kRow * 4;
+    static constexpr int MF = MF_, WK = 1, WN = 4, D = D_;
+    static constexpr int NW = WN, kThreads = NW * kWave, BM = MF * 16, BN = 32 * WN;
+    static constexpr int kStage = BM * 256;
+    static constexpr int XL = kStage / 1024 / WN;
+    static constexpr int kPassRows = BM > 32 ? 32 : BM, kRow = 36, kSums = NW * kPassRows * kRow * 4;
     static constexpr int kLds = (D + 1) * kStage > kSums ? (D + 1) * kStage : kSums;
-    static_assert(XL * WN * 1024 == X && kLds <= 160 * 1024, "LDS of a CU");
+    static_assert(XL * WN * 1024 == kStage && (D == 1 || D == 2), "loads of a stage, registers of a block");
     static constexpr int kPerCu = 160 * 1024 / kLds < 1 ? 1 : 160 * 1024 / kLds;
     static constexpr int kWavesPerSimd = NW * kPerCu / 4 < 1 ? 1 : NW * kPerCu / 4 > 4 ? 4 : NW * kPerCu / 4;
 };
 constexpr uint32_t kOutside = 0xFFFFFFF0u;   // an offset past kRange: zeros, also into LDS
 
-template <int KIND, int MF, int WK, int WN, int D>
-__global__ void __launch_bounds__((Wide<MF, WK, WN, D>::kThreads))
-    __attribute__((amdgpu_waves_per_eu((Wide<MF, WK, WN, D>::kWavesPerSimd))))
+template <int KIND, int MF, int D>
+__global__ void __launch_bounds__((Wide<MF, D>::kThreads)) __attribute__((amdgpu_waves_per_eu((Wide<MF, D>::kWavesPerSimd))))
 k_i4_wide(const Product p, const ListOf<KIND> list, const int4* __restrict__ map, int n_tiles, int m_tiles) {
-    typedef Wide<MF, WK, WN, D> C;
+    typedef Wide<MF, D> C;
+    constexpr int WN = C::WN;
     constexpr bool EXPERTS = KIND == kGateUp || KIND == kDown;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const At at = tile_at<KIND, C>(p, list, map, n_tiles, m_tiles);
     if (!at.any) return;
     const int rows = min(at.left, C::BM);
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
-    const int wn = wave % WN, wk = wave / WN;
-    const int j = lane % 16, kb = lane / 16;
-    const int blocks = (p.K + 127) / 128, n = (blocks * p.planes + WK - 1) / WK;
+    const int wn = wave, j = lane % 16, kb = lane / 16;
+    const int blocks = (p.K + 127) / 128, n = blocks * p.planes;
 
     // x: 16 lanes a row of 256 bytes, 4 rows a load; 16-byte chunk c of row r at slot c ^ (r % 16)
     uint32_t xo[C::XL];
@@ -358,21 +357,19 @@ k_i4_wide(const Product p, const ListOf<KIND> list, const int4* __restrict__ map
         step[f] = __builtin_amdgcn_readfirstlane(wa.step * 2);      // (one run of 16 rows: one step)
         E[f] = row_scale(at.w.exps[row]);
     }
-    int x_plane = p.planes - 1, x_block = wk, w_block = wk, w_plane = p.planes - 1;
+    int x_plane = p.planes - 1, x_block = 0, w_block = 0, w_plane = p.planes - 1;
     auto settle = [&](int& block, int& plane) {
-        while (block >= blocks && plane > 0) block -= blocks, --plane;
+        if (block >= blocks && plane > 0) block -= blocks, --plane;
     };
-    settle(x_block, x_plane);
-    settle(w_block, w_plane);
     auto issue_x = [&](int stage) {
         const __amdgpu_buffer_rsrc_t rx = rsrc(xp + x_plane * p.plane);
-        uint8_t* d = lds + stage * C::kStage + wk * C::X + wn * 1024;
+        uint8_t* d = lds + stage * C::kStage + wn * 1024;
 #pragma unroll
         for (int q = 0; q < C::XL; ++q) {
             const int r = (wn + WN * q) * 4 + lane / 16, c = lane % 16 ^ (r % 16);
             load16_lds(rx, d + q * (WN * 1024), x_block * 128 + c * 8 < p.K ? xo[q] + c * 16 : kOutside, x_block * 256);
         }
-        x_block += WK;
+        ++x_block;
         settle(x_block, x_plane);
     };
     dev::u32x4 code[D][2];
@@ -384,7 +381,7 @@ k_i4_wide(const Product p, const ListOf<KIND> list, const int4* __restrict__ map
             c[f] = __builtin_bit_cast(dev::u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, in ? co[f] : kOutside, w_block * 64, 0));
             g[f] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(rg, in ? wo[f] : kOutside, (w_block * 128 >> at.w.shift) * step[f], 0));
         }
-        w_block += WK;
+        ++w_block;
         settle(w_block, w_plane);
     };
     dev::f32x4 acc[MF][2];
@@ -406,11 +403,11 @@ k_i4_wide(const Product p, const ListOf<KIND> list, const int4* __restrict__ map
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt(wait_for((D - 1) * (C::XL + 4), 0));
         asm volatile("" ::: "memory");
-        if constexpr (C::WN > 1) __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
         issue_x(ahead);
-        const uint8_t* x = lds + stage * C::kStage + wk * C::X;
+        const uint8_t* x = lds + stage * C::kStage;
         float s2[2], off[2];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
@@ -440,8 +437,7 @@ k_i4_wide(const Product p, const ListOf<KIND> list, const int4* __restrict__ map
     // (past the end blocks are zeros)
     for (int it = 0; it < n; it += D) {
         block(std::integral_constant<int, 0>{});
-        if constexpr (D > 1) block(std::integral_constant<int, 1 % D>{});
-        if constexpr (D > 2) block(std::integral_constant<int, 2 % D>{});
+        if constexpr (D > 1) block(std::integral_constant<int, 1>{});
     }
     finish_sums<KIND, C>(p, acc, lds, at.r0, at.n0, at.base, at.shared, rows);
 }
@@ -502,9 +498,9 @@ template <int KIND, int MF, int WK, int WN, int S>
 hipError_t mid(const Product& p, const ExpertList* list, const void* map, int64_t max_tiles, hipStream_t s) {
     return launch_as<KIND, Mid<MF, WK, WN, S>>(&k_i4_mid<KIND, MF, WK, WN, S>, p, list, map, max_tiles, s);
 }
-template <int KIND, int MF, int WK, int WN, int D>
+template <int KIND, int MF, int D>
 hipError_t wide(const Product& p, const ExpertList* list, const void* map, int64_t max_tiles, hipStream_t s) {
-    return launch_as<KIND, Wide<MF, WK, WN, D>>(&k_i4_wide<KIND, MF, WK, WN, D>, p, list, map, max_tiles, s);
+    return launch_as<KIND, Wide<MF, D>>(&k_i4_wide<KIND, MF, D>, p, list, map, max_tiles, s);
 }
 
 template <int KIND>
@@ -515,9 +511,9 @@ hipError_t choose(int kind, const Product& p, const ExpertList* list, const void
         case kMid128x32: return mid<KIND, 8, 4, 1, 2>(p, list, map, max_tiles, s);
         case kMid64x64: return mid<KIND, 4, 4, 2, 3>(p, list, map, max_tiles, s);
         case kMid128x64: return mid<KIND, 8, 4, 2, 2>(p, list, map, max_tiles, s);
-        case kMid32x128: return wide<KIND, 2, 1, 4, 2>(p, list, map, max_tiles, s);
-        case kMid64x128: return wide<KIND, 4, 1, 4, 2>(p, list, map, max_tiles, s);
-        case kMid128x128: return wide<KIND, 8, 1, 4, 1>(p, list, map, max_tiles, s);
+        case kMid32x128: return wide<KIND, 2, 2>(p, list, map, max_tiles, s);
+        case kMid64x128: return wide<KIND, 4, 2>(p, list, map, max_tiles, s);
+        case kMid128x128: return wide<KIND, 8, 1>(p, list, map, max_tiles, s);
         default: return hipErrorInvalidValue;
     }
 }

@@ -167,6 +167,22 @@ def test_matmul(ctx, T, N, K, group, xt, yt, pad, off):
     check(got, *Q.matmul_bound(ref, *w.parts, group, NAME[yt], 3 if xt == F32 else 1))
 
 
+# (each kind of tiles: tests/test_i4_coverage_cpu.py)
+TILES = [(40, 4230, 416), (90, 4230, 160), (9, 8202, 160), (70, 8202, 288), (68, 8202, 256), (40, 20028, 96), (70, 61128, 416), (214, 61128, 288),
+         (300, 40003, 352), (333, 61003, 96), (70, 61003, 96)]
+
+
+@pytest.mark.parametrize("T,N,K", TILES)
+@pytest.mark.parametrize("xt,yt,pad,off", [(BF16, BF16, 0, 0), (BF16, F32, 8, 8), (F32, F32, 0, 0), (F32, BF16, 3, 1)])
+def test_matmul_on_every_kind_of_tiles(ctx, T, N, K, xt, yt, pad, off):
+    group = 32 << T % 3
+    w = Weights(N, K, group, T + N + K)
+    x, ref = numbers((T * (K + pad) + off,), T * N, xt)
+    x, ref = x[off:], ref[off:].reshape(T, K + pad)[:, :K]
+    got = product(ctx, x, xt, K + pad, T, w, w.upload(), yt, pad, off)
+    check(got, *Q.matmul_bound(ref, *w.parts, group, NAME[yt], 3 if xt == F32 else 1))
+
+
 @pytest.mark.parametrize("T", [1, 6, 16, 40, 200])
 @pytest.mark.parametrize("xt", [F32, BF16])
 def test_matmul_is_as_good_as_fp32(ctx, T, xt):
@@ -377,15 +393,61 @@ def some_ids(T, E, k, seed, popular=0.0):
     return np.argsort(-(r.normal(size=(T, E)) + popular * r.normal(size=(1, E))), axis=1)[:, :k].astype(np.int32)
 
 
+LAYERS = [(64, 32, 4, 2, 0, 32), (128, 96, 6, 3, 1, 64), (256, 160, 5, 1, 1, 128), (448, 416, 8, 4, 0, 128), (1024, 544, 4, 2, 1, 32)]
+TOKENS = [1, 2, 4, 5, 8, 11, 16, 17, 40, 130, 300]
+
+
 @pytest.mark.parametrize("zero", [0, 1])
-@pytest.mark.parametrize("H,I,E,k,shared,group", [(64, 32, 4, 2, 0, 32), (128, 96, 6, 3, 1, 64), (256, 160, 5, 1, 1, 128),
-                                                  (448, 416, 8, 4, 0, 128), (1024, 544, 4, 2, 1, 32)])
-@pytest.mark.parametrize("T", [1, 2, 4, 5, 8, 11, 16, 17, 40, 130, 300])
+@pytest.mark.parametrize("H,I,E,k,shared,group", LAYERS)
+@pytest.mark.parametrize("T", TOKENS)
 def test_experts(T, H, I, E, k, shared, group, zero):
     layer = Layer(H, I, E, k, shared, group, zero, seed=H)
     x, ref = numbers((T, H), T, BF16)
     ids = some_ids(T, E, k, T, 1.0)
     layer.check(layer.run(x, ids), ref, ids)
+
+
+# (each kind of tiles for either product)
+LARGE = [(384, 64, 2, 2, 0, 32, 1031), (128, 352, 2, 2, 0, 64, 1031), (192, 64, 2, 2, 0, 128, 1031), (128, 192, 2, 2, 0, 32, 1031),
+         (192, 128, 2, 2, 0, 64, 2016), (256, 192, 2, 2, 0, 64, 2016), (128, 96, 8, 4, 1, 128, 1612), (192, 96, 8, 4, 1, 32, 1612),
+         (64, 64, 8, 4, 1, 64, 1612), (384, 352, 4, 4, 1, 128, 1612), (704, 352, 4, 4, 1, 32, 1612), (256, 928, 2, 2, 1, 64, 2521),
+         (1856, 256, 2, 2, 1, 128, 2521)]
+
+
+@pytest.mark.parametrize("H,I,E,k,shared,group,T", LARGE)
+def test_experts_on_every_kind_of_tiles(H, I, E, k, shared, group, T):
+    layer = Layer(H, I, E, k, shared, group, T % 2, seed=H)
+    x, ref = numbers((T, H), T, BF16)
+    ids = some_ids(T, E, k, T, 1.0)
+    layer.check(layer.run(x, ids), ref, ids)
+
+
+@pytest.mark.parametrize("H,I,E,k,shared,group,T", LARGE)
+def test_experts_on_every_kind_of_tiles(H, I, E, k, shared, group, T):
+    layer = Layer(H, I, E, k, shared, group, T % 2, seed=H)
+    x, ref = numbers((T, H), T, BF16)
+    ids = some_ids(T, E, k, T, 1.0)
+    layer.check(layer.run(x, ids), ref, ids)
+
+
+def test_experts_of_tokens_past_4_gib():
+    """x and o of 4 GiB and more; the last rows are checked."""
+    H, I, T = 4096, 64, (1 << 19) + 300
+    layer = Layer(H, I, 2, 1, 0, 64, 1)
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    rows = np.array([0, 1, 255, 262143, 262144, 524287, 524288, T - 2, T - 1])
+    some, ref = numbers((len(rows), H), 3, BF16)
+    x[torch.from_numpy(rows).cuda()] = some
+    ids = np.random.default_rng(1).integers(0, 2, (T, 1)).astype(np.int32)
+    o = layer.run(x, ids)
+    got = o[torch.from_numpy(rows).cuda()].double().cpu().numpy()
+    for e in range(2):
+        at = ids[rows, 0] == e
+        check(got[at], *Q.expert_bound(ref[at], *layer.parts[e], layer.group))
+    assert (o[T] == -7).all()
+    few = torch.ones(T, dtype=torch.bool)
+    few[rows] = False
+    assert not bool(o[:T].any(dim=1).cpu()[few].any())
 
 
 @pytest.mark.parametrize("T", [1, 6, 16, 64, 200])

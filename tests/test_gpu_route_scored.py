@@ -89,7 +89,7 @@ SHAPES = [(1, 1, 1, 1, 1, 1), (1, 8, 2, 1, 1, 1), (4, 256, 8, 8, 4, 2), (3, 512,
           (64, 64, 1, 64, 33, 2), (5, 495, 12, 33, 20, 2), (30, 500, 10, 5, 2, 2), (63, 141, 6, 3, 1, 1),
           (129, 160, 8, 8, 3, 2), (700, 128, 8, 1, 1, 1), (515, 256, 8, 8, 4, 2), (1021, 141, 6, 1, 1, 1),
           (333, 510, 7, 17, 9, 1), (200, 65, 3, 13, 13, 2), (97, 12, 4, 2, 1, 2), (640, 7, 7, 7, 7, 1),
-          (17, 9, 1, 3, 2, 1), (256, 24, 2, 1, 1, 1), (257, 24, 3, 2, 1, 2), (2049, 64, 1, 1, 1, 1), (2051, 128, 8, 1, 1, 1),
+          (6, 100, 3, 1, 1, 1), (100, 512, 4, 1, 1, 1), (17, 9, 1, 3, 2, 1), (256, 24, 2, 1, 1, 1), (257, 24, 3, 2, 1, 2), (2049, 64, 1, 1, 1, 1), (2051, 128, 8, 1, 1, 1),
           (2050, 141, 6, 1, 1, 1), (4099, 256, 8, 8, 4, 2), (2100, 300, 5, 1, 1, 1), (2053, 512, 3, 32, 9, 2), (2060, 504, 4, 9, 5, 2),
           (2070, 48, 16, 16, 16, 2), (20001, 32, 2, 4, 2, 1)]
 
