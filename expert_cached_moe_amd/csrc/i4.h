@@ -66,19 +66,14 @@ struct Product {
     int64_t stride, shared;  // bytes from slot to slot; of the shared blob from slot 0
 };
 
-// One record of the tile map: entry, its tile of rows, its first place, its rows.
-struct MapTile {
-    int32_t entry, tile, base, count;
-};
-
 hipError_t launch_i4_quantize(const void* x, int x_type, int64_t ld_x, int64_t rows, int32_t cols, int group, int zero,
                               uint8_t* q, uint16_t* words, uint8_t* exps, hipStream_t s);
 // Rows of numbers to bf16 rows of K back to back (fp32: three parts, T K elements apart).
 hipError_t launch_i4_activations(const void* x, int x_type, int64_t ld_x, int64_t T, int32_t K, uint16_t* out, hipStream_t s);
-// Records of all row tiles of the list's entries, behind a count: int32 count, 3 of padding, records.
+// Records of all row tiles of the list's entries (map_tiles at most), behind a count: int32 count, 3 of padding, records of
+// entry, its tile of rows, its first place, its rows.
 hipError_t launch_i4_map(const ExpertList& list, const int32_t* offsets, int64_t T, int top_k, int rows, void* map,
                          hipStream_t s);
-inline int64_t map_tiles(int n, int64_t rows, int tile) { return rows / tile + n; }   // the most records that there can be
 // What the product computes (kOut16 ...) on tiles of a kind of i4_plan.h; experts: with the map for its rows.
 hipError_t launch_i4_mid(int what, int kind, const Product& p, const ExpertList* list, const void* map, int64_t max_tiles,
                          hipStream_t s);

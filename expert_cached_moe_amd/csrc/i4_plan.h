@@ -42,16 +42,25 @@ inline double kind_time(int kind, double tiles, int64_t N, int64_t slices, int n
     const double full = (k.one + (kind == kTurns ? 1 : k.slots - 1) * k.more) * steps + k.tile;
     return whole * full + (rest > 0 ? (k.one + (rest - 1) * k.more) * steps + k.tile : 0.0);
 }
+// Workgroups of a launch (the threads of one fit 31 bits; 256 x 256 tiles are few enough for every product that memory
+// holds).
+constexpr int64_t kMostBlocks = 0x7FFFFFFF / 512;
+inline bool fits(int kind, int64_t tiles, int64_t N) {
+    return kind == kTurns || tiles <= kMostBlocks / ((N + kKind[kind].cols - 1) / kKind[kind].cols);
+}
 // Dense: T rows, `planes` walks over K.
 inline int plan_dense(int64_t T, int64_t N, int64_t K, int planes, int n_cu) {
     int best = 0;
     double least = 1e30;
     for (int k = 0; k < kKinds; ++k) {
-        const double t = kind_time(k, double((T + kKind[k].rows - 1) / kKind[k].rows), N, (K + 63) / 64 * planes, n_cu);
-        if (t < least) least = t, best = k;
+        const int64_t tiles = (T + kKind[k].rows - 1) / kKind[k].rows;
+        const double t = kind_time(k, double(tiles), N, (K + 63) / 64 * planes, n_cu);
+        if (t < least && fits(k, tiles, N)) least = t, best = k;
     }
     return best;
 }
+// The most row tiles that n entries of `rows` rows in all can have.
+inline int64_t map_tiles(int64_t n, int64_t rows, int tile) { return rows / tile + n; }
 // Experts: `pairs` rows over n entries (their numbers of rows are known on the device only: as if each pair chose
 // at random), N and K of one product.
 inline double entry_tiles(int n, int64_t pairs, int rows) {
@@ -63,7 +72,7 @@ inline int plan_experts(int n, int64_t pairs, int64_t N, int64_t K, int n_cu) {
     double least = 1e30;
     for (int k = 0; k < kKinds; ++k) {
         const double t = kind_time(k, entry_tiles(n, pairs, kKind[k].rows), N, (K + 63) / 64, n_cu);
-        if (t < least) least = t, best = k;
+        if (t < least && fits(k, map_tiles(n, pairs, kKind[k].rows), N)) least = t, best = k;
     }
     return best;
 }

@@ -297,6 +297,39 @@ def test_offsets_past_2_gib_and_4_gib(ctx):
         del x, y
 
 
+def test_most_rows(ctx):
+    """2^23 rows of weights, of x and of both kinds of results; rows at the ends and in the middle are checked."""
+    N, K = 1 << 23, 32
+    rows = np.array([0, 1, 4095, 4194303, 4194304, N - 17, N - 2, N - 1])
+    at = torch.from_numpy(rows).cuda()
+    g = torch.Generator(device="cuda").manual_seed(4)
+    w = torch.randn((N, K), generator=g, device="cuda", dtype=torch.bfloat16)
+    q = torch.empty((N, K // 2), dtype=torch.uint8, device="cuda")
+    words = torch.empty(N, dtype=torch.int16, device="cuda")
+    exps = torch.empty(N, dtype=torch.uint8, device="cuda")
+    B.moe_i4_quantize(ctx, w, BF16, K, N, K, 32, 1, q, words, exps)
+    torch.cuda.synchronize()
+    want = Q.quantize(w[at].double().cpu().numpy(), 32, 1)
+    parts = (Q.unpack(q[at].cpu().numpy()), words[at].cpu().numpy().view(np.uint16)[:, None], exps[at].cpu().numpy())
+    for have, ref in zip(parts, want):
+        assert np.array_equal(have, ref)
+    for T in (2, 9):
+        x, ref = numbers((T, K), T, BF16)
+        y = torch.full((T * N + 1,), -7.0, device="cuda")
+        ws = torch.empty(B.moe_i4_workspace_bytes(T, N, K), dtype=torch.uint8, device="cuda")
+        B.moe_i4_matmul(ctx, x, BF16, K, T, q, words, exps, N, K, 32, y, F32, N, ws)
+        torch.cuda.synchronize()
+        check(y[:T * N].view(T, N)[:, at].double().cpu().numpy(), *Q.matmul_bound(ref, *parts, 32, "f32"))
+        assert y[T * N] == -7
+    few = Weights(3, K, 32, 5)
+    y = torch.full((N * 3 + 1,), -7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(B.moe_i4_workspace_bytes(N, 3, K), dtype=torch.uint8, device="cuda")
+    B.moe_i4_matmul(ctx, w, BF16, K, N, *few.upload(), 3, K, 32, y, BF16, 3, ws)
+    torch.cuda.synchronize()
+    check(y[:N * 3].view(N, 3)[at].double().cpu().numpy(), *Q.matmul_bound(w[at].double().cpu().numpy(), *few.parts, 32, "bf16"))
+    assert y[N * 3] == -7
+
+
 @pytest.mark.parametrize("T", [3, 16, 40, 300])
 @pytest.mark.parametrize("xt", [F32, BF16])
 def test_matmul_in_a_graph_on_another_stream_with_a_larger_workspace(ctx, T, xt):

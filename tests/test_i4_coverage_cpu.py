@@ -64,6 +64,22 @@ def test_every_kind_is_taken_over_the_range(kinds):
         assert kinds(calls) == KINDS
 
 
+def test_launches_fit(kinds):
+    """The threads of a launch stay within 31 bits up to the largest products (tiles of up to 512 threads)."""
+    rows, cols = (32, 64, 128, 64, 128, 32, 64, 128, 256), (32, 32, 32, 64, 64, 128, 128, 128, 256)
+
+    def blocks(k, tiles, N):
+        return tiles(rows[k]) * -(-N // cols[k])
+
+    for a in range(13, 24):
+        for K in (32, 4096):
+            T, N = 1 << a, 1 << min(23, 36 - a)
+            (k,) = kinds([f"m {T} {N} {K} 1"])
+            assert blocks(k, lambda r: -(-T // r), N) * 512 < 2 ** 31
+            (k,) = kinds([f"e 512 {T * 16} {N >> 4} {K}"])
+            assert blocks(k, lambda r: T * 16 // r + 512, N >> 4) * 512 < 2 ** 31
+
+
 def test_compiled_kernels():
     """Nine kinds, the few-row kernel by tokens (dense) and parts of x (dense), for four products."""
     out = subprocess.run(["nm", "-C", B.LIB_PATH], capture_output=True, text=True).stdout
