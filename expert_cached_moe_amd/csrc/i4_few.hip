@@ -15,6 +15,10 @@
 // registers are loaded again as soon as it is used, with the next chunk or the next unit of rows, so
 // the stream does not stop between units.
 //
+// Measured (kernel): 2048 x 2048 at one token 4.4 us (launch, one trip to memory, the sums; its 2.2 MB take 0.4), 100003 x
+// 4096 at 4 tokens 47-49 (220 MB at 4.6 TB/s; 33 at the rate of a bare read), 7 experts of 4096 x 1536 at one token 19 and 9.5
+// (50 and 25 MB).  Twice the rows a wave (more bytes in flight, fewer waves) 3% slower, half of them 14-30%.
+//
 // Experts: each workgroup lists the entries that have rows, from the offsets, in blocks of 4 rows at most, and walks their
 // units.  Blocks of 8 cost more registers, so waves, for the few entries that fill them (256 experts of 4096 x 1536 with
 // the shared one, top 6, 8 tokens: 157 us against 118; 128 of 2048 x 768, top 8: 48.5 and 48.9).

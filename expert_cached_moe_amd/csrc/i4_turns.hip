@@ -10,6 +10,11 @@
 // takes 448 of its 512 cycles.  So the codes are decoded once a tile, the weights never pass through
 // memory, and the matrix units are fed as by a product of bf16 weights.
 //
+// Measured: 8,192 x 4096 x 8192 435-452 us (1.22-1.26 PFLOP/s; 380 at the rate of a library product of 8192^3); a slice takes
+// 1.6 us with few tiles and 1.8-1.9 with every CU busy, a tile 8-10 besides for its start and its results.  128 experts of
+// 2048 x 768, top 8, 8,192 tokens 503 and 317: of the tiles of experts with 512 rows on average a fifth is empty, and the 12
+// slices of the down product are 22 of a tile's 32 us.
+//
 // In slice j of a group's turns, B of slice j lies at place u, x at u + 1, those of the next slice behind
 // them; in the reading turns x of slice j + 1 is requested into u + 3 and the weights of slice j + 2 are
 // written to u + 4 = u - 1: the places of slice j - 1, which both groups have read.

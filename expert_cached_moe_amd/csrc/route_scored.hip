@@ -18,7 +18,7 @@
 // values rounded to fp32, in order; where two of the k + 1 largest are equal there the wave makes
 // its choice again on the 64-bit values.
 //
-// Large T: workgroups of 32 tokens and more, 256 at most, count their pairs by expert, and the
+// More than 16 tokens or 64 pairs: workgroups of 4 tokens and more, 256 at most, count their pairs by expert, and the
 // second kernel's workgroups, one for each, add up the counts for themselves: E x 512 bytes from L2
 // in place of two further launches.  8,192 tokens, 256 experts in 8 groups, top 8: 14 us and 8 (a wave a
 // token, sorted by three kernels: 20, and 11 for these); 515 tokens 7.5 and 5.  The bytes take 2 us: what bounds the

@@ -235,7 +235,8 @@ int moe_route_scored(moe_ctx* ctx, const float* d_logits, const float* d_bias, i
  *   sigmoid: dlogit_j = ds_j s_j (1 - s_j), 0 for the others;
  *   softmax: dlogit_e = s_e (ds_e - sum_j ds_j s_j) (renormalised: 0 for the others).
  * The choice has no gradient, and none goes to the bias (balancing sets it).  Formed in 64 bits and
- * rounded once.  An id outside 0..E-1 counts as none chosen.  T == 0 is a no-op.  Errors as above. */
+ * rounded once.  A token's ids are distinct, as moe_route_scored's; an id outside 0..E-1 counts as none
+ * chosen.  T == 0 is a no-op.  Errors as above. */
 int moe_route_scored_backward(moe_ctx* ctx, const float* d_logits, int32_t T, const moe_route_rule* rule,
                               const int32_t* d_topk_ids, const float* d_dw, float* d_dlogits, hipStream_t s);
 

@@ -356,6 +356,26 @@ def test_matmul_in_a_graph_on_another_stream_with_a_larger_workspace(ctx, T, xt)
         assert np.array_equal(first, again)                    # the same sums in the same order
 
 
+@pytest.mark.parametrize("T", [2, 40, 600])
+def test_two_calls_at_once(ctx, T):
+    """Two streams, each with its own workspace and results, the weights shared."""
+    N, K, group = 1000, 1024, 64
+    w = Weights(N, K, group, 7)
+    dw = w.upload()
+    xs = [numbers((T, K), seed, F32) for seed in (1, 2)]
+    alone = [product(ctx, x, F32, K, T, w, dw, F32) for x, _ in xs]
+    ys = [torch.empty((T, N), device="cuda") for _ in xs]
+    ws = [torch.empty(B.moe_i4_workspace_bytes(T, N, K), dtype=torch.uint8, device="cuda") for _ in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for (x, _), y, work, s in zip(xs, ys, ws, streams):
+            B.moe_i4_matmul(ctx, x, F32, K, T, *dw, N, K, group, y, F32, N, work, s)
+    torch.cuda.synchronize()
+    for y, one in zip(ys, alone):
+        assert np.array_equal(y.double().cpu().numpy(), one)
+
+
 # ------------------------------------------------------------------ experts
 
 class Layer:

@@ -108,6 +108,23 @@ def test_choice_gates_grouping_and_gradient(T, E, k, groups, keep, top, biased, 
     r.check_gradient(logits, ids, dw)
 
 
+def test_most_tokens():
+    """2^24 tokens, counts of 32,768 tokens a workgroup (16 bits); all of one workgroup's with one expert."""
+    T, E = 1 << 24, 2
+    r = Router(E, 1, T, "sigmoid", renorm=0)
+    logits = torch.randn((T, E), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    logits[32768:65536, 0] = 9.0
+    r.forward(logits, None)
+    torch.cuda.synchronize()
+    ids = (logits[:, 1] > logits[:, 0]).int()
+    assert torch.equal(r.ids[:T], ids)
+    order = torch.sort(ids, stable=True).indices.int()
+    assert torch.equal(r.perm[:T], order)
+    assert torch.equal(r.perm[:T][r.inv[:T].long()], torch.arange(T, dtype=torch.int32, device="cuda"))
+    n = int((ids == 0).sum())
+    assert r.counts[:2].tolist() == [n, T - n] and r.offsets[:3].tolist() == [0, n, T]
+
+
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 def test_prefill_chunk(kind):
     r = Router(256, 8, 8192, kind, 8, 4, 2, 1, 2.5)
