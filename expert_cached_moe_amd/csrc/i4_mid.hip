@@ -468,7 +468,7 @@ __global__ __launch_bounds__(1024) void k_i4_map(const ExpertList list, const in
     if (lane == kWave - 1) s_sum[wave] = incl;
     __syncthreads();
     int first = incl - tiles, total = 0;
-    for (int w = 0; w < 16; ++w) {
+    for (int w = 0; w < int(blockDim.x) / kWave; ++w) {
         if (w < wave) first += s_sum[w];
         total += s_sum[w];
     }
@@ -527,7 +527,7 @@ hipError_t choose(int kind, const Product& p, const ExpertList* list, const void
 
 hipError_t launch_i4_map(const ExpertList& list, const int32_t* offsets, int64_t T, int top_k, int rows, void* map,
                          hipStream_t s) {
-    hipLaunchKernelGGL(k_i4_map, dim3(1), dim3(1024), 0, s, list, offsets, int(T), top_k, rows, static_cast<int4*>(map));
+    hipLaunchKernelGGL(k_i4_map, dim3(1), dim3((list.n + kWave - 1) / kWave * kWave), 0, s, list, offsets, int(T), top_k, rows, static_cast<int4*>(map));
     return hipGetLastError();
 }
 
