@@ -80,7 +80,7 @@ WsLayout ws_layout(const moe_config& c, int32_t max_T) {
     const int64_t rows_d = Td * c.top_k + (c.n_shared ? Td : 0);
     W.o = align256(W.h + rows * int64_t(c.inter) * act_bytes(c));
     W.scored = align256(W.o + rows_d * int64_t(c.hidden) * act_bytes(c));
-    // 16-bit counts of the router by scores, a row for each workgroup (no more of them for any smaller number of tokens)
+    // counts of the router by scores, 8 or 16 bits, a row for each workgroup (no more of them for any smaller number of tokens)
     const int64_t groups = scored_alone(T, c.top_k) ? 0 : T <= 1024 ? (T + 3) / 4 : T <= (int64_t(256) << 15) ? 256 : 512;
     W.bytes = align256(W.scored + groups * ((c.n_experts + 3) / 4 * 8));
     return W;

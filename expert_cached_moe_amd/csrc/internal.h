@@ -50,10 +50,10 @@ WsLayout ws_layout(const moe_config& c, int32_t max_T);
 // The router by scores: one workgroup without scratch takes a wave's tokens each (64 tokens, top 1: 16.8 us where several
 // workgroups and the second launch take 10; 9 tokens, top 8: 10.7 and 9.4).
 inline bool scored_alone(int64_t T, int k) { return T <= 16 && T * k <= 64; }
-// Tokens of a workgroup otherwise: 256 workgroups at most, 4 tokens and with more than 256 of them 8 (256 experts, top 8:
-// 128 tokens 10.5 us, 10.8 with 8; 1,024 tokens 15.0 and 13.2, 16.3 with 16), and counts that fit 16 bits.
+// Tokens of a workgroup otherwise: 256 workgroups at most, a multiple of 4 tokens (256 experts, top 8, 1,024 tokens: 11.6 us,
+// 12.2 with a multiple of 8; 2,048 tokens 12.4, 16.7 with 16), and counts that fit 16 bits.
 inline int32_t scored_each(int32_t T) {
-    const int32_t whole = T <= 256 ? 4 : 8, each = (T / 256 + (T % 256 ? 1 : 0) + whole - 1) / whole * whole;
+    const int32_t each = (T / 256 + (T % 256 ? 1 : 0) + 3) / 4 * 4;
     return each < 32768 ? each : 32768;
 }
 

@@ -19,8 +19,8 @@
 // its choice again on the 64-bit values.
 //
 // More than 16 tokens or 64 pairs: workgroups of 4 tokens and more, 256 at most, count their pairs by expert, and the
-// second kernel's workgroups, one for each, add up the counts for themselves: E x 512 bytes from L2
-// in place of two further launches.  8,192 tokens, 256 experts in 8 groups, top 8: 14 us and 8 (a wave a
+// second kernel's workgroups, one for each, add up the counts for themselves: E x 256 bytes from L2
+// in place of two further launches.  8,192 tokens, 256 experts in 8 groups, top 8: 14 us and 5 (a wave a
 // token, sorted by three kernels: 20, and 11 for these); 515 tokens 7.5 and 5.  The bytes take 2 us: what bounds the
 // first kernel is the length of a wave's program, read once (a token's 64-bit sigmoids, 8 rounds), and of the second a
 // chain of reads of what other dies' workgroups wrote, sums and barriers.
@@ -312,6 +312,8 @@ __device__ __forceinline__ int scored_token(const float* __restrict__ lrow, cons
     }
     return mine;
 }
+// Tokens of a workgroup up to which its counts are bytes: 256 workgroups have 65,280 then, so that sums fit 16 bits.
+constexpr int kByteTokens = 255;
 static_assert(kMaxTopK <= 16, "a token's gates have a lane each");
 
 // Tokens t0.. of [t0, t1), a wave's 64 / W at a time; each(t, expert) for the lanes of the chosen.
@@ -341,49 +343,61 @@ __global__ __launch_bounds__(1024) void k_scored_tiny(const float* __restrict__ 
     __syncthreads();
     group_tiny(s_ids, T * k, E, counts, offsets, perm, inv);
 }
-// A workgroup's tokens, and their pairs by expert: row blockIdx.x of rows, `quads` times four 16-bit counts.
+// Counts of a workgroup's pairs by expert: row blockIdx.x of rows, a byte each up to 255 tokens, 16 bits above; `parts` pieces
+// of 8 experts, or of 4.
 template <int W, int EPL>
 __global__ __launch_bounds__(512) void k_scored(const float* __restrict__ logits, const float* __restrict__ bias, int T, int E,
                                                 int k, const Rule R, int32_t* __restrict__ ids, float* __restrict__ w,
-                                                int each, int quads, uint16_t* __restrict__ rows) {
+                                                int each, int parts, uint2* __restrict__ rows) {
     __shared__ int32_t s_cnt[kMaxExperts], s_picks[512];
     for (int e = threadIdx.x; e < kMaxExperts; e += blockDim.x) s_cnt[e] = 0;
     __syncthreads();
     const int t0 = blockIdx.x * each;
     scored_tokens<W, EPL>(logits, bias, t0, min(t0 + each, T), E, k, R, ids, w, s_picks, [&](int, int e) { atomicAdd(&s_cnt[e], 1); });
     __syncthreads();
-    for (int q = threadIdx.x; q < quads; q += blockDim.x)
-        reinterpret_cast<uint2*>(rows)[int64_t(blockIdx.x) * quads + q] =
-            make_uint2(uint32_t(s_cnt[4 * q] | s_cnt[4 * q + 1] << 16), uint32_t(s_cnt[4 * q + 2] | s_cnt[4 * q + 3] << 16));
+    const bool bytes = each <= kByteTokens;
+    auto four = [&](int e) {
+        return uint32_t(s_cnt[e] | s_cnt[e + 1] << 8 | s_cnt[e + 2] << 16) | uint32_t(s_cnt[e + 3]) << 24;
+    };
+    for (int q = threadIdx.x; q < parts; q += blockDim.x)
+        rows[int64_t(blockIdx.x) * parts + q] =
+            bytes ? make_uint2(four(8 * q), four(8 * q + 4))
+                  : make_uint2(uint32_t(s_cnt[4 * q] | s_cnt[4 * q + 1] << 16), uint32_t(s_cnt[4 * q + 2] | s_cnt[4 * q + 3] << 16));
 }
 
 // The pairs of workgroup blockIdx.x of k_scored to their places: an expert's first is behind the pairs of smaller experts and
 // those of earlier rows; the others follow by their token, a bit in the expert's mask of 64 tokens (a token has an
 // expert once).
+//
+// The counts of all rows are read by every workgroup, so they are short: with bytes 8,192 tokens of 256 experts take 18.5 us
+// for both kernels, with 16 bits 21.9; 2,048 tokens 12.5 and 15.6.
+// Sums of bytes stay below 2^16 and go two to a register: the even experts of a word, and the odd ones.
+template <bool BYTES>
 __global__ __launch_bounds__(kBlock) void k_scored_place(const int32_t* __restrict__ ids, int T, int k, int E, int each,
-                                                         int quads, const uint16_t* __restrict__ rows,
+                                                         int parts, const uint2* __restrict__ rows,
                                                          int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                                                          int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
     __shared__ int32_t s_cnt[kMaxExperts], s_run[kMaxExperts + 1], s_before[kMaxExperts];
     __shared__ unsigned long long s_mask[kMaxExperts];
-    __shared__ __attribute__((aligned(16))) int32_t s_part[2][4 * kBlock];      // all, those before: [group of rows][E]
-    const int tid = threadIdx.x, groups = min(kBlock / quads, 64), q = tid % quads, g = tid / quads;
+    __shared__ uint4 s_part[2][kBlock];                       // all, those before: [group of rows][piece]
+    const int tid = threadIdx.x, groups = min(kBlock / parts, 64), q = tid % parts, g = tid / parts;
     const int t0 = blockIdx.x * each, t1 = min(t0 + each, T), own = tid / k;
     auto expert = [&](int t) { return own < 64 && t + own < t1 ? ids[int64_t(t) * k + tid] : -1; };
     int e = expert(t0);
     for (int i = tid; i < E; i += kBlock) s_mask[i] = 0;
     if (g < groups) {
-        int4 all = make_int4(0, 0, 0, 0), before = all;
+        uint4 all = make_uint4(0, 0, 0, 0), before = all;
 #pragma unroll 8
         for (int row = g; row < int(gridDim.x); row += groups) {
-            const uint2 c = reinterpret_cast<const uint2*>(rows)[row * quads + q];
-            const int4 v = make_int4(int(c.x & 0xFFFFu), int(c.x >> 16), int(c.y & 0xFFFFu), int(c.y >> 16));
-            const int in = row < int(blockIdx.x) ? -1 : 0;
-            all = make_int4(all.x + v.x, all.y + v.y, all.z + v.z, all.w + v.w);
-            before = make_int4(before.x + (v.x & in), before.y + (v.y & in), before.z + (v.z & in), before.w + (v.w & in));
+            const uint2 c = rows[row * parts + q];
+            const uint4 v = BYTES ? make_uint4(c.x & 0x00FF00FFu, c.x >> 8 & 0x00FF00FFu, c.y & 0x00FF00FFu, c.y >> 8 & 0x00FF00FFu)
+                                  : make_uint4(c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16);
+            const uint32_t in = row < int(blockIdx.x) ? ~0u : 0u;
+            all = make_uint4(all.x + v.x, all.y + v.y, all.z + v.z, all.w + v.w);
+            before = make_uint4(before.x + (v.x & in), before.y + (v.y & in), before.z + (v.z & in), before.w + (v.w & in));
         }
-        reinterpret_cast<int4*>(s_part[0])[g * quads + q] = all;
-        reinterpret_cast<int4*>(s_part[1])[g * quads + q] = before;
+        s_part[0][g * parts + q] = all;
+        s_part[1][g * parts + q] = before;
     }
     __syncthreads();
     const unsigned long long bit = 1ull << (own & 63);
@@ -391,8 +405,16 @@ __global__ __launch_bounds__(kBlock) void k_scored_place(const int32_t* __restri
     for (int i = tid; i < 2 * E; i += kBlock) {
         const int which = i >= E ? 1 : 0, c = i - which * E;
         int sum = 0;
+        if constexpr (BYTES) {
+            // expert 8 p + i: word (i / 4) * 2 + i % 2 of piece p, half i / 2 % 2
+            const uint16_t* from = reinterpret_cast<const uint16_t*>(s_part[which]) + (c & ~7) + (c & 4) + (c & 1) * 2 + (c >> 1 & 1);
 #pragma unroll 8
-        for (int j = 0; j < groups; ++j) sum += s_part[which][j * quads * 4 + c];
+            for (int j = 0; j < groups; ++j) sum += from[j * parts * 8];
+        } else {
+            const int32_t* from = reinterpret_cast<const int32_t*>(s_part[which]) + c;
+#pragma unroll 8
+            for (int j = 0; j < groups; ++j) sum += from[j * parts * 4];
+        }
         (which ? s_before : s_cnt)[c] = sum;
     }
     __syncthreads();
@@ -500,19 +522,19 @@ hipError_t launch_as(const moe_config& c, const moe_route_rule& r, const float* 
         }
         return hipErrorInvalidValue;
     }
-    const int each = scored_each(T), blocks = int((int64_t(T) + each - 1) / each), quads = (E + 3) / 4;
-    const int waves = each * W / kWave < 8 ? each * W / kWave : 8;
-    uint16_t* rows = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + ws_layout(c, T).scored);
+    const int each = scored_each(T), blocks = int((int64_t(T) + each - 1) / each);
+    const int waves = each * W / kWave < 8 ? each * W / kWave : 8, parts = each <= kByteTokens ? (E + 7) / 8 : (E + 3) / 4;
+    uint2* rows = reinterpret_cast<uint2*>(static_cast<char*>(ws) + ws_layout(c, T).scored);
     hipLaunchKernelGGL((k_scored<W, EPL>), dim3(blocks), dim3(waves * kWave), 0, s, logits, bias, T, E, k, R, ids, w, each,
-                       quads, rows);
-    hipLaunchKernelGGL(k_scored_place, dim3(blocks), dim3(kBlock), 0, s, ids, T, k, E, each, quads, rows, counts, offsets,
-                       perm, inv);
+                       parts, rows);
+    const auto place = each <= kByteTokens ? &k_scored_place<true> : &k_scored_place<false>;
+    hipLaunchKernelGGL(place, dim3(blocks), dim3(kBlock), 0, s, ids, T, k, E, each, parts, rows, counts, offsets, perm, inv);
     return hipGetLastError();
 }
 
 // More tokens than this: 16 lanes a token, 32 where a lane of 16 would have more than 16 experts (registers).  256 experts in
 // 8 groups, top 8: 2,048 tokens 18.4 us against 15.5 on waves, 4,096 19.0 against 20.5, 30,000 53 against 84; 512 experts,
-// 8,192 tokens: 34 us on 32 lanes, 38 on waves.
+// 8,192 tokens: 34 us on 32 lanes, 38 on waves (each 3 less since counts are bytes).
 constexpr int kManyTokens = 2048;
 
 // Experts of a lane where W lanes take a token.

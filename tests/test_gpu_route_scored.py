@@ -91,7 +91,8 @@ SHAPES = [(1, 1, 1, 1, 1, 1), (1, 8, 2, 1, 1, 1), (4, 256, 8, 8, 4, 2), (3, 512,
           (333, 510, 7, 17, 9, 1), (200, 65, 3, 13, 13, 2), (97, 12, 4, 2, 1, 2), (640, 7, 7, 7, 7, 1),
           (6, 100, 3, 1, 1, 1), (100, 512, 4, 1, 1, 1), (17, 9, 1, 3, 2, 1), (256, 24, 2, 1, 1, 1), (257, 24, 3, 2, 1, 2), (2049, 64, 1, 1, 1, 1), (2051, 128, 8, 1, 1, 1),
           (2050, 141, 6, 1, 1, 1), (4099, 256, 8, 8, 4, 2), (2100, 300, 5, 1, 1, 1), (2053, 512, 3, 32, 9, 2), (2060, 504, 4, 9, 5, 2),
-          (2070, 48, 16, 16, 16, 2), (20001, 32, 2, 4, 2, 1)]
+          (2070, 48, 16, 16, 16, 2), (20001, 32, 2, 4, 2, 1),
+          (70001, 9, 2, 1, 1, 1)]
 
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
@@ -108,21 +109,29 @@ def test_choice_gates_grouping_and_gradient(T, E, k, groups, keep, top, biased, 
     r.check_gradient(logits, ids, dw)
 
 
-def test_most_tokens():
-    """2^24 tokens, counts of 32,768 tokens a workgroup (16 bits); all of one workgroup's with one expert."""
-    T, E = 1 << 24, 2
-    r = Router(E, 1, T, "sigmoid", renorm=0)
-    logits = torch.randn((T, E), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
-    logits[32768:65536, 0] = 9.0
+@pytest.mark.parametrize("T", [64512, 64513, 1 << 24])
+def test_many_tokens_to_one_expert(T):
+    """The most tokens whose counts are bytes and one more; 2^24 tokens, 32,768 a workgroup (counts of 16 bits)."""
+    E = 2
+    for favour in (9.0, 0.0):
+        r = Router(E, 1, T, "sigmoid", renorm=0)
+        logits = torch.randn((T, E), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+        logits[32768:65536, 0] = 9.0
+        logits[:, 1] += favour * (T < 1 << 20)
+        r.forward(logits, None)
+        torch.cuda.synchronize()
+        ids = (logits[:, 1] > logits[:, 0]).int()
+        assert torch.equal(r.ids[:T], ids)
+        order = torch.sort(ids, stable=True).indices.int()
+        assert torch.equal(r.perm[:T], order)
+        assert torch.equal(r.perm[:T][r.inv[:T].long()], torch.arange(T, dtype=torch.int32, device="cuda"))
+        n = int((ids == 0).sum())
+        assert r.counts[:2].tolist() == [n, T - n] and r.offsets[:3].tolist() == [0, n, T]
+    r = Router(E, 1, T, "softmax", renorm=0)
+    logits[:, 0], logits[:, 1] = 1.0, -1.0
     r.forward(logits, None)
     torch.cuda.synchronize()
-    ids = (logits[:, 1] > logits[:, 0]).int()
-    assert torch.equal(r.ids[:T], ids)
-    order = torch.sort(ids, stable=True).indices.int()
-    assert torch.equal(r.perm[:T], order)
-    assert torch.equal(r.perm[:T][r.inv[:T].long()], torch.arange(T, dtype=torch.int32, device="cuda"))
-    n = int((ids == 0).sum())
-    assert r.counts[:2].tolist() == [n, T - n] and r.offsets[:3].tolist() == [0, n, T]
+    assert r.counts[:2].tolist() == [T, 0] and bool((r.perm[:T] == torch.arange(T, device="cuda")).all())
 
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
