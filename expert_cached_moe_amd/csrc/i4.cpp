@@ -49,8 +49,9 @@ ExpertWork expert_work(const moe_config& c, int64_t T) {
 }
 
 hipError_t launch_dense(int what, const Product& p, hipStream_t s) {
-    if (p.T <= kFewTokens) return launch_i4_few(what, p, nullptr, s);
-    const int kind = plan_dense(p.T, p.N, p.K, p.planes, dense::compute_units());
+    const int n_cu = dense::compute_units();
+    if (few_dense(p.T, p.N, p.K, n_cu)) return launch_i4_few(what, p, nullptr, s);
+    const int kind = plan_dense(p.T, p.N, p.K, p.planes, n_cu);
     return kind == kTurns ? launch_i4_turns(what, p, nullptr, nullptr, 0, s) : launch_i4_mid(what, kind, p, nullptr, nullptr, 0, s);
 }
 

@@ -79,7 +79,7 @@ hipError_t launch_i4_mid(int what, int kind, const Product& p, const ExpertList*
                          hipStream_t s);
 hipError_t launch_i4_turns(int what, const Product& p, const ExpertList* list, const void* map, int64_t max_tiles,
                            hipStream_t s);
-// Up to 8 rows of x, dense; experts: entries of few rows.
+// Few rows of x (few_dense); experts: up to 8 tokens.
 hipError_t launch_i4_few(int what, const Product& p, const ExpertList* list, hipStream_t s);
 
 }  // namespace i4

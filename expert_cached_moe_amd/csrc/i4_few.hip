@@ -394,7 +394,7 @@ hipError_t choose(const Product& p, const ExpertList* list, hipStream_t s) {
 
 hipError_t launch_i4_few(int kind, const Product& p, const ExpertList* list, hipStream_t s) {
     if (p.T == 0) return hipSuccess;
-    if (p.T > kFewTokens) return hipErrorInvalidValue;
+    if (list && p.T > kFewTokens) return hipErrorInvalidValue;      // (more blocks than a workgroup lists)
     const bool parts = p.planes == 3;
     switch (kind) {
         case kOut16: return parts ? choose<kOut16, 3>(p, nullptr, s) : choose<kOut16, 1>(p, nullptr, s);

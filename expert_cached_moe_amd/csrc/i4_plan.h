@@ -8,11 +8,18 @@
 namespace moe {
 namespace i4 {
 
-// Up to 8 rows of x: the few-row kernel (100003 x 4096 at 8 tokens 77-82 us against 93 on tiles of 32 rows, 4096 x 4096
+// Up to 8 rows of x, and by expert up to 8 tokens: the few-row kernel (100003 x 4096 at 8 tokens 77-82 us against 93 on tiles of 32 rows, 4096 x 4096
 // 7.8 against 8.8; at 16 tokens, in two blocks of 8, 12.8 against 8.9).  By expert too: 128 of 2048 x 768, top 8, at 8
 // tokens 43 us against 49 on tiles, at 16 tokens 68 against 61; 256 of 4096 x 1536 and the shared one, top 6, 106
 // against 123 and 173 against 168.
 constexpr int kFewTokens = 8;
+// Dense products of more rows too, where blocks of 8 rows by 16 of the weights leave a CU one workgroup at most and rows
+// are long: the tiles' waves split K no further than the few-row kernel's, and wait for each slice (16 x 2048 x 12288 13.3 us
+// against 21.5, in fp32 parts 32 x 1024 x 12288 31 and 49, 128 x 256 x 8192 9.6 and 12.9; 32 x 1024 x 1024 4.6 both; two
+// workgroups a CU, 64 x 1024 x 8192: 17.1 against 13.2).
+inline bool few_dense(int64_t T, int64_t N, int64_t K, int n_cu) {
+    return T <= kFewTokens || (K > 1024 && (N + 15) / 16 * ((T + kFewTokens - 1) / kFewTokens) <= n_cu);
+}
 
 // The kernels for more rows: tiles of `rows` of x by `cols` of the weights, K split over `split` groups of waves,
 // up to `slots` workgroups a CU.  A slice of 64 k takes `one` us with one workgroup on each CU and `more` for each further

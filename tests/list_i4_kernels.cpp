@@ -11,7 +11,7 @@ int main() {
     while (std::scanf(" %c", &what) == 1) {
         if (what == 'm') {
             if (std::scanf("%lld %lld %lld %lld", &a, &N, &K, &b) != 4) return 1;
-            std::printf("%d\n", a <= kFewTokens ? -1 : plan_dense(a, N, K, int(b), 256));
+            std::printf("%d\n", few_dense(a, N, K, 256) ? -1 : plan_dense(a, N, K, int(b), 256));
         } else {
             if (std::scanf("%lld %lld %lld %lld", &a, &b, &N, &K) != 4) return 1;
             std::printf("%d\n", plan_experts(int(a), b, N, K, 256));

@@ -169,7 +169,7 @@ def test_matmul(ctx, T, N, K, group, xt, yt, pad, off):
 
 # (each kind of tiles: tests/test_i4_coverage_cpu.py)
 TILES = [(40, 4230, 416), (90, 4230, 160), (9, 8202, 160), (70, 8202, 288), (68, 8202, 256), (40, 20028, 96), (70, 61128, 416), (214, 61128, 288),
-         (300, 40003, 352), (333, 61003, 96), (70, 61003, 96)]
+         (300, 40003, 352), (333, 61003, 96), (70, 61003, 96), (33, 4150, 4128), (70, 4100, 1120), (130, 4100, 2080)]
 
 
 @pytest.mark.parametrize("T,N,K", TILES)

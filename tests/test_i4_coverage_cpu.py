@@ -57,7 +57,7 @@ def test_every_kind_is_taken_over_the_range(kinds):
         return max(step, min(hi // step * step, round(lo * (hi / lo) ** r.random() / step) * step))
 
     for planes in (1, 3):
-        assert kinds([f"m {some(9, 8192)} {some(1, 100003)} {some(32, 12288, 32)} {planes}" for _ in range(20000)]) == KINDS
+        assert kinds([f"m {some(9, 8192)} {some(1, 100003)} {some(32, 12288, 32)} {planes}" for _ in range(20000)]) == KINDS | {-1}
     shapes = [(some(64, 8192, 64), some(32, 8192, 32), some(1, 256), r.randint(1, 8), r.randint(0, 1), some(9, 8192))
               for _ in range(20000)]
     for calls in experts(shapes):
