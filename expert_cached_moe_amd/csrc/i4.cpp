@@ -136,7 +136,6 @@ int moe_i4_matmul(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, i
     p.w = Rows{d_w, d_words, d_exps, (K + group - 1) / group, shift_of(group)};
     p.out = d_y;
     p.ldo = ld_y;
-    p.wide = aligned(d_y, 4) && ld_y % 2 == 0;
     const int kind = y_type == MOE_A_F32 ? kOut32 : kOut16;
     hipError_t e = launch_dense(kind, p, s);
     return e == hipSuccess ? MOE_OK : hip_fail(ctx, e, "moe_i4_matmul launch");

@@ -58,7 +58,6 @@ struct Product {
     Rows w;
     void* out;
     int64_t ldo;
-    int32_t wide;            // dense: every even column of out lies on 4 bytes
     int64_t T;
     // experts: entry i of the list, its places offsets[e] .. offsets[e + 1] - 1 in expert order
     const int32_t *offsets, *perm;

@@ -32,7 +32,7 @@ using dev::kWave;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((address_space(3))) void lds_void;
 typedef uint32_t __attribute__((ext_vector_type(4), aligned(4))) words4;
-typedef uint32_t __attribute__((ext_vector_type(2), aligned(4))) words2;
+typedef uint32_t __attribute__((ext_vector_type(2), aligned(2))) halves4;   // (odd rows of bf16 results lie on 2 bytes)
 
 constexpr int kSlice = 128;                  // bytes of a row of x in a slice
 
@@ -154,8 +154,8 @@ __device__ __forceinline__ void finish_sums(const Product& p, const dev::f32x4 (
                 }
             } else {
                 uint16_t* o = static_cast<uint16_t*>(p.out) + to * p.ldo + (GATE ? nn / 32 * 16 + nn % 16 : nn);
-                if (EXPERTS || (p.wide && nn + 4 <= p.N)) {
-                    *reinterpret_cast<words2*>(o) = words2{dev::pack_bf16x2(v[0], v[1]), dev::pack_bf16x2(v[2], v[3])};
+                if (EXPERTS || nn + 4 <= p.N) {
+                    *reinterpret_cast<halves4*>(o) = halves4{dev::pack_bf16x2(v[0], v[1]), dev::pack_bf16x2(v[2], v[3])};
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
