@@ -47,8 +47,8 @@ struct WsLayout {
 };
 int64_t gemm_tile_ints(const moe_config& c, int32_t T);  // tile-list entries of the grouped GEMM
 WsLayout ws_layout(const moe_config& c, int32_t max_T);
-// The router by scores: one workgroup without scratch takes a wave's tokens each (64 tokens, top 1: 16.8 us where several
-// workgroups and the second launch take 10; 9 tokens, top 8: 10.7 and 9.4).
+// The router by scores: one workgroup, a wave a token, without scratch (more tokens than waves: 64, top 1, 16.8 us where several
+// workgroups and the second launch take 8).
 inline bool scored_alone(int64_t T, int k) { return T <= 16 && T * k <= 64; }
 // Tokens of a workgroup otherwise: 256 workgroups at most, a multiple of 4 tokens (256 experts, top 8, 1,024 tokens: 11.6 us,
 // 12.2 with a multiple of 8; 2,048 tokens 12.4, 16.7 with 16), and counts that fit 16 bits.
@@ -147,9 +147,6 @@ hipError_t launch_route(const moe_config& c, const float* logits, int32_t T, int
                         int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv, void* ws,
                         hipStream_t s);
 
-// Counting sort of the pairs of ids [T][k] by expert, for any T (workspace as moe_route's).
-hipError_t launch_permute(const moe_config& c, int32_t T, const int32_t* ids, int32_t* counts, int32_t* offsets,
-                          int32_t* perm, int32_t* inv, void* ws, hipStream_t s);
 // Router by scores with a bias and groups, and its gradient (route_scored.hip).
 hipError_t launch_route_scored(const moe_config& c, const moe_route_rule& r, const float* logits, const float* bias,
                                int32_t T, int32_t* ids, float* w, int32_t* counts, int32_t* offsets, int32_t* perm,

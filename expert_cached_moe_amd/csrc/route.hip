@@ -23,6 +23,88 @@ namespace {
 
 using namespace routing;
 
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+// Wave-wide maximum of an unsigned key, left in every lane: butterflies inside each row of
+// 16 lanes (DPP quad swaps, rotations by 4 and 8), then row pairs and wave halves exchanged
+// with permlane16_swap / permlane32_swap.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_umax(uint32_t a) {
+    return max(a, uint32_t(__builtin_amdgcn_mov_dpp(int(a), CTRL, 0xF, 0xF, false)));
+}
+__device__ __forceinline__ uint32_t wave_umax(uint32_t a) {
+    a = dpp_umax<0xB1>(a);   // quad_perm [1,0,3,2]
+    a = dpp_umax<0x4E>(a);   // quad_perm [2,3,0,1]
+    a = dpp_umax<0x124>(a);  // row_ror:4
+    a = dpp_umax<0x128>(a);  // row_ror:8
+    const auto h16 = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    a = max(h16[0], h16[1]);
+    const auto h32 = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+    return max(h32[0], h32[1]);
+}
+
+// Lanes of the wave holding the same expert id (10-bit ids), among lanes with valid = 1.
+__device__ __forceinline__ uint64_t match_expert(int e, bool valid) {
+    uint64_t m = __ballot(valid);
+#pragma unroll
+    for (int b = 0; b < 10; ++b) {
+        const bool bit = valid && ((e >> b) & 1);
+        const uint64_t bb = __ballot(bit);
+        m &= bit ? bb : ~bb;
+    }
+    return valid ? m : 0;
+}
+
+// Stable scatter of one chunk of up to 1024 pairs: pair p = p0 + tid with expert
+// e = ids[tid].  run[e] is the output position of the chunk's first pair of expert
+// e; it is advanced by the chunk's count.  wc: [16][E] per-wave counts (LDS).
+__device__ inline void scatter_chunk(const int32_t* __restrict__ ids_src, int p0, int n_valid, int E,
+                              int32_t* __restrict__ run, int32_t (*wc)[kMaxExperts],
+                              int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
+    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+    const bool valid = tid < n_valid;
+    const int e = valid ? ids_src[tid] : 0;
+    const uint64_t m = match_expert(e, valid);
+    const uint64_t lt = (lane == 0) ? 0ull : (~0ull >> (kWave - lane));
+    const int rank = __popcll(m & lt);
+    const int cw = __popcll(m);
+    for (int i = tid; i < kRouteWaves * E; i += kBlock) wc[i / E][i % E] = 0;
+    __syncthreads();
+    if (valid && rank == 0) wc[wave][e] = cw;
+    __syncthreads();
+    if (valid) {
+        int pos = run[e] + rank;
+        for (int w2 = 0; w2 < wave; ++w2) pos += wc[w2][e];
+        perm[pos] = p0 + tid;
+        inv[p0 + tid] = pos;
+    }
+    __syncthreads();
+    for (int ee = tid; ee < E; ee += kBlock) {
+        int s = 0;
+#pragma unroll
+        for (int w2 = 0; w2 < kRouteWaves; ++w2) s += wc[w2][ee];
+        run[ee] += s;
+    }
+    __syncthreads();
+}
+
+// Grouping of up to 4096 pairs by one workgroup: s_ids [n] in LDS (written by every thread that
+// takes part; the call begins with a count and ends with every output stored).
+__device__ inline void group_small(const int32_t* __restrict__ s_ids, int n, int E, int32_t* __restrict__ s_cnt,
+                            int32_t* __restrict__ s_run, int32_t (*s_wc)[kMaxExperts], int32_t* __restrict__ counts,
+                            int32_t* __restrict__ offsets, int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
+    const int tid = threadIdx.x;
+    for (int e = tid; e < E; e += kBlock) s_cnt[e] = 0;
+    __syncthreads();
+    for (int p = tid; p < n; p += kBlock) atomicAdd(&s_cnt[s_ids[p]], 1);
+    __syncthreads();
+    wave0_scan(s_cnt, E, s_run, offsets, counts);
+    __syncthreads();
+    for (int p0 = 0; p0 < n; p0 += kBlock) scatter_chunk(s_ids + p0, p0, n - p0, E, s_run, s_wc, perm, inv);
+}
+
 // Route one token with one wave.  EPL = experts per lane (ceil(E/64)); lane l holds experts
 // l + 64 i.  k rounds: the wave-wide maximum of the logit keys, then the lowest expert id
 // holding it (ballots per slot i, lowest slot first, then lowest lane, since the id is
@@ -244,13 +326,6 @@ hipError_t launch_route(const moe_config& c, const float* logits, int32_t T, int
     }
     hipLaunchKernelGGL(k_route, dim3((T + kRouteWaves - 1) / kRouteWaves), dim3(kBlock), 0, s, logits, T, E, k,
                        c.renormalize, ids, w);
-    return launch_permute(c, T, ids, counts, offsets, perm, inv, ws, s);
-}
-
-hipError_t launch_permute(const moe_config& c, int32_t T, const int32_t* ids, int32_t* counts, int32_t* offsets,
-                          int32_t* perm, int32_t* inv, void* ws, hipStream_t s) {
-    const int E = c.n_experts;
-    const int64_t n = int64_t(T) * c.top_k;
     const WsLayout L = ws_layout(c, T);
     int32_t* hist = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + L.hist);
     int32_t* base = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + L.base);
