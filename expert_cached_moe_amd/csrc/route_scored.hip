@@ -447,7 +447,8 @@ __global__ __launch_bounds__(kBlock) void k_scored_place(const int32_t* __restri
 // Gradient of the logits from the gates', one wave a token.  With p the softmax or sigmoid score,
 // S the sum of the chosen scores and a_j = p_j / S:
 //   gates scale * a_j:  ds_j = scale (dw_j - sum_i dw_i a_i) / S;   gates scale * p_j:  ds_j = scale dw_j
-//   sigmoid:  dl_j = ds_j p_j (1 - p_j) for the chosen, 0 for the others;
+//   sigmoid:  dl_j = ds_j p_j (1 - p_j) for the chosen, 0 for the others.  Renormalised, ds_j p_j is formed as
+//             scale (dw_j - sum_i dw_i a_i) a_j: S can be as small as the least 64-bit number, a quotient by it infinite;
 //   softmax:  dl_e = p_e (ds_e - sum_j ds_j p_j), ds_e = 0 for the others.  Renormalised, that is
 //             scale a_j (dw_j - sum_i dw_i a_i) for the chosen and 0 for the others.
 __global__ __launch_bounds__(256) void k_scored_backward(const float* __restrict__ logits, int T, int E, int k,
@@ -488,8 +489,8 @@ __global__ __launch_bounds__(256) void k_scored_backward(const float* __restrict
     if (R.renorm) {
         double S = sum_lanes(p);
         if (S == 0.0) S = 1.0;
-        const double a = p / S, x = d - sum_lanes(d * a);
-        v = R.sigmoid ? x / S * p * sigmoid64(-double(l)) : a * x;
+        const double a = p / S, x = a * (d - sum_lanes(d * a));
+        v = R.sigmoid ? x * sigmoid64(-double(l)) : x;
     } else if (R.sigmoid) {
         v = d * p * sigmoid64(-double(l));
     } else {

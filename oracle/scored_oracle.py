@@ -43,27 +43,37 @@ def gates(s, ids, renorm, scale):
     return scale * p
 
 
-def backward(logits, ids, dw, kind, renorm, scale):
-    """dL/dlogits of gates(scores(logits)) for fixed ids."""
-    s = scores(logits, kind)
-    p = np.take_along_axis(s, ids, 1)
-    d = scale * np.asarray(dw, np.float64)
+def shares(logits, ids, kind):
+    """The chosen scores over their sum, 0 where that is 0."""
+    p = np.take_along_axis(scores(logits, kind), ids, 1)
+    total = p.sum(1, keepdims=True)
+    return p / np.where(total == 0, 1.0, total)
+
+
+def gates_of(logits, ids, kind, renorm, scale):
     if renorm:
-        total = p.sum(1, keepdims=True)
-        total = np.where(total == 0, 1.0, total)
-        ds = (d - (d * p).sum(1, keepdims=True) / total) / total
-    else:
-        ds = d
+        return scale * shares(logits, ids, kind)
+    return gates(scores(logits, kind), ids, 0, scale)
+
+
+def backward(logits, ids, dw, kind, renorm, scale):
+    """dL/dlogits of the gates of fixed ids."""
+    d = scale * np.asarray(dw, np.float64)
+    s = scores(logits, kind)
+    if renorm:
+        # (products of shares, which are 1 at most: a sum of scores can be the least of 64-bit numbers)
+        a = shares(logits, ids, kind)
+        d = (d - (d * a).sum(1, keepdims=True)) * a
+        if kind == "sigmoid":
+            d = d * sigmoid(-np.take_along_axis(np.asarray(logits, np.float64), ids, 1))
+        out = np.zeros_like(s)
+        np.put_along_axis(out, ids, d, 1)
+        return out
     full = np.zeros_like(s)
-    np.put_along_axis(full, ids, ds, 1)
+    np.put_along_axis(full, ids, d, 1)
     if kind == "sigmoid":
         return full * s * sigmoid(-np.asarray(logits, np.float64))
-    out = s * (full - (ds * p).sum(1, keepdims=True))
-    if renorm:                                  # the chosen share the gradient among themselves
-        chosen = np.zeros(s.shape, bool)
-        np.put_along_axis(chosen, ids, True, 1)
-        out[~chosen] = 0.0
-    return out
+    return s * (full - (d * np.take_along_axis(s, ids, 1)).sum(1, keepdims=True))
 
 
 def group_pairs(ids, E):

@@ -1,0 +1,43 @@
+"""The router by scores and its gradient where scores leave the ordinary range: sigmoids near the end of
+64-bit numbers."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+B = pytest.importorskip("expert_cached_moe_amd.binding")
+from oracle import scored_oracle as S  # noqa: E402
+from test_gpu_route_scored import Router, cuda  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+LEAST = 2.0 ** -1074                     # the least 64-bit number
+
+
+@pytest.mark.parametrize("T", [6, 40, 2105])
+def test_gradient_of_renormalised_sigmoids_near_the_end_of_64_bits(T):
+    """Chosen logits between -735 and -700: their scores and the sum are as small as 1e-320, the gradient is not."""
+    E, k = 12, 4
+    rng = np.random.default_rng(T)
+    logits = np.full((T, E), -np.inf, np.float32)
+    for t in range(T):
+        logits[t, rng.permutation(E)[:k + 2]] = rng.uniform(-735, -700) + rng.uniform(-3, 3, k + 2)
+    logits[0, :4], logits[0, 4:] = [-720, -721, -722, -800], -np.inf
+    dw = rng.normal(size=(T, k)).astype(np.float32)
+    r = Router(E, k, T, "sigmoid", renorm=1, scale=2.5)
+    dl = cuda(logits)
+    r.forward(dl, None)
+    r.backward(dl, cuda(dw))
+    ids, w = r.results()
+    d = r.d[:T * E].cpu().numpy().reshape(T, E)
+    s, ref = S.choose(logits, None, k, "sigmoid")
+    assert np.array_equal(ids, ref)
+    # a score is off by the least number at most, here and in the oracle, so a share by (k + 1) of them over the sum, and
+    # the gradient by that for its own share and for each term of its sum
+    total = np.take_along_axis(s, ids, 1).sum(1, keepdims=True)
+    off = 2 * (k + 1) * LEAST / total
+    gates = S.gates_of(logits, ids, "sigmoid", 1, 2.5)
+    assert (np.abs(w - gates) <= np.abs(gates) * 2.0 ** -23 + 2.5 * off).all()
+    want = S.backward(logits, ids, dw, "sigmoid", 1, 2.5)
+    size = 2.5 * np.abs(dw).sum(1, keepdims=True)
+    assert np.isfinite(d).all()
+    assert (np.abs(d - want) <= np.abs(want) * 2.0 ** -24 + size * (2.0 ** -46 + 2 * off) + 2.0 ** -149).all()
