@@ -4,7 +4,8 @@
 // gates: c_e = s_e + b_e.  Experts lie in groups of consecutive ids; a group counts as the sum of
 // its one or two largest c_e, the best groups are kept, and of their experts the k with the
 // largest c_e are chosen (without a bias: the largest logit, which is the same order, exact).
-// Gates: scale * s_e, divided by the sum of the chosen scores where they are renormalised.
+// Gates: scale * s_e, divided by the sum of the chosen scores where they are renormalised (softmax: that over the
+// chosen logits).
 //
 // The choice has to be that of the formula wherever it is run, so scores, biased values and group
 // sums are 64-bit numbers: two experts closer than fp32's rounding of a score (2^-24) occur in every
@@ -301,7 +302,11 @@ __device__ __forceinline__ int scored_token(const float* __restrict__ lrow, cons
     // gates
     const bool chosen = act && l < k;
     const float my_l = chosen ? lrow[mine] : 0.0f;
-    double s = chosen ? (R.sigmoid ? sigmoid64(my_l) : share64(my_l, m) / den) : 0.0;
+    // (renormalised softmax: of the chosen logits alone.  Where the largest is not among them they can lie so far below it
+    // that their parts of the whole row's sum are 0)
+    const bool alone = R.renorm && !R.sigmoid;
+    if (alone) m = across<16>(chosen ? my_l : -INFINITY, Max{});
+    double s = chosen ? (R.sigmoid ? sigmoid64(my_l) : share64(my_l, m) / (alone ? 1.0 : den)) : 0.0;
     if (R.renorm) {
         const double total = across<16>(s, Add{});            // k <= 16
         if (total != 0.0) s /= total;

@@ -216,7 +216,9 @@ int moe_route(moe_ctx* ctx, const float* d_logits, int32_t T, int32_t* d_topk_id
  *   the k experts with the largest c_e are chosen, lower id first on equal values (without a bias:
  *   with the largest logits, the same order without rounding);
  *   gate_e = scale * s_e (the bias has no part in it), divided by the chosen scores' sum with
- *   rule->renormalize (where that sum is 0 the gates are 0).
+ *   rule->renormalize (where that sum is 0 the gates are 0: sigmoids of logits below -745, and chosen logits of
+ *   -infinity alone; renormalised softmax gates are the softmax of the chosen logits, however far these lie below
+ *   the row's largest).
  * s, c and the groups' values are 64-bit numbers, so that the choice does not depend on fp32's
  * rounding of a score; gates are rounded once to fp32.  cfg.renormalize has no part in it.
  *   d_logits [T][E] fp32; d_bias [E] fp32 or NULL; the rest as moe_route (d_ws: moe_workspace_bytes,

@@ -44,7 +44,10 @@ def gates(s, ids, renorm, scale):
 
 
 def shares(logits, ids, kind):
-    """The chosen scores over their sum, 0 where that is 0."""
+    """The chosen scores over their sum, 0 where that is 0; softmax: that of the chosen logits, however far they lie
+    below the row's largest."""
+    if kind == "softmax":
+        return scores(np.take_along_axis(np.asarray(logits, np.float64), ids, 1), kind)
     p = np.take_along_axis(scores(logits, kind), ids, 1)
     total = p.sum(1, keepdims=True)
     return p / np.where(total == 0, 1.0, total)

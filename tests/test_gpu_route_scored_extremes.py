@@ -1,5 +1,5 @@
 """The router by scores and its gradient where scores leave the ordinary range: sigmoids near the end of
-64-bit numbers."""
+64-bit numbers, chosen logits far below the row's largest."""
 import numpy as np
 import pytest
 
@@ -41,3 +41,40 @@ def test_gradient_of_renormalised_sigmoids_near_the_end_of_64_bits(T):
     size = 2.5 * np.abs(dw).sum(1, keepdims=True)
     assert np.isfinite(d).all()
     assert (np.abs(d - want) <= np.abs(want) * 2.0 ** -24 + size * (2.0 ** -46 + 2 * off) + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("T", [6, 40, 2106])
+@pytest.mark.parametrize("how", ["bias", "groups"])
+def test_chosen_logits_far_below_the_largest(T, how):
+    """The largest logit is not chosen, by its bias or by its group, and the chosen ones lie up to 90,000 below it:
+    renormalised, they share the gates among themselves, and the gradient is that of these gates."""
+    E, k = 24, 4
+    rng = np.random.default_rng(T)
+    low = -np.exp(rng.uniform(np.log(600), np.log(90000), (T, 1)))
+    logits = (low + rng.normal(size=(T, E)) * 2).astype(np.float32)
+    logits[0, :5] = [0, -800, -801, -802, -803]
+    logits[0, 5:] = -900
+    bias = np.zeros(E, np.float32)
+    if how == "bias":
+        logits[:, 0] = 0
+        bias[0] = -np.inf
+        groups, keep = 1, 1
+    else:
+        # (the first group's best is the row's largest; the others win by their bias)
+        logits[:, 0] = 0
+        logits[:, 1:6] = -np.inf
+        bias[6:] = 2.0
+        groups, keep = 4, 3
+    bias[1:] += rng.permutation(E - 1).astype(np.float32) * np.float32(2.0 ** -10)
+    dw = rng.normal(size=(T, k)).astype(np.float32)
+    r = Router(E, k, T, "softmax", groups, keep, 1, 1, 2.5)
+    dl = cuda(logits)
+    r.forward(dl, cuda(bias))
+    r.backward(dl, cuda(dw))
+    ids, w = r.results()
+    _, ref = S.choose(logits, bias, k, "softmax", groups, keep, 1)
+    assert np.array_equal(ids, ref) and (ids != 0).all()
+    gates = S.gates_of(logits, ids, "softmax", 1, 2.5)
+    assert (np.abs(gates.sum(1) - 2.5) < 1e-12).all()
+    assert (np.abs(w - gates) <= np.abs(gates) * (2.0 ** -24 + 2.0 ** -46) + 2.0 ** -149).all()
+    r.check_gradient(logits, ids, dw)

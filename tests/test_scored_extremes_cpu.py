@@ -1,5 +1,5 @@
 """The 64-bit form of the router's gates and gradient against 60-digit numbers, where scores are near the end of
-64-bit numbers."""
+64-bit numbers or far below the row's largest."""
 import decimal
 
 import numpy as np
@@ -30,9 +30,10 @@ def exactly(logits, ids, dw, kind, scale):
 
 ROWS = [[-720, -721, -722, -1000, -1000, -1000], [-733.5, -735, -734.25, -735.5, -736, -900], [-709, -712, -744, -709.5, -800, -745],
         [3, 2.5, -720, 1, 0, -3], [40, 36.5, 33, 30, 1, 0]]
+LOW = [[-800, -801, -802, 0, -900, -900], [-2e5, -200000.5, -199999.25, 12, 11, -3e5], [-746, -747, -745.5, 0, 0, 0], [1, 2, 3, 4, 0, -1]]
 
 
-@pytest.mark.parametrize("kind,rows", [("sigmoid", ROWS), ("softmax", ROWS[:1] + ROWS[4:])])
+@pytest.mark.parametrize("kind,rows", [("sigmoid", ROWS), ("softmax", LOW + ROWS)])
 def test_gates_and_gradient_against_many_digits(kind, rows):
     k, scale = 3, 2.5
     rng = np.random.default_rng(3)
