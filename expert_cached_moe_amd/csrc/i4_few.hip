@@ -7,8 +7,10 @@
 // group.  Codes become bf16 numbers 0..15 by three masks and shifts and four conversions per eight (bytes
 // 0..15 are e4m3 numbers 2^-9 times themselves), eight instructions of the matrix unit sum x * code over
 // the piece for four tokens, started with -z * (sum of x), which gives sum x * (code - z); four
-// multiply-adds add that, times s, to the sums.  So a code takes 1.2 operations of a lane for up to 4 tokens
-// and 1.4 for 8, of the 3.3 that there is time for; scaling every weight would take 2.4.
+// multiply-adds add that, times s and the row's power of two, to the sums.  So a code takes 1.2 operations of a lane
+// for up to 4 tokens and 1.4 for 8, of the 3.3 that there is time for; scaling every weight would take 2.4.  The power of
+// two takes part in each step, and not once at the end, because sums without it leave fp32 at one end or the other: of x
+// from 2^103 up in rows of small weights, or of x below 2^-94 in rows of large ones (it costs 1-3%).
 //
 // The waves of a workgroup split K (by chunks of 512); sums meet once a
 // unit of rows, across the blocks in registers, across the waves in LDS, in a fixed order.  Every tile's
@@ -40,8 +42,6 @@ typedef __attribute__((ext_vector_type(4))) short s16x4;
 
 constexpr int kChunk = 512, kMaxWaves = 8, kStream = 2;       // cache policy of a non-temporal load
 constexpr int kFewBlocks = kFewTokens * kMaxTopK + 2;          // of up to 4 rows: a block a pair at most, the shared expert's two
-// The row's power of two comes last; until then sums are held 2^-32 times as large, in range whatever x is.
-constexpr float kDown32 = 2.3283064365386963e-10f;
 constexpr uint32_t kOutside = 0xFFFFFFF0u, kRange = 0x80000000u;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p) {
@@ -69,13 +69,14 @@ __device__ __forceinline__ s16x4 codes4(uint32_t even, uint32_t odd) {
     return __builtin_bit_cast(s16x4, u);
 }
 
+// 512 times a group's scale times its row's 2^(e - 127); 255 is NaN
+__device__ __forceinline__ float row_and_group(uint32_t word, uint32_t e) {
+    return __builtin_amdgcn_ldexpf(word_scale(e == 255u ? 0x7Fu : word), int(e) - 118);
+}
+
 // Waves on a SIMD: what the registers allow.
 template <int MAXMT, int P>
 constexpr int kWavesPerSimd = MAXMT * P == 1 ? 4 : MAXMT * P <= 3 ? 3 : 2;
-
-__device__ __forceinline__ float scaled(float sum, uint32_t e) {
-    return e == 255u ? __uint_as_float(0x7FC00000u) : __builtin_ldexpf(sum, int(e) - 127 + 32);
-}
 
 struct Few {
     int kw;                  // waves along K
@@ -162,8 +163,8 @@ k_i4_few(const Product p, const ListOf<KIND> list, const Few f) {
     auto tile_row = [](int r) { return GATE ? r / (R / 2) * 16 + r % (R / 2) * 4 : r * 4; };
 
     dev::u32x4 w[R];
-    uint32_t word[R];
-    __amdgpu_buffer_rsrc_t rc = rsrc(p.w.codes), rg = rsrc(p.w.words);
+    uint32_t word[R], ex[R];
+    __amdgpu_buffer_rsrc_t rc = rsrc(p.w.codes), rg = rsrc(p.w.words), re = rsrc(p.w.exps);
     uint32_t first = 0, left = 0;                               // first row of the unit, and rows behind it
     auto aim = [&](int u) {
         const Entry e = entry_of(u);
@@ -171,6 +172,7 @@ k_i4_few(const Product p, const ListOf<KIND> list, const Few f) {
         const Rows rows = rows_at(p.w, e.offset);
         rc = rsrc(rows.codes + int64_t(n0) * (p.K / 2));
         rg = rsrc(rows.words + int64_t(n0 & ~15) * p.w.groups);
+        re = rsrc(rows.exps + n0);
         first = uint32_t(n0);
         left = uint32_t(p.N - 1 - n0);
     };
@@ -187,6 +189,7 @@ k_i4_few(const Product p, const ListOf<KIND> list, const Few f) {
             rc, in ? row * uint32_t(p.K / 2) + uint32_t(piece) * 16 : kOutside, 0, kStream));
         word[r] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(
             rg, in ? word_of(row, uint32_t(piece) * 32 >> p.w.shift) * 2 : kOutside, 0, 0));
+        ex[r] = uint8_t(__builtin_amdgcn_raw_buffer_load_b8(re, row, 0, 0));
     };
 
     // this workgroup's units.  Experts: a run of them, so that it changes entries seldom; else all workgroups
@@ -233,21 +236,11 @@ k_i4_few(const Product p, const ListOf<KIND> list, const Few f) {
             auto place = [&](int v) { return (v / Q * 4 + row % 4) * Q + v % Q; };
             return Item{n, t, place(v), place(v + 2 * R), i < ITEMS && t < e.count && n < p.N};
         };
-        // what finishing an item reads: its rows' exponents, and its row of out
-        struct Needs {
-            uint32_t exp, up;
-            int32_t to;
+        // its row of out
+        auto row_of = [&](const Item& i) {
+            return i.live ? int32_t(EXPERTS ? row_out<KIND>(p, e.shared, e.base, i.t) : int64_t(e.base) + i.t) : 0;
         };
-        auto needs = [&](const Item& i) {
-            Needs n{0, 0, 0};
-            if (!i.live) return n;
-            const uint8_t* exps = p.w.exps + e.offset;
-            n.exp = exps[i.n];
-            if constexpr (GATE) n.up = exps[i.n + 16];
-            n.to = int32_t(EXPERTS ? row_out<KIND>(p, e.shared, e.base, i.t) : int64_t(e.base) + i.t);
-            return n;
-        };
-        Needs first{0, 0, 0};
+        int32_t first = 0;
         for (int pass = 0; pass < passes; ++pass) {
             const int piece = (pass * f.kw + wave) * 16 + block;
             if (fresh || passes > 1) {
@@ -276,15 +269,15 @@ k_i4_few(const Product p, const ListOf<KIND> list, const Few f) {
             }
             const bool last = pass + 1 == passes;
             if (last) {
-                // what finishing reads, ahead of the next unit's weights (a wait for a load waits for every older
-                // one; a thread has one item with four waves along K and more)
-                first = needs(item(0));
+                // (ahead of the next unit's weights: a wait for a load waits for every older one; a thread has one item
+                // with four waves along K and more)
+                first = row_of(item(0));
                 if (next < end) aim(next);
             }
             const int ahead = last ? 0 : pass + 1;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float s = word_scale(word[r]) * (512.0f * kDown32), z = -word_zero(word[r]);
+                const float s = row_and_group(word[r], ex[r]), z = -word_zero(word[r]);
                 s16x4 b[8];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -334,17 +327,14 @@ k_i4_few(const Product p, const ListOf<KIND> list, const Few f) {
         for (int q = 0; q * threads < ITEMS; ++q) {
             const Item i = item(q);
             if (!i.live) continue;
-            const Needs n = q == 0 ? first : needs(i);
-            const int64_t to = n.to;
+            const int64_t to = q == 0 ? first : row_of(i);
             float sum = 0.0f, up = 0.0f;
 #pragma unroll 8
             for (int k = 0; k < f.kw; ++k) {
                 sum += mine[i.at + k * (V * 4)];
                 if constexpr (GATE) up += mine[i.up + k * (V * 4)];
             }
-            sum = scaled(sum, n.exp);
             if constexpr (GATE) {
-                up = scaled(up, n.up);
                 static_cast<uint16_t*>(p.out)[to * p.ldo + i.n / 32 * 16 + i.n % 16] = dev::f32_to_bf16_bits(gated(sum, up));
             } else if constexpr (KIND == kOut32) {
                 static_cast<float*>(p.out)[to * p.ldo + i.n] = sum;

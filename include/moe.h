@@ -501,7 +501,8 @@ int moe_i4_quantize(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x,
 /* Scratch bytes of moe_i4_matmul for up to max_T tokens, or a negative status. */
 int64_t moe_i4_workspace_bytes(int32_t max_T, int32_t N, int32_t K);
 /* y[t][n] = sum_k x[t][k] * weight[n][k] (async on s), products exact, sums in fp32, the result
- * rounded once where y is bf16.
+ * rounded once where y is bf16.  With few rows of x the sums are of x * code and of x, z times which is taken off: then
+ * a term counts as |x| * s * (code + z) in the sums' error.
  *   d_x: MOE_A_F32 or MOE_A_BF16, rows ld_x >= K elements apart, any alignment of the element (bf16 rows
  *     that start on 16 bytes each are read as they are, others are laid out in the workspace first; fp32
  *     numbers enter the matrix cores as three bf16 parts that add up to them);
