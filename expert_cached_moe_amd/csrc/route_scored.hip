@@ -9,8 +9,9 @@
 //
 // The choice has to be that of the formula wherever it is run, so scores, biased values and group
 // sums are 64-bit numbers: two experts closer than fp32's rounding of a score (2^-24) occur in every
-// chunk of a few thousand tokens; closer than 2^-53 does not happen.  Equal values choose the lower
-// id.  Gates are formed in 64 bits and rounded once.
+// chunk of a few thousand tokens, closer than 2^-51 only where scores are next to 1: sigmoids of 30 and more, which from
+// 53 ln 2 = 36.74 up are 1.  Equal values choose the lower id; which of two unequal ones closer than 2^-51 (1 + e^-z and its
+// reciprocal each 2^-53 off) comes first is left open.  Gates are formed in 64 bits and rounded once.
 //
 // W lanes take one token, 16 or, where few tokens are to be had, a wave; a lane holds consecutive
 // experts, and with groups a group has a power of two of lanes to itself.  64-bit work is the same

@@ -220,7 +220,8 @@ int moe_route(moe_ctx* ctx, const float* d_logits, int32_t T, int32_t* d_topk_id
  *   -infinity alone; renormalised softmax gates are the softmax of the chosen logits, however far these lie below
  *   the row's largest).
  * s, c and the groups' values are 64-bit numbers, so that the choice does not depend on fp32's
- * rounding of a score; gates are rounded once to fp32.  cfg.renormalize has no part in it.
+ * rounding of a score (equal ones: sigmoids of logits above 36.74 are all 1; the order of scores that differ by less than
+ * 2^-51 of their size is not specified); gates are rounded once to fp32.  cfg.renormalize has no part in it.
  *   d_logits [T][E] fp32; d_bias [E] fp32 or NULL; the rest as moe_route (d_ws: moe_workspace_bytes,
  *   needed for T > 16 and for T*k > 64).  Infinite negative logits and biases are taken (score 0; chosen last).
  *   NaNs and positive infinities: that token's ids are distinct and in range, their order and its

@@ -1,5 +1,7 @@
 """The router by scores and its gradient where scores leave the ordinary range: sigmoids near the end of
-64-bit numbers, chosen logits far below the row's largest."""
+64-bit numbers, chosen logits far below the row's largest, scores that 64 bits do not tell apart."""
+import decimal
+
 import numpy as np
 import pytest
 
@@ -78,3 +80,33 @@ def test_chosen_logits_far_below_the_largest(T, how):
     assert (np.abs(gates.sum(1) - 2.5) < 1e-12).all()
     assert (np.abs(w - gates) <= np.abs(gates) * (2.0 ** -24 + 2.0 ** -46) + 2.0 ** -149).all()
     r.check_gradient(logits, ids, dw)
+
+
+def sigmoid_exactly(z):
+    with decimal.localcontext(decimal.Context(prec=60)):
+        return 1 / (1 + (-decimal.Decimal(float(z))).exp())
+
+
+@pytest.mark.parametrize("T", [6, 40, 2107])
+def test_scores_that_64_bits_do_not_tell_apart(T):
+    """Sigmoids of 30 to 45: above 53 ln 2 = 36.74 they are 1 (e^-z < 2^-53, half a step of 1 + e^-z, which rounds to 1) and
+    the lower id comes first; below, the order is that of the exact scores but where these are as close as the 64-bit
+    ones' errors: 2^-53 from 1 + e^-z, 2^-53 from its reciprocal."""
+    E, k = 32, 12
+    rng = np.random.default_rng(T)
+    logits = rng.uniform(30, 45, (T, E)).astype(np.float32)
+    logits[T // 2:] = rng.uniform(30, 37.5, (T - T // 2, E)).astype(np.float32)
+    r = Router(E, k, T, "sigmoid", renorm=0)
+    r.forward(cuda(logits), cuda(np.zeros(E, np.float32)))
+    ids, _ = r.results()
+    near = decimal.Decimal(2) ** -51
+    for t in range(0, T, max(1, T // 40)):
+        full = [e for e in range(E) if logits[t, e] > 53 * np.log(2)]
+        n = min(len(full), k)
+        assert ids[t, :n].tolist() == full[:n]
+        assert len(set(ids[t].tolist())) == k
+        s = [sigmoid_exactly(z) for z in logits[t]]
+        left = set(range(E))
+        for j in range(k):
+            left.discard(int(ids[t, j]))
+            assert all(s[e] <= s[ids[t, j]] + near for e in left)
