@@ -26,7 +26,8 @@ struct Rows {
     int32_t shift;           // log2 of a group's length
 };
 
-// What a product computes and where its rows come from and go to.
+// What a product computes and where its rows come from and go to.  (h is rounded to bf16 once, as moe_expert_ffn's: what
+// the down product's matrix instructions take; with all its bits it would enter as three parts, three times the work.)
 enum {
     kOut16 = 0,   // dense: row r of x to row r of out, bf16
     kOut32 = 1,   // the same in fp32

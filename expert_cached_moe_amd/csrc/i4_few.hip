@@ -14,11 +14,15 @@
 //
 // The waves of a workgroup split K (by chunks of 512); sums meet once a
 // unit of rows, across the blocks in registers, across the waves in LDS, in a fixed order.  Every tile's
-// registers are loaded again as soon as it is used, with the next chunk or the next unit of rows, so
-// the stream does not stop between units.
+// registers are loaded again as soon as it is used, with the next chunk or the next unit of rows.  The stream still
+// stops once a pass: the loop's registers are copied at its back edge and behind it, so the compiler waits there until all
+// weights of the next pass have landed, before this unit's sums are reduced.  With K above 4096 there are several passes
+// (8 waves of 512), and x is read again in each pass of each unit, its loads under branches, with no weights in flight.
+// These waits bound the kernel, and where few workgroups have a row's passes to walk, their number.
 //
-// Measured (kernel): 2048 x 2048 at one token 4.4 us (launch, one trip to memory, the sums; its 2.2 MB take 0.4), 100003 x
-// 4096 at 4 tokens 47-49 (220 MB at 4.6 TB/s; 33 at the rate of a bare read), 7 experts of 4096 x 1536 at one token 19 and 9.5
+// Measured (kernel): 2048 x 2048 at one token 4.0-4.6 us (launch, one trip to memory, the sums; its 2.2 MB take 0.4), 100003 x
+// 4096 at 4 tokens 48-50 (220 MB at 4.5 TB/s; 33 at the rate of a bare read), at 8 tokens 71, at 4 fp32 tokens 71; 32768 x 12288
+// at one token 46, at 4 tokens 58 (214 MB: 32 at the rate of a bare read); 7 experts of 4096 x 1536 at one token 19 and 9.9
 // (50 and 25 MB).  Twice the rows a wave (more bytes in flight, fewer waves) 3% slower, half of them 14-30%.
 //
 // Experts: each workgroup lists the entries that have rows, from the offsets, in blocks of 4 rows at most, and walks their

@@ -12,8 +12,10 @@
 // words one in four bytes.  A lane turns 16 codes of a weight row, one group, into two fragments of exact bf16
 // weights, once for all rows of x.  Sums of the waves meet in LDS at the end, in a fixed order.
 //
-// Measured (bf16 x): 4096 x 4096 at 32 rows 8.9 us, at 128 11.7, at 512 29; 77 fp32 rows of 1568 to 1037 10.5 (75 walks of a slice
-// over three parts of x).  What bounds them is the time of a slice with its wait and decoding, 0.9-1.5 us, not the matrix unit.
+// Measured (bf16 x): 4096 x 4096 at 32 rows 8.4 us, at 128 11.2, at 512 27; 4096 x 12288 at 256 rows 50; 77 fp32 rows of 1568 to 1037
+// 10.4 (75 walks of a slice: the codes are read and decoded once for each of the three parts of x).  What bounds them is the
+// time of a slice with its wait and decoding, 0.9-1.5 us, not the matrix unit: a wave has 32 rows of the weights, so each fragment of
+// x feeds two matrix instructions only; and K is not split over workgroups, so that with fewer tiles than CUs some are idle.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -305,8 +307,9 @@ k_i4_mid(const Product p, const ListOf<KIND> list, const int4* __restrict__ map,
 // The same with whole lines of codes in registers: a wave's 32 rows by blocks of 128 k, 16 bytes a lane and 16 rows, so
 // that the 32 codes of a lane share a group, D blocks ahead; x alone goes through LDS, in D + 1 stages.  Half the
 // waits, words and addresses for a code: for products whose time is the decoding, many rows of weights or many experts.
-// Measured: 100003 x 4096 at 32 rows 71 us, at 64 94, at 128 154; 128 experts of 2048 x 768, top 8, at 16 tokens 36 and 21 (166 MB at
-// 2.9 TB/s), at 64 tokens 79 in all, at 2,048 299.
+// Measured: 100003 x 4096 at 32 rows 71 us, at 64 92, at 128 147 (two workgroups read 256 KB of LDS a block, 2,048 cycles, as many as
+// their matrix instructions take, and the decoding comes on top); 128 experts of 2048 x 768, top 8, at 16 tokens 36 and 21 (166 MB at
+// 2.9 TB/s), at 64 tokens 86 in all, at 256 94, at 2,048 291.
 template <int MF_, int D_>
 struct Wide {
     static constexpr int MF = MF_, WK = 1, WN = 4, D = D_;

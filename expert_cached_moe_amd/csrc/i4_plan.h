@@ -8,15 +8,15 @@
 namespace moe {
 namespace i4 {
 
-// Up to 8 rows of x, and by expert up to 8 tokens: the few-row kernel (100003 x 4096 at 8 tokens 77-82 us against 93 on tiles of 32 rows, 4096 x 4096
-// 7.8 against 8.8; at 16 tokens, in two blocks of 8, 12.8 against 8.9).  By expert too: 128 of 2048 x 768, top 8, at 8
-// tokens 43 us against 49 on tiles, at 16 tokens 68 against 61; 256 of 4096 x 1536 and the shared one, top 6, 106
-// against 123 and 173 against 168.
+// Up to 8 rows of x, and by expert up to 8 tokens: the few-row kernel (8 tokens: 4096 x 4096 7.5 us against 8.3 on tiles of 32
+// rows, 12288 x 4096 13.2 against 25, 32768 x 4096 27 against 26, 100003 x 4096 71 against 65; 4 tokens there 48 against 65; 4096 x
+// 4096 at 16 tokens, in two blocks of 8, 12.2 against 8.3).  By expert too: 128 of 2048 x 768, top 8, at 8 tokens 42 us against 46
+// on tiles, at 16 tokens 68 against 61; 256 of 4096 x 1536 and the shared one, top 6, 113-118 against 132 and 173 against 168.
 constexpr int kFewTokens = 8;
 // Dense products of more rows too, where blocks of 8 rows by 16 of the weights leave a CU one workgroup at most and rows
-// are long: the tiles' waves split K no further than the few-row kernel's, and wait for each slice (16 x 2048 x 12288 13.3 us
-// against 21.5, in fp32 parts 32 x 1024 x 12288 31 and 49, 128 x 256 x 8192 9.6 and 12.9; 32 x 1024 x 1024 4.6 both; two
-// workgroups a CU, 64 x 1024 x 8192: 17.1 against 13.2).
+// are long: the tiles' waves split K no further than the few-row kernel's, and wait for each slice (16 x 2048 x 12288 13.4 us
+// against 17.0, in fp32 parts 32 x 1024 x 12288 29 and 46, 128 x 256 x 8192 10.5 and 12.5; 32 x 1024 x 1024 4.3 both; two
+// workgroups a CU, 64 x 1024 x 8192: 17.7 against 12.7).
 inline bool few_dense(int64_t T, int64_t N, int64_t K, int n_cu) {
     return T <= kFewTokens || (K > 1024 && (N + 15) / 16 * ((T + kFewTokens - 1) / kFewTokens) <= n_cu);
 }
@@ -25,12 +25,13 @@ inline bool few_dense(int64_t T, int64_t N, int64_t K, int n_cu) {
 // up to `slots` workgroups a CU.  A slice of 64 k takes `one` us with one workgroup on each CU and `more` for each further
 // one; 256 x 256 tiles take `one` and, with more of them than CUs, `more` on top: a chip at its power limit.  `tile` us are
 // for the start and the results.
-// Measured on bf16 x (dense, whole kernel): 4096 x 4096 at 32 rows 8.6 us on 32 x 32 tiles (17 on 128 x 32 and 64 x 64),
-// at 128 11.1 on 64 x 32 (17.3 on 128 x 32), at 512 28 on 128 x 64 (34 on 128 x 32, 102 on 256 x 256); 4096 x 12288 at 256
-// rows 48 on 128 x 32 (77 on 128 x 64); 16384 x 4096 at 1024 rows 121 on 256 x 256 (180 on 128 x 128); 100003 x 4096 at 32
-// rows 71 on 32 x 128 (98 on 64 x 128, 111 on 32 x 32), at 64 105 on 64 x 128 (140), at 128 161 on 128 x 128 (190), at 256
-// 245 on 256 x 256 (309).  By expert (as above): at 64 tokens 80 on 32 x 128 (104 on 64 x 128), at 2,048 299 on 64 x 128
-// (341 on 32 x 128, 369 on 256 x 256), at 4,096 493 on 256 x 256 (519 on 128 x 128, 976 on 64 x 64).
+// Measured on bf16 x (replays of a graph over weights used in turn): 4096 x 4096 at 32 rows 8.4 us on 32 x 32 tiles (17 on 128 x
+// 32 and 64 x 64), at 128 11.2 on 64 x 32 (17.3 on 128 x 32), at 512 27 on 128 x 64 (34 on 128 x 32, 102 on 256 x 256); 4096 x
+// 12288 at 256 rows 50 on 128 x 32 (86 on 128 x 64); 16384 x 4096 at 1024 rows 118 on 256 x 256 (151 on 128 x 128); 100003 x 4096
+// at 32 rows 71 on 32 x 128 (88 on 64 x 128, 108 on 32 x 32), at 64 92 on 64 x 128 (112 on 32 x 128), at 128 147 on 128 x 128 (153
+// on 64 x 128), at 256 224 on 256 x 256 (259 on 128 x 128).  By expert (as above): at 64 tokens 86 on 32 x 128 (114 on 64 x 128), at
+// 1,024 180 on 64 x 128 (201 on 32 x 128, 253 on 256 x 256), at 2,048 291 on 64 x 128 (339 on 32 x 128, but 275 on 256 x 256), at 4,096
+// 446 on 256 x 256 (499 on 128 x 128, 1008 on 64 x 64).
 struct Kind {
     int rows, cols, split, slots;
     double one, more, tile;

@@ -6,8 +6,10 @@
 // scale s is t / S as an e4m3 number, rounded to nearest even, or up where there are zero points: then
 // the span is at most 15 steps (to nearest it could be 15.9 and lose a whole step); without them the
 // largest magnitude lies below 7.5 steps either way (e4m3 numbers are at most 1/17 off).  Quotients are
-// formed in 64 bits and rounded half to even.  Done once for a model's weights: 8192 x 4096 bf16 weights 87 us,
-// 100003 x 4096 1060 (0.8 TB/s read in effect), bound by the 64-bit divisions; activations of 77 x 1568 fp32 numbers 3.
+// formed in 64 bits and rounded half to even.  Done once for a model's weights: 8192 x 4096 bf16 weights 86 us,
+// 100003 x 4096 950-1090 (0.8 TB/s read in effect; 17 and 200 at a copy's rate).  Bound by its loads: the numbers of a piece are
+// read under branches of their own, two at most by one load, each waited for before the next, and rows shorter than 8192 leave
+// threads idle.  The 64-bit divisions are some 17 us of the 86 (20 operations each).  Activations of 77 x 1568 fp32 numbers 3.
 #include <hip/hip_runtime.h>
 
 #include "i4_common.h"

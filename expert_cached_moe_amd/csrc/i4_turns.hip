@@ -4,13 +4,14 @@
 // of half a slice of K (32 of them, 512 cycles of the matrix unit), the other reads its fragments of the
 // next half from LDS; a barrier ends each turn.  A slice is 64 of K, 32 KiB of either operand, in a ring of
 // five places that is all of the LDS.  x comes straight into its place by loads into LDS; the weights
-// come as codes, 16 bytes a thread and slice, requested four slices ahead, and become exact bf16 weights in the
-// reading turns: 32 codes of one group a thread, 16 in each turn, 38 vector operations and two 16-byte
+// come as codes, 16 bytes a thread and slice, requested two slices before they are decoded and four before they are
+// multiplied (the wait for those of an even slice is one for all loads, so also for the odd slice's behind them,
+// requested a turn earlier), and become exact bf16 weights in the reading turns: 32 codes of one group a thread, 16 in each turn, 38 vector operations and two 16-byte
 // LDS writes, beside 12 fragment reads.  A turn's LDS traffic, 48 KiB read and 8 written by a group,
 // takes 448 of its 512 cycles.  So the codes are decoded once a tile, the weights never pass through
 // memory, and the matrix units are fed as by a product of bf16 weights.
 //
-// Measured: 8,192 x 4096 x 8192 435-452 us (1.22-1.26 PFLOP/s; 380 at the rate of a library product of 8192^3); a slice takes
+// Measured: 8,192 x 4096 x 8192 435-466 us (1.18-1.26 PFLOP/s; 380 at the rate of a library product of 8192^3); a slice takes
 // 1.6 us with few tiles and 1.8-1.9 with every CU busy, a tile 8-10 besides for its start and its results.  128 experts of
 // 2048 x 768, top 8, 8,192 tokens 503 and 317: of the tiles of experts with 512 rows on average a fifth is empty, and the 12
 // slices of the down product are 22 of a tile's 32 us.

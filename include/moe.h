@@ -499,7 +499,8 @@ int moe_i8_ffn(moe_ctx* ctx, const void* d_x, int32_t T, const void* d_blob8, vo
  * Errors: MOE_EINVAL (null, type, group, ld_x < cols, alignment), MOE_ESHAPE (cols, rows). */
 int moe_i4_quantize(moe_ctx* ctx, const void* d_x, int32_t x_type, int64_t ld_x, int32_t rows, int32_t cols, int32_t group,
                     int32_t zero_points, uint8_t* d_q, uint16_t* d_words, uint8_t* d_exps, hipStream_t s);
-/* Scratch bytes of moe_i4_matmul for up to max_T tokens, or a negative status. */
+/* Scratch bytes of moe_i4_matmul for up to max_T tokens, or a negative status: 6 for each number of x, what fp32 rows
+ * take (bf16 rows that are laid out take 2, those that are read as they are none). */
 int64_t moe_i4_workspace_bytes(int32_t max_T, int32_t N, int32_t K);
 /* y[t][n] = sum_k x[t][k] * weight[n][k] (async on s), products exact, sums in fp32, the result
  * rounded once where y is bf16.  With few rows of x the sums are of x * code and of x, z times which is taken off: then
